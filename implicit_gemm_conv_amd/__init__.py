@@ -19,6 +19,8 @@ IGC_OK, IGC_ERR_INVALID_VALUE, IGC_ERR_MISALIGNED, IGC_ERR_UNSUPPORTED, IGC_ERR_
 ROW_MAJOR, COL_MAJOR = 0, 1
 OUT_F32, OUT_BF16, OUT_F16 = 0, 1, 2
 OUT_CODES = {"f32": OUT_F32, "bf16": OUT_BF16, "f16": OUT_F16}
+ACT_NONE, ACT_RELU, ACT_GELU, ACT_GELU_TANH, ACT_SILU = range(5)
+ACT_CODES = {"none": ACT_NONE, "relu": ACT_RELU, "gelu": ACT_GELU, "gelu_tanh": ACT_GELU_TANH, "silu": ACT_SILU}
 OP_GEMM, OP_CONV_FPROP, OP_CONV_DGRAD, OP_CONV_WGRAD = range(4)
 
 # Every exported entry point (include/igc.h), for the load check.
@@ -30,6 +32,15 @@ EXPORTS = (
     "conv2d_nhwc_dgrad_implicit_gemm_fp16_ex",
     "conv2d_nhwc_wgrad_implicit_gemm", "conv2d_nhwc_wgrad_implicit_gemm_fp16", "conv2d_nhwc_wgrad_implicit_gemm_ex",
     "conv2d_nhwc_wgrad_implicit_gemm_fp16_ex",
+    "gemm_bf16_epilogue", "gemm_fp16_epilogue", "gemm_bf16_epilogue_ex", "gemm_fp16_epilogue_ex",
+    "conv2d_nhwc_implicit_gemm_epilogue", "conv2d_nhwc_implicit_gemm_epilogue_fp16",
+    "conv2d_nhwc_implicit_gemm_epilogue_ex", "conv2d_nhwc_implicit_gemm_epilogue_fp16_ex",
+    "igc_epilogue_workspace_bytes",
+    "epilogue_backward_bf16", "epilogue_backward_fp16", "epilogue_backward_bf16_ex", "epilogue_backward_fp16_ex",
+    "igc_epilogue_backward_workspace_bytes",
+    "group_norm_nhwc_bf16", "group_norm_nhwc_fp16", "group_norm_nhwc_bf16_ex", "group_norm_nhwc_fp16_ex",
+    "group_norm_nhwc_backward_bf16", "group_norm_nhwc_backward_fp16", "group_norm_nhwc_backward_bf16_ex",
+    "group_norm_nhwc_backward_fp16_ex", "igc_group_norm_workspace_bytes",
     "igc_workspace_bytes", "igc_tune_supported", "igc_default_tune", "igc_tune_count", "igc_tune_get",
     "igc_tune_scope", "igc_tune_lds_bytes", "igc_status_string", "igc_take_device_error", "igc_debug_stream_k",
     "igc_pool_allocations", "igc_ring_schedule", "igc_lds_chunk", "igc_stage_slot",
@@ -62,6 +73,60 @@ def tune(cfg, k_splits=0, stream_k=0, sk_hybrid=0):
     return Tune(*cfg[:8], k_splits, stream_k, ring_sync, sk_hybrid)
 
 
+class CEpilogue(ctypes.Structure):
+    """igc_epilogue_t."""
+    _fields_ = [("act", ctypes.c_int), ("backward", ctypes.c_int), ("bias", ctypes.c_void_p),
+                ("bias_type", ctypes.c_int), ("residual", ctypes.c_void_p), ("ldr", ctypes.c_int64),
+                ("residual_type", ctypes.c_int), ("pre", ctypes.c_void_p), ("ldp", ctypes.c_int64),
+                ("pre_type", ctypes.c_int)]
+
+
+def act_code(act):
+    """The code of an activation given by name ("none", "relu", "gelu", "gelu_tanh", "silu") or by code."""
+    return ACT_CODES[act] if isinstance(act, str) else int(act)
+
+
+_DTYPE_CODES = {"torch.float32": OUT_F32, "torch.bfloat16": OUT_BF16, "torch.float16": OUT_F16}
+
+
+def out_code(dtype):
+    """The OUT_ code of a torch dtype."""
+    try:
+        return _DTYPE_CODES[str(dtype)]
+    except KeyError:
+        raise TypeError(f"{dtype}: float32, bfloat16 or float16 wanted") from None
+
+
+class Epilogue:
+    """A fused epilogue (igc_epilogue_t) from tensors: types come from their dtypes, the leading dimensions of
+    `residual` and `pre` from their first stride unless given, and the tensors are kept alive with it.  A raw
+    device address needs its type (bias_type, residual_type, pre_type: an OUT_ code) and leading dimension."""
+    __slots__ = ("c", "_keep")
+
+    def __init__(self, act="none", bias=None, residual=None, pre=None, backward=False, ldr=None, ldp=None,
+                 bias_type=None, residual_type=None, pre_type=None):
+        c = self.c = CEpilogue()
+        self._keep = (bias, residual, pre)
+        c.act, c.backward = act_code(act), int(backward)
+        if bias is not None:
+            c.bias, c.bias_type, _ = self._tensor(bias, bias_type, 0, 1)
+        if residual is not None:
+            c.residual, c.residual_type, c.ldr = self._tensor(residual, residual_type, ldr, 2)
+        if pre is not None:
+            c.pre, c.pre_type, c.ldp = self._tensor(pre, pre_type, ldp, 2)
+
+    @staticmethod
+    def _tensor(x, code, ld, dims):
+        if not hasattr(x, "data_ptr"):
+            if code is None or ld is None:
+                raise TypeError("a raw address needs its type and leading dimension")
+            return int(x), code, ld
+        if x.dim() >= 1 and x.shape[-1] > 1 and x.stride(-1) != 1:
+            raise ValueError("values of a row must lie together")
+        return (x.data_ptr(), out_code(x.dtype) if code is None else code,
+                ld if ld is not None else (x.stride(0) if x.dim() == dims else 0))
+
+
 _lib = None
 
 
@@ -90,6 +155,28 @@ def lib():
             protos[base + "_fp16"] = conv + [p]
             protos[base + "_ex"] = conv + [tp, p, i64, p]
             protos[base + "_fp16_ex"] = conv + [tp, p, i64, p]
+        ep, f32 = ctypes.POINTER(CEpilogue), ctypes.c_float
+        for base in ("gemm_bf16_epilogue", "gemm_fp16_epilogue"):
+            protos[base] = gemm + [ep, p]
+            protos[base + "_ex"] = gemm + [ep, tp, p, i64, p]
+        for base in ("conv2d_nhwc_implicit_gemm_epilogue", "conv2d_nhwc_implicit_gemm_epilogue_fp16"):
+            protos[base] = conv + [ep, p]
+            protos[base + "_ex"] = conv + [ep, tp, p, i64, p]
+        for t in ("bf16", "fp16"):
+            back = [i64, i64, i32, p, i64, p, i64, p, i64, p, i32]
+            protos["epilogue_backward_" + t] = back + [p]
+            protos["epilogue_backward_" + t + "_ex"] = back + [p, i64, p]
+            norm = [i32] * 5 + [p, i64, p, p, i32, f32, i32, p, i64, p, p]
+            protos["group_norm_nhwc_" + t] = norm + [p]
+            protos["group_norm_nhwc_" + t + "_ex"] = norm + [p, i64, p]
+            grad = [i32] * 5 + [p, i64, p, p, i32, p, p, i32, p, i64, p, i64, p, p]
+            protos["group_norm_nhwc_backward_" + t] = grad + [p]
+            protos["group_norm_nhwc_backward_" + t + "_ex"] = grad + [p, i64, p]
+        for name, args, res in (("igc_epilogue_workspace_bytes", [i32, i64, i64, i64, tp], i64),
+                                ("igc_epilogue_backward_workspace_bytes", [i64, i64], i64),
+                                ("igc_group_norm_workspace_bytes", [i32] * 5, i64)):
+            getattr(L, name).argtypes = args
+            getattr(L, name).restype = res
         for name, args in protos.items():
             fn = getattr(L, name)
             fn.argtypes = args
@@ -222,6 +309,114 @@ conv2d_nhwc_wgrad_implicit_gemm_ex = _conv_ex("conv2d_nhwc_wgrad_implicit_gemm_e
 conv2d_nhwc_wgrad_implicit_gemm_fp16_ex = _conv_ex("conv2d_nhwc_wgrad_implicit_gemm_fp16_ex")
 
 
+def _epi(e):
+    if e is None:
+        return None
+    return ctypes.byref(e.c if isinstance(e, Epilogue) else e)
+
+
+def _gemm_epilogue(name):
+    def call(M, N, K, A, lda, la, B, ldb, lb, D, ldd, d_type, epilogue, stream=None):
+        return getattr(lib(), name)(M, N, K, _ptr(A), lda, la, _ptr(B), ldb, lb, _ptr(D), ldd, d_type, _epi(epilogue),
+                                    _stream(stream))
+
+    def call_ex(M, N, K, A, lda, la, B, ldb, lb, D, ldd, d_type, epilogue, tune=None, workspace=None,
+                workspace_bytes=None, stream=None):
+        wsb = workspace_bytes if workspace_bytes is not None else _nbytes(workspace)
+        return getattr(lib(), name + "_ex")(M, N, K, _ptr(A), lda, la, _ptr(B), ldb, lb, _ptr(D), ldd, d_type,
+                                            _epi(epilogue), _tune(tune), _ptr(workspace), wsb, _stream(stream))
+    call.__name__, call_ex.__name__ = name, name + "_ex"
+    return call, call_ex
+
+
+def _conv_epilogue(name):
+    def call(N, H, W, C, K, R, S, stride_h, stride_w, pad_h, pad_w, dil_h, dil_w, x, w, y, y_type, epilogue,
+             stream=None):
+        return getattr(lib(), name)(N, H, W, C, K, R, S, stride_h, stride_w, pad_h, pad_w, dil_h, dil_w, _ptr(x),
+                                    _ptr(w), _ptr(y), y_type, _epi(epilogue), _stream(stream))
+
+    def call_ex(N, H, W, C, K, R, S, stride_h, stride_w, pad_h, pad_w, dil_h, dil_w, x, w, y, y_type, epilogue,
+                tune=None, workspace=None, workspace_bytes=None, stream=None):
+        wsb = workspace_bytes if workspace_bytes is not None else _nbytes(workspace)
+        return getattr(lib(), name + "_ex")(N, H, W, C, K, R, S, stride_h, stride_w, pad_h, pad_w, dil_h, dil_w,
+                                            _ptr(x), _ptr(w), _ptr(y), y_type, _epi(epilogue), _tune(tune),
+                                            _ptr(workspace), wsb, _stream(stream))
+    call.__name__, call_ex.__name__ = name, name + "_ex"
+    return call, call_ex
+
+
+def _epilogue_backward(name):
+    def call(M, N, act, dD, ldd, pre, ldp, dz, ldz, dbias, dbias_type, stream=None):
+        return getattr(lib(), name)(M, N, act_code(act), _ptr(dD), ldd, _ptr(pre), ldp, _ptr(dz), ldz, _ptr(dbias),
+                                    dbias_type, _stream(stream))
+
+    def call_ex(M, N, act, dD, ldd, pre, ldp, dz, ldz, dbias, dbias_type, workspace=None, workspace_bytes=None,
+                stream=None):
+        wsb = workspace_bytes if workspace_bytes is not None else _nbytes(workspace)
+        return getattr(lib(), name + "_ex")(M, N, act_code(act), _ptr(dD), ldd, _ptr(pre), ldp, _ptr(dz), ldz,
+                                            _ptr(dbias), dbias_type, _ptr(workspace), wsb, _stream(stream))
+    call.__name__, call_ex.__name__ = name, name + "_ex"
+    return call, call_ex
+
+
+def _group_norm(name):
+    def call(N, H, W, C, G, x, ldx, gamma, beta, param_type, eps, act, y, ldy, mean=None, rstd=None, stream=None):
+        return getattr(lib(), name)(N, H, W, C, G, _ptr(x), ldx, _ptr(gamma), _ptr(beta), param_type, eps,
+                                    act_code(act), _ptr(y), ldy, _ptr(mean), _ptr(rstd), _stream(stream))
+
+    def call_ex(N, H, W, C, G, x, ldx, gamma, beta, param_type, eps, act, y, ldy, mean=None, rstd=None,
+                workspace=None, workspace_bytes=None, stream=None):
+        wsb = workspace_bytes if workspace_bytes is not None else _nbytes(workspace)
+        return getattr(lib(), name + "_ex")(N, H, W, C, G, _ptr(x), ldx, _ptr(gamma), _ptr(beta), param_type, eps,
+                                            act_code(act), _ptr(y), ldy, _ptr(mean), _ptr(rstd), _ptr(workspace), wsb,
+                                            _stream(stream))
+    call.__name__, call_ex.__name__ = name, name + "_ex"
+    return call, call_ex
+
+
+def _group_norm_backward(name):
+    def call(N, H, W, C, G, x, ldx, gamma, beta, param_type, mean, rstd, act, dy, lddy, dx, lddx, dgamma=None,
+             dbeta=None, stream=None):
+        return getattr(lib(), name)(N, H, W, C, G, _ptr(x), ldx, _ptr(gamma), _ptr(beta), param_type, _ptr(mean),
+                                    _ptr(rstd), act_code(act), _ptr(dy), lddy, _ptr(dx), lddx, _ptr(dgamma),
+                                    _ptr(dbeta), _stream(stream))
+
+    def call_ex(N, H, W, C, G, x, ldx, gamma, beta, param_type, mean, rstd, act, dy, lddy, dx, lddx, dgamma=None,
+                dbeta=None, workspace=None, workspace_bytes=None, stream=None):
+        wsb = workspace_bytes if workspace_bytes is not None else _nbytes(workspace)
+        return getattr(lib(), name + "_ex")(N, H, W, C, G, _ptr(x), ldx, _ptr(gamma), _ptr(beta), param_type,
+                                            _ptr(mean), _ptr(rstd), act_code(act), _ptr(dy), lddy, _ptr(dx), lddx,
+                                            _ptr(dgamma), _ptr(dbeta), _ptr(workspace), wsb, _stream(stream))
+    call.__name__, call_ex.__name__ = name, name + "_ex"
+    return call, call_ex
+
+
+gemm_bf16_epilogue, gemm_bf16_epilogue_ex = _gemm_epilogue("gemm_bf16_epilogue")
+gemm_fp16_epilogue, gemm_fp16_epilogue_ex = _gemm_epilogue("gemm_fp16_epilogue")
+conv2d_nhwc_implicit_gemm_epilogue, conv2d_nhwc_implicit_gemm_epilogue_ex = \
+    _conv_epilogue("conv2d_nhwc_implicit_gemm_epilogue")
+conv2d_nhwc_implicit_gemm_epilogue_fp16, conv2d_nhwc_implicit_gemm_epilogue_fp16_ex = \
+    _conv_epilogue("conv2d_nhwc_implicit_gemm_epilogue_fp16")
+epilogue_backward_bf16, epilogue_backward_bf16_ex = _epilogue_backward("epilogue_backward_bf16")
+epilogue_backward_fp16, epilogue_backward_fp16_ex = _epilogue_backward("epilogue_backward_fp16")
+group_norm_nhwc_bf16, group_norm_nhwc_bf16_ex = _group_norm("group_norm_nhwc_bf16")
+group_norm_nhwc_fp16, group_norm_nhwc_fp16_ex = _group_norm("group_norm_nhwc_fp16")
+group_norm_nhwc_backward_bf16, group_norm_nhwc_backward_bf16_ex = _group_norm_backward("group_norm_nhwc_backward_bf16")
+group_norm_nhwc_backward_fp16, group_norm_nhwc_backward_fp16_ex = _group_norm_backward("group_norm_nhwc_backward_fp16")
+
+
+def igc_epilogue_workspace_bytes(op, M, N, K, tune=None):
+    return lib().igc_epilogue_workspace_bytes(op, M, N, K, _tune(tune))
+
+
+def igc_epilogue_backward_workspace_bytes(M, N):
+    return lib().igc_epilogue_backward_workspace_bytes(M, N)
+
+
+def igc_group_norm_workspace_bytes(N, H, W, C, G):
+    return lib().igc_group_norm_workspace_bytes(N, H, W, C, G)
+
+
 def conv_out_hw(H, W, R, S, sh=1, sw=1, ph=0, pw=0, dh=1, dw=1):
     """Output size (P, Q) of the forward convolution."""
     return (H + 2 * ph - dh * (R - 1) - 1) // sh + 1, (W + 2 * pw - dw * (S - 1) - 1) // sw + 1
@@ -262,7 +457,7 @@ def igc_tune_get(i):
     return t if lib().igc_tune_get(i, ctypes.byref(t)) else None
 
 
-SCOPE_ALL, SCOPE_STREAM_K, SCOPE_CONV_FPROP = 1, 2, 4
+SCOPE_ALL, SCOPE_STREAM_K, SCOPE_CONV_FPROP, SCOPE_EPILOGUE = 1, 2, 4, 8
 
 
 def igc_tune_scope(i):
@@ -276,7 +471,7 @@ def igc_tune_lds_bytes(t):
 def tunes(scope=0):
     """Compiled (bm, bn, bk, pipe_depth, waves, mfma, half_stage, loader_waves, ring_sync) configurations whose
     scope includes every bit of `scope` (SCOPE_ALL: every type, layout and operation; SCOPE_STREAM_K;
-    SCOPE_CONV_FPROP: the complete forward convolution)."""
+    SCOPE_CONV_FPROP: the complete forward convolution; SCOPE_EPILOGUE: the fused epilogue)."""
     return [igc_tune_get(i).astuple() for i in range(igc_tune_count()) if igc_tune_scope(i) & scope == scope]
 
 

@@ -8,8 +8,10 @@ csrc/instances.hip as one object per operation family (bf16 GEMM, fp16 GEMM,
 forward convolution, data gradient, filter gradient; study-only
 configurations build the bf16 and fp16 GEMM and the bf16 forward convolution,
 forward-convolution configurations the study GEMMs and the complete forward
-convolution), all in parallel, then linked with the host-side C ABI (csrc/igc_lib.hip,
-csrc/registry.hip) and the split-K reduction (csrc/split_reduce.hip).
+convolution), and from csrc/epilogue_instances.hip as one object per family for the
+configurations that also have a fused epilogue, all in parallel, then linked with the host-side C ABI
+(csrc/igc_lib.hip, csrc/registry.hip), the split-K reduction (csrc/split_reduce.hip), the product of a few rows
+(csrc/few_rows.hip), the epilogue's gradient (csrc/epilogue_backward.hip) and group norm (csrc/group_norm.hip).
 """
 import concurrent.futures
 import os
@@ -75,6 +77,15 @@ def instance_units(configs=None):
                           f"-DIGC_FULL={fam_full}", f"-DIGC_SK={sk}", f"-DIGC_FAMILY={fam}", "-c",
                           os.path.join(CSRC, "instances.hip"),
                           "-o", obj])
+        if (scope >> 3) & 1:  # the kernels with the fused epilogue
+            for fam in ((0, 1, 2) if full else (2,)):
+                obj = os.path.join(OBJ_DIR, f"epi_{bm}x{bn}x{bk}x{d}x{w}x{mi}x{h}x{lw}x{sy}_f{fam}.o")
+                units.append([HIPCC, *FLAGS, f"-DIGC_BM={bm}", f"-DIGC_BN={bn}", f"-DIGC_BK={bk}", f"-DIGC_D={d}",
+                              f"-DIGC_W={w}", f"-DIGC_MI={mi}", f"-DIGC_HALF={h}", f"-DIGC_LW={lw}",
+                              f"-DIGC_SYNC={sy}", f"-DIGC_FAMILY={fam}", "-c",
+                              os.path.join(CSRC, "epilogue_instances.hip"), "-o", obj])
+    # the epilogue units with every operand layout take longest: first, so that none is left at the end
+    units.sort(key=lambda u: "epi_256x256" not in u[-1])
     return units
 
 
@@ -84,7 +95,8 @@ def host_unit(name):
 
 def build(jobs=None, verbose=False):
     os.makedirs(OBJ_DIR, exist_ok=True)
-    units = instance_units() + [host_unit(n) for n in ("igc_lib", "registry", "split_reduce", "probes")]
+    units = instance_units() + [host_unit(n) for n in ("group_norm", "few_rows", "epilogue_backward", "igc_lib",
+                                                 "registry", "split_reduce", "probes")]
     # longest first: the instance objects dominate
     jobs = jobs or min(len(units), max(1, (os.cpu_count() or 4)))
     with concurrent.futures.ThreadPoolExecutor(jobs) as ex:

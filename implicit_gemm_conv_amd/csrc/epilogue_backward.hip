@@ -1,0 +1,226 @@
+// epilogue_backward.hip -- the gradient of the products' epilogue:
+//   dz[m][n] = dD[m][n] * act'(pre[m][n]),   dbias[n] = sum_m dz[m][n]
+// One pass over dD and pre.  Bound by memory: 6 bytes a value with dz, 4
+// without.  A thread keeps eight columns and walks down the rows, so every
+// access is a 16-byte piece of a row and the column sums (in fp32, of the
+// unrounded dz) stay in registers; a workgroup's row lanes join through LDS,
+// and the row chunks' partial sums are added in order by a second kernel, so
+// the result does not depend on timing.
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "epilogue.hpp"
+#include "host.hpp"
+
+namespace igc {
+
+struct BackArgs {
+    const void* d;    // dD
+    const void* pre;  // nullptr: act' = 1
+    void* dz;         // nullptr: not wanted
+    void* dbias;      // nullptr: not wanted
+    float* part;      // chunks x N partial column sums
+    int64_t M, N, ldd, ldp, ldz, rows_per;
+    int cl_shift;     // log2 of the workgroup's column lanes
+    int col_blocks, chunks, act, bias_kind;
+};
+
+constexpr int kBackThreads = 256;
+
+template <bool FP16>
+__global__ __launch_bounds__(kBackThreads) void epilogue_backward_kernel(const BackArgs a) {
+    __shared__ float red[kBackThreads * 8];
+    const int cl = 1 << a.cl_shift, row_lanes = kBackThreads >> a.cl_shift;
+    const int cb = (int)blockIdx.x % a.col_blocks, chunk = (int)blockIdx.x / a.col_blocks;
+    const int c = (int)threadIdx.x & (cl - 1), rl = (int)threadIdx.x >> a.cl_shift;
+    const int64_t n = ((int64_t)cb * cl + c) * 8;
+    const int left = a.N - n >= 8 ? 8 : (int)(a.N - n);
+    const int64_t m0 = (int64_t)chunk * a.rows_per, m1 = m0 + a.rows_per < a.M ? m0 + a.rows_per : a.M;
+    float sum[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+    if (left > 0) {
+        with_act(a.pre ? a.act : (int)ACT_NONE, [&](auto A) __attribute__((always_inline)) {
+            constexpr int ACT = decltype(A)::value;
+            constexpr int U = 4;  // rows in flight
+            for (int64_t m = m0 + rl; m < m1; m += U * row_lanes) {
+                u32x4s_t d[U], p[U];
+#pragma unroll
+                for (int u = 0; u < U; ++u) {
+                    const int64_t mu = m + u * row_lanes;
+                    d[u] = u32x4s_t{0, 0, 0, 0};
+                    p[u] = u32x4s_t{0, 0, 0, 0};
+                    if (mu < m1) {
+                        d[u] = raw8(a.d, mu * a.ldd + n);
+                        if constexpr (ACT != ACT_NONE) p[u] = raw8(a.pre, mu * a.ldp + n);
+                    }
+                }
+#pragma unroll
+                for (int u = 0; u < U; ++u) {
+                    const int64_t mu = m + u * row_lanes;
+                    if (mu >= m1) break;
+                    float v[8];
+                    unpack8<FP16>(d[u], v);
+                    if constexpr (ACT != ACT_NONE) {
+                        float z[8];
+                        unpack8<FP16>(p[u], z);
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) v[i] *= act_grad_of<ACT>(z[i]);
+                    }
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) sum[i] += v[i];
+                    if (a.dz) store8(a.dz, mu * a.ldz + n, FP16 ? KIND_F16 : KIND_BF16, left, true, v);
+                }
+            }
+        });
+    }
+    if (!a.dbias) return;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) red[(rl * cl + c) * 8 + i] = sum[i];
+    __syncthreads();
+    for (int x = (int)threadIdx.x; x < cl * 8; x += kBackThreads) {
+        const int64_t col = (int64_t)cb * cl * 8 + x;
+        if (col >= a.N) break;
+        float s = 0.0f;
+        for (int r = 0; r < row_lanes; ++r) s += red[r * cl * 8 + x];
+        if (a.chunks > 1)
+            a.part[(int64_t)chunk * a.N + col] = s;
+        else
+            store_kind(a.dbias, col, a.bias_kind, s);
+    }
+}
+
+// dbias = the chunks' partial sums: 32 columns by 8 chunk lanes a workgroup.
+__global__ __launch_bounds__(256) void column_sum_kernel(const float* part, int64_t N, int chunks, void* out, int kind) {
+    __shared__ float red[8][32];
+    const int c = (int)threadIdx.x & 31, l = (int)threadIdx.x >> 5;
+    const int64_t n = (int64_t)blockIdx.x * 32 + c;
+    float s = 0.0f;
+    if (n < N) {
+        for (int k = l; k < chunks; k += 8) s += part[(int64_t)k * N + n];
+    }
+    red[l][c] = s;
+    __syncthreads();
+    if (l == 0 && n < N) {
+#pragma unroll
+        for (int k = 1; k < 8; ++k) s += red[k][c];
+        store_kind(out, n, kind, s);
+    }
+}
+
+struct BackPlan {
+    int cl_shift, col_blocks, chunks;
+    int64_t rows_per;
+};
+
+static BackPlan back_plan(int64_t M, int64_t N) {
+    BackPlan pl{};
+    while (pl.cl_shift < 5 && (8ll << pl.cl_shift) < N) ++pl.cl_shift;  // up to 32 column lanes (512 bytes of a row)
+    const int64_t cols = 8ll << pl.cl_shift, row_lanes = kBackThreads >> pl.cl_shift;
+    pl.col_blocks = (int)((N + cols - 1) / cols);
+    // about four workgroups a CU, each with at least four rows a lane
+    int64_t chunks = (1024 + pl.col_blocks - 1) / pl.col_blocks;
+    const int64_t most = (M + 4 * row_lanes - 1) / (4 * row_lanes);
+    if (chunks > most) chunks = most;
+    if (chunks < 1) chunks = 1;
+    pl.rows_per = (M + chunks - 1) / chunks;
+    if (pl.rows_per < 1) pl.rows_per = 1;
+    pl.chunks = M > 0 ? (int)((M + pl.rows_per - 1) / pl.rows_per) : 1;
+    return pl;
+}
+static int64_t back_bytes(const BackPlan& pl, int64_t N) {
+    return pl.chunks > 1 ? round_up((int64_t)pl.chunks * N * 4, 256) : 0;
+}
+
+static igc_status_t backward_any(bool fp16, int64_t M, int64_t N, igc_act_t act, const void* d, int64_t ldd,
+                                 const void* pre, int64_t ldp, void* dz, int64_t ldz, void* dbias, igc_out_t bias_type,
+                                 void* user_ws, int64_t user_ws_bytes, hipStream_t stream) {
+    if (M < 0 || N < 0 || (int)act < IGC_ACT_NONE || (int)act > IGC_ACT_SILU) return IGC_ERR_INVALID_VALUE;
+    if (dbias && !valid_type(bias_type)) return IGC_ERR_INVALID_VALUE;
+    if (N == 0 || (M == 0 && !dbias)) return IGC_OK;
+    if (!dz && !dbias) return IGC_ERR_INVALID_VALUE;
+    if (M > 0) {
+        if (!d || ldd < N || (act != IGC_ACT_NONE && !pre) || (pre && ldp < N) || (dz && ldz < N))
+            return IGC_ERR_INVALID_VALUE;
+        if (!aligned16(d) || ldd % 8 != 0 || (pre && (!aligned16(pre) || ldp % 8 != 0)) ||
+            (dz && (!aligned16(dz) || ldz % 8 != 0)))
+            return IGC_ERR_MISALIGNED;
+    }
+    if (dbias && reinterpret_cast<uintptr_t>(dbias) % out_size(bias_type)) return IGC_ERR_MISALIGNED;
+    if (N >= (1ll << 31) || M >= (1ll << 40)) return IGC_ERR_UNSUPPORTED;
+    const BackPlan pl = back_plan(M, N);
+    if ((int64_t)pl.col_blocks * pl.chunks > 0x7fffffff) return IGC_ERR_UNSUPPORTED;
+    Workspace ws;
+    if (const igc_status_t st = ws.take(dbias ? back_bytes(pl, N) : 0, user_ws, user_ws_bytes, stream)) return st;
+    (void)hipGetLastError();
+    BackArgs a{};
+    a.d = d;
+    a.pre = act == IGC_ACT_NONE ? nullptr : pre;
+    a.dz = dz;
+    a.dbias = dbias;
+    a.part = (float*)ws.ptr;
+    a.M = M;
+    a.N = N;
+    a.ldd = ldd;
+    a.ldp = ldp;
+    a.ldz = ldz;
+    a.rows_per = pl.rows_per;
+    a.cl_shift = pl.cl_shift;
+    a.col_blocks = pl.col_blocks;
+    a.chunks = pl.chunks;
+    a.act = (int)act;
+    a.bias_kind = (int)bias_type;
+    const dim3 grid((unsigned)(pl.col_blocks * pl.chunks));
+    if (fp16)
+        hipLaunchKernelGGL(epilogue_backward_kernel<true>, grid, dim3(kBackThreads), 0, stream, a);
+    else
+        hipLaunchKernelGGL(epilogue_backward_kernel<false>, grid, dim3(kBackThreads), 0, stream, a);
+    hipError_t e = hipGetLastError();
+    if (e == hipSuccess && dbias && pl.chunks > 1) {
+        hipLaunchKernelGGL(column_sum_kernel, dim3((unsigned)((N + 31) / 32)), dim3(256), 0, stream, a.part, N,
+                           pl.chunks, dbias, (int)bias_type);
+        e = hipGetLastError();
+    }
+    return e == hipSuccess ? IGC_OK : IGC_ERR_HIP;
+}
+
+}  // namespace igc
+
+using namespace igc;
+
+extern "C" {
+
+igc_status_t epilogue_backward_bf16(int64_t M, int64_t N, igc_act_t act, const void* dD, int64_t ldd, const void* pre,
+                                    int64_t ldp, void* dz, int64_t ldz, void* dbias, igc_out_t dbias_type,
+                                    igc_stream_t stream) {
+    return backward_any(false, M, N, act, dD, ldd, pre, ldp, dz, ldz, dbias, dbias_type, nullptr, 0,
+                        (hipStream_t)stream);
+}
+
+igc_status_t epilogue_backward_fp16(int64_t M, int64_t N, igc_act_t act, const void* dD, int64_t ldd, const void* pre,
+                                    int64_t ldp, void* dz, int64_t ldz, void* dbias, igc_out_t dbias_type,
+                                    igc_stream_t stream) {
+    return backward_any(true, M, N, act, dD, ldd, pre, ldp, dz, ldz, dbias, dbias_type, nullptr, 0,
+                        (hipStream_t)stream);
+}
+
+igc_status_t epilogue_backward_bf16_ex(int64_t M, int64_t N, igc_act_t act, const void* dD, int64_t ldd,
+                                       const void* pre, int64_t ldp, void* dz, int64_t ldz, void* dbias,
+                                       igc_out_t dbias_type, void* workspace, int64_t workspace_bytes,
+                                       igc_stream_t stream) {
+    return backward_any(false, M, N, act, dD, ldd, pre, ldp, dz, ldz, dbias, dbias_type, workspace, workspace_bytes,
+                        (hipStream_t)stream);
+}
+
+igc_status_t epilogue_backward_fp16_ex(int64_t M, int64_t N, igc_act_t act, const void* dD, int64_t ldd,
+                                       const void* pre, int64_t ldp, void* dz, int64_t ldz, void* dbias,
+                                       igc_out_t dbias_type, void* workspace, int64_t workspace_bytes,
+                                       igc_stream_t stream) {
+    return backward_any(true, M, N, act, dD, ldd, pre, ldp, dz, ldz, dbias, dbias_type, workspace, workspace_bytes,
+                        (hipStream_t)stream);
+}
+
+int64_t igc_epilogue_backward_workspace_bytes(int64_t M, int64_t N) {
+    if (M < 0 || N < 0) return -1;
+    return N == 0 ? 0 : back_bytes(back_plan(M, N), N);
+}
+
+}  // extern "C"

@@ -12,6 +12,9 @@
 #include <mutex>
 
 #include "igc.h"
+#include "epilogue.hpp"
+#include "few_rows.hpp"
+#include "host.hpp"
 #include "instances.hpp"
 #include "mainloop.hpp"
 #include "ring.hpp"
@@ -40,8 +43,6 @@ static __device__ __align__(256) char scratch[kScratchBytes];
 namespace igc {
 
 constexpr int kMaxDevices = 64;
-
-static bool aligned16(const void* ptr) { return (reinterpret_cast<uintptr_t>(ptr) & 15u) == 0; }
 
 // Per-device addresses of the library's device variables, looked up once per
 // device with that device current.  nullptr if the lookup failed.
@@ -114,7 +115,7 @@ static hipMemPool_t workspace_pool() {
 }
 
 // Stream-ordered workspace of `bytes` on the current device; nullptr on failure.
-static void* workspace_alloc(size_t bytes, hipStream_t stream) {
+void* workspace_alloc(size_t bytes, hipStream_t stream) {
     void* ptr = nullptr;
     hipMemPool_t pool = workspace_pool();
     hipError_t e = pool ? hipMallocFromPoolAsync(&ptr, bytes, pool, stream) : hipMallocAsync(&ptr, bytes, stream);
@@ -128,7 +129,7 @@ static void* workspace_alloc(size_t bytes, hipStream_t stream) {
 // caller's graph, allocated from the library's own pool; that use is refused
 // (the caller passes a workspace, or calls gemm_bf16_noalloc), since it has
 // not been shown to work on this runtime.
-static bool capturing(hipStream_t stream) {
+bool capturing(hipStream_t stream) {
     hipStreamCaptureStatus st = hipStreamCaptureStatusNone;
     if (hipStreamIsCapturing(stream, &st) != hipSuccess) {
         (void)hipGetLastError();
@@ -142,10 +143,6 @@ constexpr int kDefaultSpinLimit = 1 << 20;  // about a second of polling
 static std::atomic<int> g_sk_spin_limit{0};
 static std::atomic<int> g_sk_drop{-1};
 
-static int out_size(igc_out_t t) { return t == IGC_OUT_F32 ? 4 : 2; }
-
-static int64_t round_up(int64_t v, int64_t m) { return (v + m - 1) / m * m; }
-
 struct Plan {
     const Instance* inst = nullptr;
     igc_tune_t tune = {};
@@ -154,9 +151,10 @@ struct Plan {
 
 // The tile configuration and schedule for one call: an explicit tune is taken
 // as is; otherwise the built-in choice for the operation and shape.
-static Plan pick(const igc_tune_t* tune, bool fp16, bool a_kc, bool b_kc, int op, int64_t M, int64_t N, int64_t K) {
+static Plan pick(const igc_tune_t* tune, bool fp16, bool a_kc, bool b_kc, int op, int64_t M, int64_t N, int64_t K,
+                 bool epilogue = false) {
     Plan pl;
-    pl.tune = tune ? *tune : default_tune(M, N, K, op);
+    pl.tune = tune ? *tune : (epilogue ? epilogue_tune(M, N, K, op) : default_tune(M, N, K, op));
     const igc_tune_t& t = pl.tune;
     pl.inst = find_instance(t, fp16, a_kc, b_kc, op);
     pl.valid = t.stream_k >= 0 && !(t.k_splits > 1 && t.stream_k > 0) && (t.sk_hybrid == 0 || t.sk_hybrid == 1) &&
@@ -223,16 +221,26 @@ static int loop_variant(const Params& p, const Instance* inst) {
 }
 
 // Launches the mainloop (and, for a K split, the fixed-order reduction; for
-// stream-K, the flag clearing before it).  The workspace is the caller's, or
+// stream-K, the flag clearing before it).  With an epilogue, the kernel that
+// applies it, or the plain kernel's K split followed by the reduction that
+// does; stream-K has no such form.  The workspace is the caller's, or
 // taken from the library's pool and released with hipFreeAsync after the work
 // is enqueued, so concurrent calls on different streams never share it.
-static igc_status_t launch(const Plan& pl, Params p, void* user_ws, int64_t user_ws_bytes, hipStream_t stream) {
+static igc_status_t launch(const Plan& pl, Params p, const Epi* epi, void* user_ws, int64_t user_ws_bytes,
+                           hipStream_t stream) {
     const Instance* inst = pl.inst;
     const Layout L = layout_of(pl, p.M, p.N, p.K);
     if (L.tiles <= 0) return IGC_OK;
     if (L.tiles * L.S > 0x7fffffff) return IGC_ERR_UNSUPPORTED;
     // a configuration built without this loop variant or without stream-K kernels
-    if (!(L.G > 0 ? inst->fn_sk : inst->fn)[loop_variant(p, inst)]) return IGC_ERR_UNSUPPORTED;
+    const int v = loop_variant(p, inst);
+    const void* fn = L.G > 0 ? inst->fn_sk[v] : inst->fn[v];
+    if (epi && L.G > 0) return IGC_ERR_UNSUPPORTED;
+    if (epi && L.S == 1) {
+        const EpiInstance* ei = find_epilogue(*inst);
+        fn = ei ? ei->fn[epi->backward ? 1 : 0][v] : nullptr;
+    }
+    if (!fn) return IGC_ERR_UNSUPPORTED;
     if (user_ws && (user_ws_bytes < L.bytes || (reinterpret_cast<uintptr_t>(user_ws) & 255u)))
         return IGC_ERR_INVALID_VALUE;
     int* err = err_word_ptr();
@@ -248,8 +256,6 @@ static igc_status_t launch(const Plan& pl, Params p, void* user_ws, int64_t user
     }
     hipError_t e = hipSuccess;
     unsigned grid = 0;
-    const int v = loop_variant(p, inst);
-    const void* fn = L.G > 0 ? inst->fn_sk[v] : inst->fn[v];
     if (L.G > 0) {
         p.sk_grid = L.G;
         p.sk_units = L.UT;
@@ -276,25 +282,108 @@ static igc_status_t launch(const Plan& pl, Params p, void* user_ws, int64_t user
     }
     if (e == hipSuccess) {
         Params arg = p;
-        void* args[] = {&arg};
+        Epi earg = epi ? *epi : Epi{};
+        void* args[] = {&arg, &earg};  // (the plain kernels take the first alone)
         e = hipLaunchKernel(fn, dim3(grid), dim3(64 * inst->waves), args, 0, stream);
     }
     if (e == hipSuccess && L.G == 0 && L.S > 1)
-        e = launch_split_reduce(p.ws, L.S, p.ws_stride, p.M, p.N, p.ldws, p.C, p.ldc, p.out_kind, stream);
+        e = epi ? launch_split_epilogue(p.ws, L.S, p.ws_stride, p.M, p.N, p.ldws, p.C, p.ldc, p.out_kind, p.vec_ok, *epi,
+                                        stream)
+                : launch_split_reduce(p.ws, L.S, p.ws_stride, p.M, p.N, p.ldws, p.C, p.ldc, p.out_kind, stream);
     if (owned) (void)hipFreeAsync(ws, stream);
     if (e != hipSuccess) return IGC_ERR_HIP;
     return hipGetLastError() == hipSuccess ? IGC_OK : IGC_ERR_HIP;
 }
 
+// Checks an epilogue for an M x N output and fills the kernels' form of it.
+// dense: the convolutions, whose residual and pre are dense NPQK like their
+// output (the leading dimensions are not looked at and need no alignment).
+static igc_status_t check_epilogue(const igc_epilogue_t* q, int64_t N, bool dense, Epi& e) {
+    if (!q || (int)q->act < IGC_ACT_NONE || (int)q->act > IGC_ACT_SILU || (q->backward != 0 && q->backward != 1))
+        return IGC_ERR_INVALID_VALUE;
+    if (q->backward && q->act != IGC_ACT_NONE && !q->pre) return IGC_ERR_INVALID_VALUE;
+    e = Epi{};
+    e.act = (int)q->act;
+    e.backward = q->backward;
+    if (q->bias) {
+        if (!valid_type(q->bias_type)) return IGC_ERR_INVALID_VALUE;
+        if (reinterpret_cast<uintptr_t>(q->bias) % out_size(q->bias_type)) return IGC_ERR_MISALIGNED;
+        e.bias = q->bias;
+        e.bias_kind = (int)q->bias_type;
+    }
+    auto matrix = [&](const void* ptr, int64_t ld, igc_out_t type) {
+        if (!valid_type(type) || (!dense && ld < N)) return IGC_ERR_INVALID_VALUE;
+        if (!aligned16(ptr) || (!dense && ld * out_size(type) % 16 != 0)) return IGC_ERR_MISALIGNED;
+        return IGC_OK;
+    };
+    if (q->residual) {
+        if (const igc_status_t st = matrix(q->residual, q->ldr, q->residual_type)) return st;
+        e.res = q->residual;
+        e.ldr = dense ? N : q->ldr;
+        e.res_kind = (int)q->residual_type;
+    }
+    if (q->pre) {
+        if (const igc_status_t st = matrix(q->pre, q->ldp, q->pre_type)) return st;
+        e.pre = q->pre;
+        e.ldp = dense ? N : q->ldp;
+        e.pre_kind = (int)q->pre_type;
+    }
+    return IGC_OK;
+}
+
+// Whether a product runs on the kernel of few_rows.hip: at most kFewRows rows,
+// row-major A, and the 32-bit lane offsets of its loads in range.
+static bool takes_few_rows(int64_t M, int64_t N, int64_t K, int64_t lda, bool a_kc, int64_t ldb, bool b_kc) {
+    return a_kc && M >= 1 && M <= kFewRows && N < (1ll << 30) && K < (1ll << 31) && M * lda * 2 < 0x7fffffffLL &&
+           ((b_kc ? 16 : 32) * ldb + 256) * 2 < 0x7fffffffLL;
+}
+static int64_t few_rows_bytes(const FewRowsPlan& pl, int64_t M, int64_t N) {
+    return pl.splits > 1 ? round_up(pl.splits * M * round_up(N, 4) * 4, 256) : 0;
+}
+
+static igc_status_t few_rows(bool fp16, int64_t M, int64_t N, int64_t K, const void* A, int64_t lda, const void* B,
+                             int64_t ldb, bool b_kc, void* C, int64_t ldc, igc_out_t ct, const Epi& e, void* user_ws,
+                             int64_t user_ws_bytes, hipStream_t stream) {
+    const FewRowsPlan pl = few_rows_plan(M, N, K, b_kc);
+    if (pl.cols * pl.splits > 0x7fffffff) return IGC_ERR_UNSUPPORTED;
+    Workspace ws;
+    if (const igc_status_t st = ws.take(few_rows_bytes(pl, M, N), user_ws, user_ws_bytes, stream)) return st;
+    (void)hipGetLastError();
+    FewRowsArgs a{};
+    a.A = A;
+    a.B = B;
+    a.C = C;
+    a.ws = (float*)ws.ptr;
+    a.N = N;
+    a.K = K;
+    a.lda = lda;
+    a.ldb = ldb;
+    a.ldc = ldc;
+    a.ldws = round_up(N, 4);
+    a.per = pl.per;
+    a.M = (int)M;
+    a.cols = (int)pl.cols;
+    a.splits = pl.splits;
+    a.out_kind = (int)ct;
+    hipError_t err = launch_few_rows(a, e, fp16, b_kc, pl.vc, stream);
+    if (err == hipSuccess && pl.splits > 1)
+        err = launch_split_epilogue(a.ws, pl.splits, M * a.ldws, M, N, a.ldws, C, ldc, (int)ct, true, e, stream);
+    return err == hipSuccess ? IGC_OK : IGC_ERR_HIP;
+}
+
 static igc_status_t gemm_any(bool fp16, int64_t M, int64_t N, int64_t K, const void* A, int64_t lda,
                              igc_layout_t la, const void* B, int64_t ldb, igc_layout_t lb, void* C, int64_t ldc,
-                             igc_out_t ct, const igc_tune_t* tune, void* ws, int64_t ws_bytes, hipStream_t stream) {
+                             igc_out_t ct, const igc_tune_t* tune, void* ws, int64_t ws_bytes, hipStream_t stream,
+                             bool with_epilogue = false, const igc_epilogue_t* epi = nullptr) {
     if (M < 0 || N < 0 || K < 0) return IGC_ERR_INVALID_VALUE;
     if ((la != IGC_ROW_MAJOR && la != IGC_COL_MAJOR) || (lb != IGC_ROW_MAJOR && lb != IGC_COL_MAJOR))
         return IGC_ERR_INVALID_VALUE;
-    if (ct != IGC_OUT_F32 && ct != IGC_OUT_BF16 && ct != IGC_OUT_F16) return IGC_ERR_INVALID_VALUE;
+    if (!valid_type(ct)) return IGC_ERR_INVALID_VALUE;
+    Epi e{};
+    if (with_epilogue)
+        if (const igc_status_t st = check_epilogue(epi, N, false, e)) return st;
     const bool a_kc = la == IGC_ROW_MAJOR, b_kc = lb == IGC_COL_MAJOR;
-    const Plan pl = pick(tune, fp16, a_kc, b_kc, OP_GEMM, M, N, K);
+    const Plan pl = pick(tune, fp16, a_kc, b_kc, OP_GEMM, M, N, K, with_epilogue);
     if (!pl.valid) return IGC_ERR_INVALID_VALUE;
     const Instance* inst = pl.inst;
     if (!inst) return IGC_ERR_UNSUPPORTED;
@@ -314,6 +403,8 @@ static igc_status_t gemm_any(bool fp16, int64_t M, int64_t N, int64_t K, const v
     if (!aligned16(C) || (ldc * out_size(ct)) % 16 != 0) return IGC_ERR_MISALIGNED;
     if ((M + inst->bm - 1) / inst->bm > 0x7fffffff || (N + inst->bn - 1) / inst->bn > 0x7fffffff)
         return IGC_ERR_UNSUPPORTED;
+    if (with_epilogue && !tune && takes_few_rows(M, N, K, lda, a_kc, ldb, b_kc))
+        return few_rows(fp16, M, N, K, A, lda, B, ldb, b_kc, C, ldc, ct, e, ws, ws_bytes, stream);
 
     Params p = {};
     p.A = A;
@@ -331,7 +422,7 @@ static igc_status_t gemm_any(bool fp16, int64_t M, int64_t N, int64_t K, const v
     p.group_m = IGC_GROUP_M;
     p.k_ragged8 = (K % 8) != 0;
     p.vec_ok = 1;
-    return launch(pl, p, ws, ws_bytes, stream);
+    return launch(pl, p, with_epilogue ? &e : nullptr, ws, ws_bytes, stream);
 }
 
 // The GEMM view (M x N x K) of a convolution operation.
@@ -349,20 +440,26 @@ static void conv_view(int op, int64_t N, int64_t C, int64_t K, int64_t R, int64_
 // in0 / in1 / out: FPROP x, w -> y; DGRAD dy, w -> dx; WGRAD x, dy -> dw.
 static igc_status_t conv_any(int op, bool fp16, int N, int H, int W, int C, int K, int R, int S, int sh, int sw,
                              int ph, int pw, int dh, int dw, const void* in0, const void* in1, void* out,
-                             igc_out_t ot, const igc_tune_t* tune, void* ws, int64_t ws_bytes, hipStream_t stream) {
+                             igc_out_t ot, const igc_tune_t* tune, void* ws, int64_t ws_bytes, hipStream_t stream,
+                             bool with_epilogue = false, const igc_epilogue_t* epi = nullptr) {
     if (N < 0 || K < 0 || H < 1 || W < 1 || C < 1 || R < 1 || S < 1 || sh < 1 || sw < 1 || ph < 0 || pw < 0 ||
         dh < 1 || dw < 1)
         return IGC_ERR_INVALID_VALUE;
-    if (ot != IGC_OUT_F32 && ot != IGC_OUT_BF16 && ot != IGC_OUT_F16) return IGC_ERR_INVALID_VALUE;
+    if (!valid_type(ot)) return IGC_ERR_INVALID_VALUE;
     const int64_t hspan = (int64_t)H + 2LL * ph - (int64_t)dh * (R - 1) - 1;
     const int64_t wspan = (int64_t)W + 2LL * pw - (int64_t)dw * (S - 1) - 1;
     if (hspan < 0 || wspan < 0) return IGC_ERR_INVALID_VALUE;
     const int64_t P = hspan / sh + 1, Q = wspan / sw + 1;
     int64_t Mg, Ng, Kg;
     conv_view(op, N, C, K, R, S, H, W, P, Q, Mg, Ng, Kg);
+    Epi e{};
+    if (with_epilogue) {
+        if (const igc_status_t st = check_epilogue(epi, Ng, true, e)) return st;
+        if (e.backward) return IGC_ERR_UNSUPPORTED;
+    }
     // operand layouts of the views: FPROP A row / B col, DGRAD A row / B row, WGRAD A col / B row
     const bool a_kc = op != OP_WGRAD, b_kc = op == OP_FPROP;
-    const Plan pl = pick(tune, fp16, a_kc, b_kc, op, Mg, Ng, Kg);
+    const Plan pl = pick(tune, fp16, a_kc, b_kc, op, Mg, Ng, Kg, with_epilogue);
     if (!pl.valid) return IGC_ERR_INVALID_VALUE;
     const Instance* inst = pl.inst;
     if (!inst) return IGC_ERR_UNSUPPORTED;
@@ -433,7 +530,7 @@ static igc_status_t conv_any(int op, bool fp16, int N, int H, int W, int C, int 
     p.tpt_magic = fastdiv_magic((uint32_t)p.tpt);
     p.q_magic = fastdiv_magic((uint32_t)Q);
     p.pq_magic = fastdiv_magic((uint32_t)(P * Q));
-    return launch(pl, p, ws, ws_bytes, stream);
+    return launch(pl, p, with_epilogue ? &e : nullptr, ws, ws_bytes, stream);
 }
 
 }  // namespace igc
@@ -586,6 +683,85 @@ igc_status_t gemm_bf16_noalloc(int64_t M, int64_t N, int64_t K, const void* A, i
     if (!ws) return IGC_ERR_HIP;
     return gemm_any(false, M, N, K, A, lda, la, B, ldb, lb, C, ldc, c_type, tune, ws, kScratchBytes,
                     (hipStream_t)stream);
+}
+
+igc_status_t gemm_bf16_epilogue(int64_t M, int64_t N, int64_t K, const void* A, int64_t lda, igc_layout_t la,
+                                const void* B, int64_t ldb, igc_layout_t lb, void* D, int64_t ldd, igc_out_t d_type,
+                                const igc_epilogue_t* epilogue, igc_stream_t stream) {
+    return gemm_any(false, M, N, K, A, lda, la, B, ldb, lb, D, ldd, d_type, nullptr, nullptr, 0, (hipStream_t)stream,
+                    true, epilogue);
+}
+
+igc_status_t gemm_fp16_epilogue(int64_t M, int64_t N, int64_t K, const void* A, int64_t lda, igc_layout_t la,
+                                const void* B, int64_t ldb, igc_layout_t lb, void* D, int64_t ldd, igc_out_t d_type,
+                                const igc_epilogue_t* epilogue, igc_stream_t stream) {
+    return gemm_any(true, M, N, K, A, lda, la, B, ldb, lb, D, ldd, d_type, nullptr, nullptr, 0, (hipStream_t)stream,
+                    true, epilogue);
+}
+
+igc_status_t gemm_bf16_epilogue_ex(int64_t M, int64_t N, int64_t K, const void* A, int64_t lda, igc_layout_t la,
+                                   const void* B, int64_t ldb, igc_layout_t lb, void* D, int64_t ldd,
+                                   igc_out_t d_type, const igc_epilogue_t* epilogue, const igc_tune_t* tune,
+                                   void* workspace, int64_t workspace_bytes, igc_stream_t stream) {
+    return gemm_any(false, M, N, K, A, lda, la, B, ldb, lb, D, ldd, d_type, tune, workspace, workspace_bytes,
+                    (hipStream_t)stream, true, epilogue);
+}
+
+igc_status_t gemm_fp16_epilogue_ex(int64_t M, int64_t N, int64_t K, const void* A, int64_t lda, igc_layout_t la,
+                                   const void* B, int64_t ldb, igc_layout_t lb, void* D, int64_t ldd,
+                                   igc_out_t d_type, const igc_epilogue_t* epilogue, const igc_tune_t* tune,
+                                   void* workspace, int64_t workspace_bytes, igc_stream_t stream) {
+    return gemm_any(true, M, N, K, A, lda, la, B, ldb, lb, D, ldd, d_type, tune, workspace, workspace_bytes,
+                    (hipStream_t)stream, true, epilogue);
+}
+
+igc_status_t conv2d_nhwc_implicit_gemm_epilogue(int N, int H, int W, int C, int K, int R, int S, int stride_h,
+                                                int stride_w, int pad_h, int pad_w, int dil_h, int dil_w,
+                                                const void* x, const void* w, void* y, igc_out_t y_type,
+                                                const igc_epilogue_t* epilogue, igc_stream_t stream) {
+    return conv_any(OP_FPROP, false, N, H, W, C, K, R, S, stride_h, stride_w, pad_h, pad_w, dil_h, dil_w, x, w, y,
+                    y_type, nullptr, nullptr, 0, (hipStream_t)stream, true, epilogue);
+}
+
+igc_status_t conv2d_nhwc_implicit_gemm_epilogue_fp16(int N, int H, int W, int C, int K, int R, int S, int stride_h,
+                                                     int stride_w, int pad_h, int pad_w, int dil_h, int dil_w,
+                                                     const void* x, const void* w, void* y, igc_out_t y_type,
+                                                     const igc_epilogue_t* epilogue, igc_stream_t stream) {
+    return conv_any(OP_FPROP, true, N, H, W, C, K, R, S, stride_h, stride_w, pad_h, pad_w, dil_h, dil_w, x, w, y,
+                    y_type, nullptr, nullptr, 0, (hipStream_t)stream, true, epilogue);
+}
+
+igc_status_t conv2d_nhwc_implicit_gemm_epilogue_ex(int N, int H, int W, int C, int K, int R, int S, int stride_h,
+                                                   int stride_w, int pad_h, int pad_w, int dil_h, int dil_w,
+                                                   const void* x, const void* w, void* y, igc_out_t y_type,
+                                                   const igc_epilogue_t* epilogue, const igc_tune_t* tune,
+                                                   void* workspace, int64_t workspace_bytes, igc_stream_t stream) {
+    return conv_any(OP_FPROP, false, N, H, W, C, K, R, S, stride_h, stride_w, pad_h, pad_w, dil_h, dil_w, x, w, y,
+                    y_type, tune, workspace, workspace_bytes, (hipStream_t)stream, true, epilogue);
+}
+
+igc_status_t conv2d_nhwc_implicit_gemm_epilogue_fp16_ex(int N, int H, int W, int C, int K, int R, int S, int stride_h,
+                                                        int stride_w, int pad_h, int pad_w, int dil_h, int dil_w,
+                                                        const void* x, const void* w, void* y, igc_out_t y_type,
+                                                        const igc_epilogue_t* epilogue, const igc_tune_t* tune,
+                                                        void* workspace, int64_t workspace_bytes,
+                                                        igc_stream_t stream) {
+    return conv_any(OP_FPROP, true, N, H, W, C, K, R, S, stride_h, stride_w, pad_h, pad_w, dil_h, dil_w, x, w, y,
+                    y_type, tune, workspace, workspace_bytes, (hipStream_t)stream, true, epilogue);
+}
+
+int64_t igc_epilogue_workspace_bytes(igc_op_t op, int64_t M, int64_t N, int64_t K, const igc_tune_t* tune) {
+    if (M < 0 || N < 0 || K < 0 || (op != IGC_OP_GEMM && op != IGC_OP_CONV_FPROP)) return -1;
+    const Plan pl = pick(tune, false, true, true, (int)op, M, N, K, true);
+    if (!pl.valid || !pl.inst) return -1;
+    if (M == 0 || N == 0) return 0;
+    int64_t bytes = layout_of(pl, M, N, K).bytes;
+    if (op == IGC_OP_GEMM && !tune && M <= kFewRows)  // the operand layouts decide which kernel runs: room for either
+        for (const bool b_kc : {false, true}) {
+            const int64_t few = few_rows_bytes(few_rows_plan(M, N, K, b_kc), M, N);
+            bytes = few > bytes ? few : bytes;
+        }
+    return bytes;
 }
 
 int64_t igc_workspace_bytes(igc_op_t op, int64_t M, int64_t N, int64_t K, const igc_tune_t* tune) {

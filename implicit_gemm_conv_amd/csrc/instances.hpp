@@ -18,12 +18,24 @@ struct Instance {
     int64_t lds_bytes;   // static LDS of one workgroup
 };
 
+// The same configuration's kernels with the fused epilogue (epilogue.hpp).
+struct EpiInstance {
+    int bm, bn, bk, d, waves, mfma, half, loaders, sync;
+    int op;
+    bool fp16, a_kc, b_kc;
+    const void* fn[2][4];  // forward and backward, by loop variant; nullptr where not built
+};
+
 // Each compiled object (one configuration, one operation family) registers
 // its table when the library is loaded.
 void register_instances(const Instance* table, int count);
 
 const Instance* find_instance(const igc_tune_t& t, bool fp16, bool a_kc, bool b_kc, int op);
+void register_epilogues(const EpiInstance* table, int count);
+const EpiInstance* find_epilogue(const Instance& inst);
 igc_tune_t default_tune(int64_t M, int64_t N, int64_t K, int op);
+// The built-in choice for a call with an epilogue: no stream-K.
+igc_tune_t epilogue_tune(int64_t M, int64_t N, int64_t K, int op);
 int num_tunes();
 igc_tune_t tune_at(int i);
 int tune_scope(int i);

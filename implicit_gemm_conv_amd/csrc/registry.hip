@@ -29,6 +29,31 @@ void register_instances(const Instance* table, int count) {
     }
 }
 
+static const EpiInstance* g_epi_tables[kMaxTables];
+static int g_epi_counts[kMaxTables];
+static int g_nepi = 0;
+
+void register_epilogues(const EpiInstance* table, int count) {
+    if (g_nepi < kMaxTables) {
+        g_epi_tables[g_nepi] = table;
+        g_epi_counts[g_nepi] = count;
+        ++g_nepi;
+    }
+}
+
+const EpiInstance* find_epilogue(const Instance& q) {
+    for (int t = 0; t < g_nepi; ++t) {
+        for (int i = 0; i < g_epi_counts[t]; ++i) {
+            const EpiInstance& e = g_epi_tables[t][i];
+            if (e.bm == q.bm && e.bn == q.bn && e.bk == q.bk && e.d == q.d && e.waves == q.waves && e.mfma == q.mfma &&
+                e.half == q.half && e.loaders == q.loaders && e.sync == q.sync && e.op == q.op && e.fp16 == q.fp16 &&
+                e.a_kc == q.a_kc && e.b_kc == q.b_kc)
+                return &e;
+        }
+    }
+    return nullptr;
+}
+
 int num_tunes() { return (int)(sizeof(kTunes) / sizeof(kTunes[0])); }
 
 igc_tune_t tune_at(int i) { return kTunes[i]; }
@@ -132,6 +157,23 @@ igc_tune_t default_tune(int64_t M, int64_t N, int64_t K, int op) {
             small.stream_k = (int)kCUs;
     }
     return small;
+}
+
+// As default_tune, except that the shapes it gives to stream-K (128 x 128 tiles
+// that leave CUs idle, a deep K, and no even split) split K instead: the split
+// count that leaves the fewest CU rounds for one part's share, at least 1024 of
+// K a part, with the smaller count (fewer partial sums) on a tie.
+igc_tune_t epilogue_tune(int64_t M, int64_t N, int64_t K, int op) {
+    igc_tune_t t = default_tune(M, N, K, op);
+    if (t.stream_k <= 0) return t;
+    constexpr int64_t kCUs = 256;
+    const int64_t tiles = ((M + t.bm - 1) / t.bm) * ((N + t.bn - 1) / t.bn);
+    t.stream_k = 0;
+    int64_t best = 1;
+    for (int64_t s = 2; s <= 16 && K / s >= 1024; ++s)
+        if (((tiles * s + kCUs - 1) / kCUs) * best < ((tiles * best + kCUs - 1) / kCUs) * s) best = s;
+    t.k_splits = best > 1 ? (int)best : 0;
+    return t;
 }
 
 }  // namespace igc

@@ -5,6 +5,7 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include "epilogue.hpp"
 #include "split_reduce.hpp"
 
 namespace igc {
@@ -88,6 +89,80 @@ hipError_t launch_split_reduce(const float* ws, int S, int64_t ws_stride, int64_
     else
         hipLaunchKernelGGL(split_reduce_kernel<false>, dim3((unsigned)blocks), dim3(256), 0, stream, ws, S,
                            ws_stride, M, N, ldws, C, ldc, kind);
+    return hipGetLastError();
+}
+
+// The same sum, then the epilogue: eight outputs of a row a thread, partials added in split order.  VEC:
+// every row of the output, residual and pre is a 16-byte multiple from the next.
+template <bool VEC>
+__global__ __launch_bounds__(256) void split_epilogue_kernel(const float* __restrict__ ws, int S, int64_t ws_stride,
+                                                             int64_t M, int64_t N, int64_t ldws, void* C, int64_t ldc,
+                                                             int kind, const Epi e) {
+    const int64_t n8 = (N + 7) / 8;
+    const int64_t idx = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
+    if (idx >= M * n8) return;
+    const int64_t m = M * n8 <= 0xffffffffLL ? (int64_t)((uint32_t)idx / (uint32_t)n8) : idx / n8;
+    const int64_t n = (idx - m * n8) * 8;
+    const int left = N - n >= 8 ? 8 : (int)(N - n);
+    const bool two = left > 4;  // ldws is N rounded up to 4: the second 16 bytes of a part may lie past the row
+    float r[8], g[8], b[8];
+    if (e.res) load8(e.res, m * e.ldr + n, e.res_kind, left, VEC, r);
+    if (e.backward && e.pre) load8(e.pre, m * e.ldp + n, e.pre_kind, left, VEC, g);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) b[i] = e.bias && i < left ? load_kind(e.bias, n + i, e.bias_kind) : 0.0f;
+    const float* src = ws + m * ldws + n;
+    const float* src1 = two ? src + 4 : src;
+    f32x4r_t lo = *(const f32x4r_t*)src, hi = *(const f32x4r_t*)src1;
+    int s = 1;
+    for (; s + 3 < S; s += 4) {
+        f32x4r_t p0[4], p1[4];
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+            p0[u] = *(const f32x4r_t*)(src + (s + u) * ws_stride);
+            p1[u] = *(const f32x4r_t*)(src1 + (s + u) * ws_stride);
+        }
+#pragma unroll
+        for (int u = 0; u < 4; ++u) lo += p0[u], hi += p1[u];
+    }
+    for (; s < S; ++s) {
+        lo += *(const f32x4r_t*)(src + s * ws_stride);
+        hi += *(const f32x4r_t*)(src1 + s * ws_stride);
+    }
+    float v[8];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = lo[i] + b[i], v[4 + i] = hi[i] + b[4 + i];
+    if (e.backward) {
+        if (e.pre)
+            with_act(e.act, [&](auto A) __attribute__((always_inline)) {
+#pragma unroll
+                for (int i = 0; i < 8; ++i) v[i] *= act_grad_of<decltype(A)::value>(g[i]);
+            });
+    } else {
+        if (e.pre) store8(e.pre, m * e.ldp + n, e.pre_kind, left, VEC, v);
+        with_act(e.act, [&](auto A) __attribute__((always_inline)) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v[i] = act_of<decltype(A)::value>(v[i]);
+        });
+    }
+    if (e.res) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] += r[i];
+    }
+    store8(C, m * ldc + n, kind, left, VEC, v);
+}
+
+hipError_t launch_split_epilogue(const float* ws, int S, int64_t ws_stride, int64_t M, int64_t N, int64_t ldws,
+                                 void* C, int64_t ldc, int kind, bool vec, const Epi& e, hipStream_t stream) {
+    const int64_t work = M * ((N + 7) / 8);
+    if (work <= 0) return hipSuccess;
+    const int64_t blocks = (work + 255) / 256;
+    if (blocks > 0x7fffffff) return hipErrorInvalidValue;
+    if (vec)
+        hipLaunchKernelGGL(split_epilogue_kernel<true>, dim3((unsigned)blocks), dim3(256), 0, stream, ws, S, ws_stride,
+                           M, N, ldws, C, ldc, kind, e);
+    else
+        hipLaunchKernelGGL(split_epilogue_kernel<false>, dim3((unsigned)blocks), dim3(256), 0, stream, ws, S,
+                           ws_stride, M, N, ldws, C, ldc, kind, e);
     return hipGetLastError();
 }
 

@@ -11,6 +11,12 @@ namespace igc {
 hipError_t launch_split_reduce(const float* ws, int S, int64_t ws_stride, int64_t M, int64_t N, int64_t ldws,
                                void* C, int64_t ldc, int kind, hipStream_t stream);
 
+// C = epilogue(sum_{s<S} ws[s*ws_stride + m*ldws + n]) (epilogue.hpp).  vec: the rows and bases of C, of the residual
+// and of pre are 16-byte multiples.
+struct Epi;
+hipError_t launch_split_epilogue(const float* ws, int S, int64_t ws_stride, int64_t M, int64_t N, int64_t ldws,
+                                 void* C, int64_t ldc, int kind, bool vec, const Epi& e, hipStream_t stream);
+
 // Sets flags[0 .. n) to zero, ordered before later work on `stream`.
 hipError_t launch_clear_flags(int* flags, int n, hipStream_t stream);
 

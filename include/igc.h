@@ -2,7 +2,9 @@
  * igc.h -- C ABI of libigc: a software-pipelined bf16/fp16 GEMM with fp32
  * accumulation, and the same mainloop run as implicit-GEMM (im2col) NHWC
  * convolutions (forward, data gradient, filter gradient), for AMD Instinct
- * MI355X (gfx950).
+ * MI355X (gfx950); products and forward convolutions with bias, activation and
+ * residual in their epilogue, the epilogue's gradient, and group norm with an
+ * activation, forward and backward.
  *
  * What is computed follows the "B200 TMA Pipeline Designer" page (section
  * "E -- Executable steps": a tiled matrix product fed by a ring of PIPE_DEPTH
@@ -42,7 +44,8 @@
  *   elements for 16-bit types, 4 for fp32).  Otherwise IGC_ERR_MISALIGNED.
  * - Arguments are checked before anything is launched; on any error nothing
  *   is enqueued and the output is untouched.  No exception crosses the ABI.
- * - Outputs must not alias inputs (not checked; the result is undefined).
+ * - Outputs must not alias inputs except where an operation says so (not
+ *   checked; the result is undefined).
  * - Results are deterministic: the same inputs and tune give the same bits on
  *   every call (no atomics; a fixed summation order per output element).
  * - Device errors: a stream-K owner waits for the partials of the workgroups
@@ -270,6 +273,188 @@ igc_status_t gemm_bf16_noalloc(int64_t M, int64_t N, int64_t K, const void *A, i
                                const void *B, int64_t ldb, igc_layout_t lb, void *C, int64_t ldc, igc_out_t c_type,
                                igc_stream_t stream);
 
+/*
+ * Fused epilogues.  What a layer does to a product before it is rounded, in
+ * fp32 and with one rounding:
+ *   backward 0:  z = (A*B)[m][n] + bias[n];  pre[m][n] = z (rounded, if pre is given);
+ *                D[m][n] = act(z) + residual[m][n]
+ *   backward 1:  D[m][n] = ((A*B)[m][n] + bias[n]) * act'(pre[m][n]) + residual[m][n]
+ * the second being the gradient that reaches z of the layer below when A*B is
+ * the product of dy with the upper layer's weights.
+ *   act            IGC_ACT_NONE: z; RELU: max(z, 0), derivative 0 at 0; GELU:
+ *                  z Phi(z); GELU_TANH: z/2 (1 + tanh(sqrt(2/pi) (z + 0.044715 z^3)));
+ *                  SILU: z / (1 + exp(-z)).  A NaN stays a NaN.
+ *   bias           N values of bias_type, aligned to their size; NULL: none
+ *   residual       M x N of residual_type, row-major, ldr >= N; NULL: none
+ *   pre            M x N of pre_type, row-major, ldp >= N: written (backward 0)
+ *                  or read (backward 1); NULL: not kept, allowed with backward 1
+ *                  only for IGC_ACT_NONE
+ * residual and pre keep the alignment rule of every tensor.  Either may be D
+ * itself (same pointer, leading dimension and type) when it is read: each
+ * element is read before it is written.  Otherwise nothing may alias.
+ */
+typedef enum {
+    IGC_ACT_NONE = 0,
+    IGC_ACT_RELU = 1,
+    IGC_ACT_GELU = 2,
+    IGC_ACT_GELU_TANH = 3,
+    IGC_ACT_SILU = 4
+} igc_act_t;
+
+typedef struct {
+    igc_act_t act;
+    int backward;
+    const void *bias;
+    igc_out_t bias_type;
+    const void *residual;
+    int64_t ldr;
+    igc_out_t residual_type;
+    void *pre;
+    int64_t ldp;
+    igc_out_t pre_type;
+} igc_epilogue_t;
+
+/* GEMM with a fused epilogue: operands, layouts, sizes, alignment and errors
+ * as gemm_bf16 / gemm_fp16, D in the place of C; epilogue must not be NULL.
+ * K == 0 leaves z = bias.  With the built-in choice, at most 64 rows of a
+ * row-major A run on a kernel that streams B once; tiles and schedules with an
+ * explicit tune as gemm_bf16_ex, without stream-K (IGC_ERR_UNSUPPORTED), and
+ * without a K split only for the configurations the built-in choice takes.
+ * Workspace: igc_epilogue_workspace_bytes. */
+igc_status_t gemm_bf16_epilogue(int64_t M, int64_t N, int64_t K, const void *A, int64_t lda, igc_layout_t la,
+                                const void *B, int64_t ldb, igc_layout_t lb, void *D, int64_t ldd, igc_out_t d_type,
+                                const igc_epilogue_t *epilogue, igc_stream_t stream);
+igc_status_t gemm_fp16_epilogue(int64_t M, int64_t N, int64_t K, const void *A, int64_t lda, igc_layout_t la,
+                                const void *B, int64_t ldb, igc_layout_t lb, void *D, int64_t ldd, igc_out_t d_type,
+                                const igc_epilogue_t *epilogue, igc_stream_t stream);
+igc_status_t gemm_bf16_epilogue_ex(int64_t M, int64_t N, int64_t K, const void *A, int64_t lda, igc_layout_t la,
+                                   const void *B, int64_t ldb, igc_layout_t lb, void *D, int64_t ldd,
+                                   igc_out_t d_type, const igc_epilogue_t *epilogue, const igc_tune_t *tune,
+                                   void *workspace, int64_t workspace_bytes, igc_stream_t stream);
+igc_status_t gemm_fp16_epilogue_ex(int64_t M, int64_t N, int64_t K, const void *A, int64_t lda, igc_layout_t la,
+                                   const void *B, int64_t ldb, igc_layout_t lb, void *D, int64_t ldd,
+                                   igc_out_t d_type, const igc_epilogue_t *epilogue, const igc_tune_t *tune,
+                                   void *workspace, int64_t workspace_bytes, igc_stream_t stream);
+
+/* Forward convolution with a fused epilogue: arguments and errors as
+ * conv2d_nhwc_implicit_gemm; bias has one value per filter, residual and pre
+ * are dense NPQK like y (ldr and ldp are not looked at).  backward 1 is
+ * IGC_ERR_UNSUPPORTED. */
+igc_status_t conv2d_nhwc_implicit_gemm_epilogue(int N, int H, int W, int C, int K, int R, int S, int stride_h,
+                                                int stride_w, int pad_h, int pad_w, int dil_h, int dil_w,
+                                                const void *x, const void *w, void *y, igc_out_t y_type,
+                                                const igc_epilogue_t *epilogue, igc_stream_t stream);
+igc_status_t conv2d_nhwc_implicit_gemm_epilogue_fp16(int N, int H, int W, int C, int K, int R, int S, int stride_h,
+                                                     int stride_w, int pad_h, int pad_w, int dil_h, int dil_w,
+                                                     const void *x, const void *w, void *y, igc_out_t y_type,
+                                                     const igc_epilogue_t *epilogue, igc_stream_t stream);
+igc_status_t conv2d_nhwc_implicit_gemm_epilogue_ex(int N, int H, int W, int C, int K, int R, int S, int stride_h,
+                                                   int stride_w, int pad_h, int pad_w, int dil_h, int dil_w,
+                                                   const void *x, const void *w, void *y, igc_out_t y_type,
+                                                   const igc_epilogue_t *epilogue, const igc_tune_t *tune,
+                                                   void *workspace, int64_t workspace_bytes, igc_stream_t stream);
+igc_status_t conv2d_nhwc_implicit_gemm_epilogue_fp16_ex(int N, int H, int W, int C, int K, int R, int S,
+                                                        int stride_h, int stride_w, int pad_h, int pad_w, int dil_h,
+                                                        int dil_w, const void *x, const void *w, void *y,
+                                                        igc_out_t y_type, const igc_epilogue_t *epilogue,
+                                                        const igc_tune_t *tune, void *workspace,
+                                                        int64_t workspace_bytes, igc_stream_t stream);
+
+/* Workspace bytes of a call with an epilogue (op IGC_OP_GEMM or
+ * IGC_OP_CONV_FPROP; GEMM view M x N x K; enough for every operand layout);
+ * 0 when the schedule does not split K, -1 for bad arguments. */
+int64_t igc_epilogue_workspace_bytes(igc_op_t op, int64_t M, int64_t N, int64_t K, const igc_tune_t *tune);
+
+/*
+ * Gradient of the epilogue in one pass, for a dD and a pre of the input type
+ * (bf16 or fp16), M x N row-major (a convolution's dense y: M = N*P*Q, N = K):
+ *   dz[m][n] = dD[m][n] * act'(pre[m][n])      (rounded once)
+ *   dbias[n] = sum over m of dD[m][n] * act'(pre[m][n])      (summed in fp32 before any rounding)
+ * The gradient of the residual is dD itself.  dz NULL: only dbias (of
+ * dbias_type, aligned to its size); dbias NULL: only dz; both NULL is
+ * IGC_ERR_INVALID_VALUE.  pre is read only when act is not IGC_ACT_NONE.  dz
+ * may be dD or pre (same leading dimension).  M == 0 writes dbias = 0.
+ * Workspace when dbias is given: igc_epilogue_backward_workspace_bytes.
+ */
+igc_status_t epilogue_backward_bf16(int64_t M, int64_t N, igc_act_t act, const void *dD, int64_t ldd, const void *pre,
+                                    int64_t ldp, void *dz, int64_t ldz, void *dbias, igc_out_t dbias_type,
+                                    igc_stream_t stream);
+igc_status_t epilogue_backward_fp16(int64_t M, int64_t N, igc_act_t act, const void *dD, int64_t ldd, const void *pre,
+                                    int64_t ldp, void *dz, int64_t ldz, void *dbias, igc_out_t dbias_type,
+                                    igc_stream_t stream);
+igc_status_t epilogue_backward_bf16_ex(int64_t M, int64_t N, igc_act_t act, const void *dD, int64_t ldd,
+                                       const void *pre, int64_t ldp, void *dz, int64_t ldz, void *dbias,
+                                       igc_out_t dbias_type, void *workspace, int64_t workspace_bytes,
+                                       igc_stream_t stream);
+igc_status_t epilogue_backward_fp16_ex(int64_t M, int64_t N, igc_act_t act, const void *dD, int64_t ldd,
+                                       const void *pre, int64_t ldp, void *dz, int64_t ldz, void *dbias,
+                                       igc_out_t dbias_type, void *workspace, int64_t workspace_bytes,
+                                       igc_stream_t stream);
+int64_t igc_epilogue_backward_workspace_bytes(int64_t M, int64_t N);
+
+/*
+ * Group norm with an activation over channels-last images (bf16 or fp16 x and
+ * y, fp32 inside): N images of H x W pixels whose C channels lie together,
+ * pixels ldx (ldy) elements apart, images H*W*ldx apart, so that a slice of a
+ * wider tensor's channels can be read or written in place.  The C channels
+ * form G groups of C/G neighbours; mean and variance (of the values, not of a
+ * sample) are taken over a group's H*W*(C/G) values of one image:
+ *   y = act((x - mean) / sqrt(var + eps) * gamma[c] + beta[c])
+ * gamma, beta: C values of param_type, aligned to their size; NULL: 1 and 0.
+ * mean, rstd: N*G fp32 values each, written when not NULL (the backward pass
+ * takes them).  y may be x (ldy == ldx).
+ * Requirements: H, W, C, G >= 1, N >= 0 (N == 0 is a no-op), C % G == 0, ldx,
+ * ldy >= C, eps >= 0, else IGC_ERR_INVALID_VALUE; C % 8 == 0 and the alignment
+ * rule, else IGC_ERR_MISALIGNED; H*W < 2^31 and N*C < 2^30, else
+ * IGC_ERR_UNSUPPORTED.  Workspace: igc_group_norm_workspace_bytes.
+ */
+igc_status_t group_norm_nhwc_bf16(int N, int H, int W, int C, int G, const void *x, int64_t ldx, const void *gamma,
+                                  const void *beta, igc_out_t param_type, float eps, igc_act_t act, void *y,
+                                  int64_t ldy, float *mean, float *rstd, igc_stream_t stream);
+igc_status_t group_norm_nhwc_fp16(int N, int H, int W, int C, int G, const void *x, int64_t ldx, const void *gamma,
+                                  const void *beta, igc_out_t param_type, float eps, igc_act_t act, void *y,
+                                  int64_t ldy, float *mean, float *rstd, igc_stream_t stream);
+igc_status_t group_norm_nhwc_bf16_ex(int N, int H, int W, int C, int G, const void *x, int64_t ldx,
+                                     const void *gamma, const void *beta, igc_out_t param_type, float eps,
+                                     igc_act_t act, void *y, int64_t ldy, float *mean, float *rstd, void *workspace,
+                                     int64_t workspace_bytes, igc_stream_t stream);
+igc_status_t group_norm_nhwc_fp16_ex(int N, int H, int W, int C, int G, const void *x, int64_t ldx,
+                                     const void *gamma, const void *beta, igc_out_t param_type, float eps,
+                                     igc_act_t act, void *y, int64_t ldy, float *mean, float *rstd, void *workspace,
+                                     int64_t workspace_bytes, igc_stream_t stream);
+
+/*
+ * Gradient of the group norm above, from its x, gamma, beta, act and the mean
+ * and rstd that it wrote: with xh = (x - mean) rstd and dz = dy * act'(gamma xh + beta),
+ *   dx = rstd (gamma dz - mean(gamma dz) - xh mean(gamma dz xh))     (means over the group)
+ *   dgamma[c] = sum dz xh,  dbeta[c] = sum dz      (over every image's pixels; of param_type; either may be NULL)
+ * dx may be dy or x (same pixel distance).  N == 0 writes zero dgamma and
+ * dbeta.  Requirements and workspace as the forward pass.
+ */
+igc_status_t group_norm_nhwc_backward_bf16(int N, int H, int W, int C, int G, const void *x, int64_t ldx,
+                                           const void *gamma, const void *beta, igc_out_t param_type,
+                                           const float *mean, const float *rstd, igc_act_t act, const void *dy,
+                                           int64_t lddy, void *dx, int64_t lddx, void *dgamma, void *dbeta,
+                                           igc_stream_t stream);
+igc_status_t group_norm_nhwc_backward_fp16(int N, int H, int W, int C, int G, const void *x, int64_t ldx,
+                                           const void *gamma, const void *beta, igc_out_t param_type,
+                                           const float *mean, const float *rstd, igc_act_t act, const void *dy,
+                                           int64_t lddy, void *dx, int64_t lddx, void *dgamma, void *dbeta,
+                                           igc_stream_t stream);
+igc_status_t group_norm_nhwc_backward_bf16_ex(int N, int H, int W, int C, int G, const void *x, int64_t ldx,
+                                              const void *gamma, const void *beta, igc_out_t param_type,
+                                              const float *mean, const float *rstd, igc_act_t act, const void *dy,
+                                              int64_t lddy, void *dx, int64_t lddx, void *dgamma, void *dbeta,
+                                              void *workspace, int64_t workspace_bytes, igc_stream_t stream);
+igc_status_t group_norm_nhwc_backward_fp16_ex(int N, int H, int W, int C, int G, const void *x, int64_t ldx,
+                                              const void *gamma, const void *beta, igc_out_t param_type,
+                                              const float *mean, const float *rstd, igc_act_t act, const void *dy,
+                                              int64_t lddy, void *dx, int64_t lddx, void *dgamma, void *dbeta,
+                                              void *workspace, int64_t workspace_bytes, igc_stream_t stream);
+
+/* Workspace bytes of either direction of the group norm; -1 for bad arguments. */
+int64_t igc_group_norm_workspace_bytes(int N, int H, int W, int C, int G);
+
 /* Workspace bytes a call needs for operation `op` with GEMM view M x N x K
  * (see each operation above) under `tune` (NULL: the built-in choice): 0 when
  * the schedule does not split K.  Returns -1 for negative sizes, a bad op or
@@ -290,8 +475,9 @@ int igc_default_tune(igc_op_t op, int64_t M, int64_t N, int64_t K, igc_tune_t *o
  * K % 8 == 0, and the bf16 forward convolution with whole filter taps per K tile and filters of at most
  * 16 x 16 -- other calls are IGC_ERR_UNSUPPORTED), IGC_SCOPE_STREAM_K (stream-K schedules; without it
  * a tune with stream_k > 0 is IGC_ERR_UNSUPPORTED) and IGC_SCOPE_CONV_FPROP (the bf16 and fp16 forward
- * convolution with every loop variant, besides the GEMMs with row-major A); 0 for an index out of range. */
-enum { IGC_SCOPE_ALL = 1, IGC_SCOPE_STREAM_K = 2, IGC_SCOPE_CONV_FPROP = 4 };
+ * convolution with every loop variant, besides the GEMMs with row-major A) and IGC_SCOPE_EPILOGUE (the fused
+ * epilogue of the forward convolution, and with IGC_SCOPE_ALL of the GEMMs); 0 for an index out of range. */
+enum { IGC_SCOPE_ALL = 1, IGC_SCOPE_STREAM_K = 2, IGC_SCOPE_CONV_FPROP = 4, IGC_SCOPE_EPILOGUE = 8 };
 int igc_tune_count(void);
 int igc_tune_get(int i, igc_tune_t *out);
 int igc_tune_scope(int i);
