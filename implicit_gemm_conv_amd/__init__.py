@@ -11,6 +11,7 @@ Build it with `python -m implicit_gemm_conv_amd.build` (or __graft_entry__.build
 """
 import ctypes
 import os
+import struct
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libigc.so")
@@ -86,45 +87,65 @@ def act_code(act):
     return ACT_CODES[act] if isinstance(act, str) else int(act)
 
 
-_DTYPE_CODES = {"torch.float32": OUT_F32, "torch.bfloat16": OUT_BF16, "torch.float16": OUT_F16}
+_DTYPE_CODES = {}
 
 
 def out_code(dtype):
     """The OUT_ code of a torch dtype."""
-    try:
-        return _DTYPE_CODES[str(dtype)]
-    except KeyError:
-        raise TypeError(f"{dtype}: float32, bfloat16 or float16 wanted") from None
+    code = _DTYPE_CODES.get(dtype)
+    if code is None:
+        code = {"torch.float32": OUT_F32, "torch.bfloat16": OUT_BF16, "torch.float16": OUT_F16}.get(str(dtype))
+        if code is None:
+            raise TypeError(f"{dtype}: float32, bfloat16 or float16 wanted")
+        _DTYPE_CODES[dtype] = code
+    return code
+
+
+_EPILOGUE = struct.Struct("@iiPiPqiPqi0q")  # igc_epilogue_t, the layout of CEpilogue
+assert _EPILOGUE.size == ctypes.sizeof(CEpilogue)
+
+
+def _bias(x, code):
+    if hasattr(x, "data_ptr"):
+        if x.dim() and x.shape[-1] > 1 and x.stride(-1) != 1:
+            raise ValueError("values of a row must lie together")
+        return x.data_ptr(), out_code(x.dtype) if code is None else code
+    if code is None:
+        raise TypeError("a raw address needs its type")
+    return int(x), code
+
+
+def _matrix(x, code, ld):
+    if hasattr(x, "data_ptr"):
+        strides = x.stride()
+        if strides and strides[-1] != 1 and x.shape[-1] > 1:
+            raise ValueError("values of a row must lie together")
+        if ld is None:
+            ld = strides[0] if len(strides) == 2 else 0
+        return x.data_ptr(), ld, out_code(x.dtype) if code is None else code
+    if code is None or ld is None:
+        raise TypeError("a raw address needs its type and leading dimension")
+    return int(x), ld, code
 
 
 class Epilogue:
-    """A fused epilogue (igc_epilogue_t) from tensors: types come from their dtypes, the leading dimensions of
-    `residual` and `pre` from their first stride unless given, and the tensors are kept alive with it.  A raw
-    device address needs its type (bias_type, residual_type, pre_type: an OUT_ code) and leading dimension."""
-    __slots__ = ("c", "_keep")
+    """A fused epilogue (igc_epilogue_t) from tensors: types come from their dtypes, the leading dimensions of a
+    `residual` and `pre` of two dimensions from their first stride unless given (a convolution's are not looked at),
+    and the tensors are kept alive with it.  A raw device address needs its type (bias_type, residual_type, pre_type:
+    an OUT_ code) and leading dimension.  `raw` holds the packed C structure: calls take it as it is."""
+    __slots__ = ("raw", "_keep")
 
     def __init__(self, act="none", bias=None, residual=None, pre=None, backward=False, ldr=None, ldp=None,
                  bias_type=None, residual_type=None, pre_type=None):
-        c = self.c = CEpilogue()
         self._keep = (bias, residual, pre)
-        c.act, c.backward = act_code(act), int(backward)
-        if bias is not None:
-            c.bias, c.bias_type, _ = self._tensor(bias, bias_type, 0, 1)
-        if residual is not None:
-            c.residual, c.residual_type, c.ldr = self._tensor(residual, residual_type, ldr, 2)
-        if pre is not None:
-            c.pre, c.pre_type, c.ldp = self._tensor(pre, pre_type, ldp, 2)
+        self.raw = _EPILOGUE.pack(act_code(act), backward, *((0, 0) if bias is None else _bias(bias, bias_type)),
+                                  *((0, 0, 0) if residual is None else _matrix(residual, residual_type, ldr)),
+                                  *((0, 0, 0) if pre is None else _matrix(pre, pre_type, ldp)))
 
-    @staticmethod
-    def _tensor(x, code, ld, dims):
-        if not hasattr(x, "data_ptr"):
-            if code is None or ld is None:
-                raise TypeError("a raw address needs its type and leading dimension")
-            return int(x), code, ld
-        if x.dim() >= 1 and x.shape[-1] > 1 and x.stride(-1) != 1:
-            raise ValueError("values of a row must lie together")
-        return (x.data_ptr(), out_code(x.dtype) if code is None else code,
-                ld if ld is not None else (x.stride(0) if x.dim() == dims else 0))
+    @property
+    def c(self):
+        """A copy of the C structure."""
+        return CEpilogue.from_buffer_copy(self.raw)
 
 
 _lib = None
@@ -155,7 +176,7 @@ def lib():
             protos[base + "_fp16"] = conv + [p]
             protos[base + "_ex"] = conv + [tp, p, i64, p]
             protos[base + "_fp16_ex"] = conv + [tp, p, i64, p]
-        ep, f32 = ctypes.POINTER(CEpilogue), ctypes.c_float
+        ep, f32 = p, ctypes.c_float  # (a packed igc_epilogue_t)
         for base in ("gemm_bf16_epilogue", "gemm_fp16_epilogue"):
             protos[base] = gemm + [ep, p]
             protos[base + "_ex"] = gemm + [ep, tp, p, i64, p]
@@ -224,8 +245,8 @@ def _ptr(x):
 def _nbytes(x):
     if x is None:
         return 0
-    if hasattr(x, "numel"):
-        return x.numel() * x.element_size()
+    if hasattr(x, "nbytes"):
+        return x.nbytes
     raise TypeError("pass workspace_bytes with a raw workspace address")
 
 
@@ -236,6 +257,24 @@ def _stream(stream):
     if hasattr(stream, "cuda_stream"):
         return ctypes.c_void_p(stream.cuda_stream)
     return ctypes.c_void_p(int(stream))
+
+
+_current_handle = None
+
+
+def _raw_stream(stream):
+    """The handle of `stream`, or of torch's current one, as an integer.  (torch.cuda.current_stream() builds a Stream
+    object, 2.8 us a call; torch's own generated code asks for the handle alone, 0.2 us.)"""
+    if stream is None:
+        global _current_handle
+        if _current_handle is None:
+            import torch
+            raw, device = (getattr(torch._C, n, None) for n in ("_cuda_getCurrentRawStream", "_cuda_getDevice"))
+            torch.cuda.init()
+            _current_handle = (lambda: raw(device())) if raw and device else \
+                (lambda: torch.cuda.current_stream().cuda_stream)
+        return _current_handle()
+    return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
 def _tune(t):
@@ -310,83 +349,111 @@ conv2d_nhwc_wgrad_implicit_gemm_fp16_ex = _conv_ex("conv2d_nhwc_wgrad_implicit_g
 
 
 def _epi(e):
-    if e is None:
-        return None
-    return ctypes.byref(e.c if isinstance(e, Epilogue) else e)
+    return e.raw if isinstance(e, Epilogue) else None if e is None else bytes(e)
 
+
+def _address(x):
+    """A tensor's device address, or an address as it is."""
+    try:
+        return x.data_ptr()
+    except AttributeError:
+        return None if x is None else int(x)
+
+
+def _entry(name):
+    """The C function, looked up once, at the first call."""
+    found = []
+
+    def get():
+        if not found:
+            found.append(getattr(lib(), name))
+        return found[0]
+    return get
+
+
+# The calls of small operators are bound by their host side, so these look their C function up once, pass plain
+# addresses and take the raw stream handle.
 
 def _gemm_epilogue(name):
+    plain, ex = _entry(name), _entry(name + "_ex")
+
     def call(M, N, K, A, lda, la, B, ldb, lb, D, ldd, d_type, epilogue, stream=None):
-        return getattr(lib(), name)(M, N, K, _ptr(A), lda, la, _ptr(B), ldb, lb, _ptr(D), ldd, d_type, _epi(epilogue),
-                                    _stream(stream))
+        return plain()(M, N, K, _address(A), lda, la, _address(B), ldb, lb, _address(D), ldd, d_type, _epi(epilogue),
+                       _raw_stream(stream))
 
     def call_ex(M, N, K, A, lda, la, B, ldb, lb, D, ldd, d_type, epilogue, tune=None, workspace=None,
                 workspace_bytes=None, stream=None):
         wsb = workspace_bytes if workspace_bytes is not None else _nbytes(workspace)
-        return getattr(lib(), name + "_ex")(M, N, K, _ptr(A), lda, la, _ptr(B), ldb, lb, _ptr(D), ldd, d_type,
-                                            _epi(epilogue), _tune(tune), _ptr(workspace), wsb, _stream(stream))
+        return ex()(M, N, K, _address(A), lda, la, _address(B), ldb, lb, _address(D), ldd, d_type, _epi(epilogue),
+                    _tune(tune), _address(workspace), wsb, _raw_stream(stream))
     call.__name__, call_ex.__name__ = name, name + "_ex"
     return call, call_ex
 
 
 def _conv_epilogue(name):
+    plain, ex = _entry(name), _entry(name + "_ex")
+
     def call(N, H, W, C, K, R, S, stride_h, stride_w, pad_h, pad_w, dil_h, dil_w, x, w, y, y_type, epilogue,
              stream=None):
-        return getattr(lib(), name)(N, H, W, C, K, R, S, stride_h, stride_w, pad_h, pad_w, dil_h, dil_w, _ptr(x),
-                                    _ptr(w), _ptr(y), y_type, _epi(epilogue), _stream(stream))
+        return plain()(N, H, W, C, K, R, S, stride_h, stride_w, pad_h, pad_w, dil_h, dil_w, _address(x), _address(w),
+                       _address(y), y_type, _epi(epilogue), _raw_stream(stream))
 
     def call_ex(N, H, W, C, K, R, S, stride_h, stride_w, pad_h, pad_w, dil_h, dil_w, x, w, y, y_type, epilogue,
                 tune=None, workspace=None, workspace_bytes=None, stream=None):
         wsb = workspace_bytes if workspace_bytes is not None else _nbytes(workspace)
-        return getattr(lib(), name + "_ex")(N, H, W, C, K, R, S, stride_h, stride_w, pad_h, pad_w, dil_h, dil_w,
-                                            _ptr(x), _ptr(w), _ptr(y), y_type, _epi(epilogue), _tune(tune),
-                                            _ptr(workspace), wsb, _stream(stream))
+        return ex()(N, H, W, C, K, R, S, stride_h, stride_w, pad_h, pad_w, dil_h, dil_w, _address(x), _address(w),
+                    _address(y), y_type, _epi(epilogue), _tune(tune), _address(workspace), wsb, _raw_stream(stream))
     call.__name__, call_ex.__name__ = name, name + "_ex"
     return call, call_ex
 
 
 def _epilogue_backward(name):
+    plain, ex = _entry(name), _entry(name + "_ex")
+
     def call(M, N, act, dD, ldd, pre, ldp, dz, ldz, dbias, dbias_type, stream=None):
-        return getattr(lib(), name)(M, N, act_code(act), _ptr(dD), ldd, _ptr(pre), ldp, _ptr(dz), ldz, _ptr(dbias),
-                                    dbias_type, _stream(stream))
+        return plain()(M, N, act_code(act), _address(dD), ldd, _address(pre), ldp, _address(dz), ldz, _address(dbias),
+                       dbias_type, _raw_stream(stream))
 
     def call_ex(M, N, act, dD, ldd, pre, ldp, dz, ldz, dbias, dbias_type, workspace=None, workspace_bytes=None,
                 stream=None):
         wsb = workspace_bytes if workspace_bytes is not None else _nbytes(workspace)
-        return getattr(lib(), name + "_ex")(M, N, act_code(act), _ptr(dD), ldd, _ptr(pre), ldp, _ptr(dz), ldz,
-                                            _ptr(dbias), dbias_type, _ptr(workspace), wsb, _stream(stream))
+        return ex()(M, N, act_code(act), _address(dD), ldd, _address(pre), ldp, _address(dz), ldz, _address(dbias),
+                    dbias_type, _address(workspace), wsb, _raw_stream(stream))
     call.__name__, call_ex.__name__ = name, name + "_ex"
     return call, call_ex
 
 
 def _group_norm(name):
+    plain, ex = _entry(name), _entry(name + "_ex")
+
     def call(N, H, W, C, G, x, ldx, gamma, beta, param_type, eps, act, y, ldy, mean=None, rstd=None, stream=None):
-        return getattr(lib(), name)(N, H, W, C, G, _ptr(x), ldx, _ptr(gamma), _ptr(beta), param_type, eps,
-                                    act_code(act), _ptr(y), ldy, _ptr(mean), _ptr(rstd), _stream(stream))
+        return plain()(N, H, W, C, G, _address(x), ldx, _address(gamma), _address(beta), param_type, eps,
+                       act_code(act), _address(y), ldy, _address(mean), _address(rstd), _raw_stream(stream))
 
     def call_ex(N, H, W, C, G, x, ldx, gamma, beta, param_type, eps, act, y, ldy, mean=None, rstd=None,
                 workspace=None, workspace_bytes=None, stream=None):
         wsb = workspace_bytes if workspace_bytes is not None else _nbytes(workspace)
-        return getattr(lib(), name + "_ex")(N, H, W, C, G, _ptr(x), ldx, _ptr(gamma), _ptr(beta), param_type, eps,
-                                            act_code(act), _ptr(y), ldy, _ptr(mean), _ptr(rstd), _ptr(workspace), wsb,
-                                            _stream(stream))
+        return ex()(N, H, W, C, G, _address(x), ldx, _address(gamma), _address(beta), param_type, eps, act_code(act),
+                    _address(y), ldy, _address(mean), _address(rstd), _address(workspace), wsb, _raw_stream(stream))
     call.__name__, call_ex.__name__ = name, name + "_ex"
     return call, call_ex
 
 
 def _group_norm_backward(name):
+    plain, ex = _entry(name), _entry(name + "_ex")
+
     def call(N, H, W, C, G, x, ldx, gamma, beta, param_type, mean, rstd, act, dy, lddy, dx, lddx, dgamma=None,
              dbeta=None, stream=None):
-        return getattr(lib(), name)(N, H, W, C, G, _ptr(x), ldx, _ptr(gamma), _ptr(beta), param_type, _ptr(mean),
-                                    _ptr(rstd), act_code(act), _ptr(dy), lddy, _ptr(dx), lddx, _ptr(dgamma),
-                                    _ptr(dbeta), _stream(stream))
+        return plain()(N, H, W, C, G, _address(x), ldx, _address(gamma), _address(beta), param_type, _address(mean),
+                       _address(rstd), act_code(act), _address(dy), lddy, _address(dx), lddx, _address(dgamma),
+                       _address(dbeta), _raw_stream(stream))
 
     def call_ex(N, H, W, C, G, x, ldx, gamma, beta, param_type, mean, rstd, act, dy, lddy, dx, lddx, dgamma=None,
                 dbeta=None, workspace=None, workspace_bytes=None, stream=None):
         wsb = workspace_bytes if workspace_bytes is not None else _nbytes(workspace)
-        return getattr(lib(), name + "_ex")(N, H, W, C, G, _ptr(x), ldx, _ptr(gamma), _ptr(beta), param_type,
-                                            _ptr(mean), _ptr(rstd), act_code(act), _ptr(dy), lddy, _ptr(dx), lddx,
-                                            _ptr(dgamma), _ptr(dbeta), _ptr(workspace), wsb, _stream(stream))
+        return ex()(N, H, W, C, G, _address(x), ldx, _address(gamma), _address(beta), param_type, _address(mean),
+                    _address(rstd), act_code(act), _address(dy), lddy, _address(dx), lddx, _address(dgamma),
+                    _address(dbeta), _address(workspace), wsb, _raw_stream(stream))
     call.__name__, call_ex.__name__ = name, name + "_ex"
     return call, call_ex
 

@@ -36,11 +36,13 @@ struct GnArgs {
     float *mean, *rstd;    // N x G
     float* part;           // N x chunks x C pairs: (mean, M2), or (sum dz, sum dz xh)
     float* joined;         // backward: N x G pairs (mean of gamma dz, mean of gamma dz xh)
+    float* sums;           // backward: N x C pairs (sum dz, sum dz xh)
     void *dgamma, *dbeta;  // nullptr: not wanted
     int64_t ldx, lddy, ldo;
     int64_t HW;
     int N, C, G, cpg, param_kind, act;
     int chunks, pixels;    // chunks of an image and pixels per chunk
+    int grid;              // workgroups over the images
     int sv, pl, slabs;     // vectors (8 channels) a workgroup covers, its pixel lanes, slabs of an image's channels
     float eps;
 };
@@ -274,56 +276,86 @@ __global__ __launch_bounds__(kGnThreads) void gn_backward_partial_kernel(const G
     }
 }
 
-// The first N*G workgroups: a group's two means.  The others: 32 channels'
-// dgamma and dbeta each, summed over the images' chunks by 8 lanes a channel.
+// One group of one image: its channels' sums over the chunks (kept for dgamma
+// and dbeta) and its two means.  Lanes run over channels first, then chunks.
 __global__ __launch_bounds__(256) void gn_backward_finish_kernel(const GnArgs a) {
-    __shared__ float red[2 * 8 * 32];
-    const int groups = a.N * a.G;
-    if ((int)blockIdx.x < groups) {
-        const int n = (int)blockIdx.x / a.G, g = (int)blockIdx.x % a.G;
-        const float* part = a.part + ((int64_t)n * a.chunks * a.C + (int64_t)g * a.cpg) * 2;
-        const int items = a.chunks * a.cpg;
+    __shared__ float red[2 * 256];
+    const int n = (int)blockIdx.x / a.G, g = (int)blockIdx.x % a.G;
+    int cw = 1;
+    while (cw < a.cpg && cw < 256) cw *= 2;
+    const int lanes = 256 / cw, cl = (int)threadIdx.x % cw, kl = (int)threadIdx.x / cw;
+    const float* part = a.part + ((int64_t)n * a.chunks * a.C + (int64_t)g * a.cpg) * 2;
+    float m1 = 0.0f, m2 = 0.0f;
+    for (int c0 = 0; c0 < a.cpg; c0 += cw) {
+        const int c = c0 + cl;
         float t1 = 0.0f, t2 = 0.0f;
-        for (int i = (int)threadIdx.x; i < items; i += 256) {
-            const int k = i / a.cpg, c = i - k * a.cpg;
-            const float ga = a.gamma ? load_kind(a.gamma, (int64_t)g * a.cpg + c, a.param_kind) : 1.0f;
-            t1 = __builtin_fmaf(ga, part[((int64_t)k * a.C + c) * 2], t1);
-            t2 = __builtin_fmaf(ga, part[((int64_t)k * a.C + c) * 2 + 1], t2);
+        if (c < a.cpg)
+            for (int k = kl; k < a.chunks; k += lanes) {
+                t1 += part[((int64_t)k * a.C + c) * 2];
+                t2 += part[((int64_t)k * a.C + c) * 2 + 1];
+            }
+        __syncthreads();
+        red[threadIdx.x] = t1;
+        red[256 + threadIdx.x] = t2;
+        __syncthreads();
+        if (kl == 0 && c < a.cpg) {
+            for (int l = 1; l < lanes; ++l) {
+                t1 += red[l * cw + cl];
+                t2 += red[256 + l * cw + cl];
+            }
+            const int64_t ch = (int64_t)g * a.cpg + c;
+            float* dst = a.sums + ((int64_t)n * a.C + ch) * 2;
+            dst[0] = t1;
+            dst[1] = t2;
+            const float ga = a.gamma ? load_kind(a.gamma, ch, a.param_kind) : 1.0f;
+            m1 = __builtin_fmaf(ga, t1, m1);
+            m2 = __builtin_fmaf(ga, t2, m2);
         }
-        const float total = (float)a.HW * (float)a.cpg;
-        t1 = block_sum(t1, red) / total;
-        t2 = block_sum(t2, red) / total;
-        if (threadIdx.x == 0) {
-            a.joined[blockIdx.x * 2] = t1;
-            a.joined[blockIdx.x * 2 + 1] = t2;
-        }
-        return;
     }
-    const int c = ((int)blockIdx.x - groups) * 32 + ((int)threadIdx.x & 31), l = (int)threadIdx.x >> 5;
+    __syncthreads();
+    const float total = (float)a.HW * (float)a.cpg;
+    m1 = block_sum(m1, red) / total;
+    m2 = block_sum(m2, red) / total;
+    if (threadIdx.x == 0) {
+        a.joined[blockIdx.x * 2] = m1;
+        a.joined[blockIdx.x * 2 + 1] = m2;
+    }
+}
+
+// dgamma and dbeta of 32 channels: the images' sums, added in order by 8 lanes a channel.
+__device__ __forceinline__ void gn_param_sums(const GnArgs& a, int block, int threads, float* red) {
+    const int t = (int)threadIdx.x, lanes = threads / 32;
+    const int c = block * 32 + (t & 31), l = t >> 5;
     float t1 = 0.0f, t2 = 0.0f;
-    if (c < a.C) {
-        const int64_t items = (int64_t)a.N * a.chunks;
-        for (int64_t i = l; i < items; i += 8) {
-            t1 += a.part[(i * a.C + c) * 2];
-            t2 += a.part[(i * a.C + c) * 2 + 1];
+    if (c < a.C)
+        for (int n = l; n < a.N; n += lanes) {
+            t1 += a.sums[((int64_t)n * a.C + c) * 2];
+            t2 += a.sums[((int64_t)n * a.C + c) * 2 + 1];
         }
-    }
-    red[threadIdx.x] = t1;
-    red[256 + threadIdx.x] = t2;
+    red[t] = t1;
+    red[threads + t] = t2;
     __syncthreads();
     if (l == 0 && c < a.C) {
-#pragma unroll
-        for (int k = 1; k < 8; ++k) {
-            t1 += red[k * 32 + threadIdx.x];
-            t2 += red[256 + k * 32 + threadIdx.x];
+        for (int k = 1; k < lanes; ++k) {
+            t1 += red[k * 32 + t];
+            t2 += red[threads + k * 32 + t];
         }
         if (a.dbeta) store_kind(a.dbeta, c, a.param_kind, t1);
         if (a.dgamma) store_kind(a.dgamma, c, a.param_kind, t2);
     }
 }
+__global__ __launch_bounds__(256) void gn_param_kernel(const GnArgs a) {
+    __shared__ float red[2 * 256];
+    gn_param_sums(a, (int)blockIdx.x, 256, red);
+}
 
 template <bool FP16>
 __global__ __launch_bounds__(kGnThreads) void gn_backward_apply_kernel(const GnArgs a) {
+    if ((int)blockIdx.x >= a.grid) {  // the workgroups past the images': dgamma and dbeta
+        __shared__ float red[2 * kGnThreads];
+        gn_param_sums(a, (int)blockIdx.x - a.grid, (int)blockDim.x, red);
+        return;
+    }
     const GnSpot s(a);
     if (!s.on) return;
     const GnChannels k(a, s.n, s.c);
@@ -366,15 +398,322 @@ __global__ __launch_bounds__(kGnThreads) void gn_backward_apply_kernel(const GnA
     });
 }
 
+// ---- images held on chip ----------------------------------------------------
+// Where a workgroup's registers hold all of an image's pixels for a slab of
+// whole groups, one kernel reads x once, reduces, and writes y: 4 bytes a value
+// and one launch.  A thread keeps NV vectors; sums of a group go through LDS in
+// a fixed order.  The mean comes first and then the squared deviations from it,
+// from the registers, so the variance needs no shift.
+__device__ __forceinline__ void one_at_a_time() { __builtin_amdgcn_sched_barrier(0); }  // one vector unpacked at once
+
+// The packed values are what stays in registers from one phase to the next:
+// without this the compiler keeps their unpacked form, twice the size.
+template <int NV>
+__device__ __forceinline__ void keep_packed(u32x4s_t (&x)[NV]) {
+#pragma unroll
+    for (int k = 0; k < NV; ++k) asm volatile("" : "+v"(x[k]));
+}
+
+struct GnSlab {
+    int n, v, p, c, sv;  // image, vector, pixel lane, first channel, vectors of this slab
+    int groups, g0;      // of this slab, and the first
+    bool on;
+    __device__ __forceinline__ explicit GnSlab(const GnArgs& a) {
+        const int id = xcd_order((int)blockIdx.x, a.grid);  // an image's slabs share lines: keep them on one XCD
+        n = id / a.slabs;
+        const int slab = id - n * a.slabs;
+        sv = a.C / 8 - slab * a.sv < a.sv ? a.C / 8 - slab * a.sv : a.sv;
+        v = (int)threadIdx.x % a.sv;
+        p = (int)threadIdx.x / a.sv;
+        c = (slab * a.sv + v) * 8;
+        groups = sv * 8 / a.cpg;
+        g0 = slab * a.sv * 8 / a.cpg;
+        on = p < a.pl && v < sv;
+    }
+};
+
+// Sums over the slab's groups: `w` values a thread (one, all its channels being
+// of one group, or its eight channels apart), to out[group].  `red` holds
+// threads * w floats.  Every thread calls it.
+template <int W>
+__device__ __forceinline__ void group_sums(const GnArgs& a, const GnSlab& s, const float (&val)[W], float* red,
+                                           float* out) {
+    __syncthreads();  // `red` and `out` of an earlier call have been read
+#pragma unroll
+    for (int i = 0; i < W; ++i) red[threadIdx.x * W + i] = s.on ? val[i] : 0.0f;
+    __syncthreads();
+    const int lane = (int)threadIdx.x & 63, waves = (int)(blockDim.x >> 6);
+    const int per = W == 1 ? a.cpg / 8 : a.cpg;  // entries of a group in one pixel lane
+    for (int g = (int)(threadIdx.x >> 6); g < s.groups; g += waves) {
+        float t = 0.0f;
+        for (int e = 0; e < per; ++e)
+            for (int p = lane; p < a.pl; p += 64) t += red[p * a.sv * W + g * per + e];
+#pragma unroll
+        for (int d = 32; d >= 1; d >>= 1) t += __shfl_xor(t, d);
+        if (lane == 0) out[g] = t;
+    }
+    __syncthreads();
+}
+
+constexpr int kGnMaxThreads = 1024, kGnMaxVecs = 256;  // of a workgroup of the resident kernels
+
+template <bool FP16, int NV, bool SINGLE>
+__global__ __launch_bounds__(kGnMaxThreads) void gn_resident_kernel(const GnArgs a) {
+    constexpr int W = SINGLE ? 1 : 8;
+    __shared__ float red[kGnMaxThreads * W];
+    __shared__ float sums[kGnMaxVecs * W];  // by group of the slab
+    const GnSlab s(a);
+    const char* img = (const char*)a.x + ((int64_t)s.n * a.HW * a.ldx + s.c) * 2;
+    u32x4s_t x[NV];
+#pragma unroll
+    for (int k = 0; k < NV; ++k) {
+        const int p = s.p + k * a.pl;
+        x[k] = u32x4s_t{0, 0, 0, 0};
+        if (s.on && p < a.HW) x[k] = *(const u32x4s_t*)(img + p * a.ldx * 2);
+    }
+    float ga[8], be[8];
+    int gi[W];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        ga[i] = s.on && a.gamma ? load_kind(a.gamma, s.c + i, a.param_kind) : 1.0f;
+        be[i] = s.on && a.beta ? load_kind(a.beta, s.c + i, a.param_kind) : 0.0f;
+    }
+#pragma unroll
+    for (int i = 0; i < W; ++i) gi[i] = s.on ? (s.c + i) / a.cpg - s.g0 : 0;
+    const float rn = 1.0f / ((float)a.HW * (float)a.cpg);
+    float acc[W], mu[W], rs[W];
+#pragma unroll
+    for (int i = 0; i < W; ++i) acc[i] = 0.0f;
+#pragma unroll
+    for (int k = 0; k < NV; ++k) {  // absent pixels are zeros
+        float v[8];
+        unpack8<FP16>(x[k], v);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) acc[i % W] += v[i];
+        one_at_a_time();
+    }
+    group_sums<W>(a, s, acc, red, sums);
+    keep_packed(x);
+#pragma unroll
+    for (int i = 0; i < W; ++i) {
+        mu[i] = sums[gi[i]] * rn;
+        acc[i] = 0.0f;
+    }
+#pragma unroll
+    for (int k = 0; k < NV; ++k) {
+        if (s.p + k * a.pl >= a.HW) break;
+        float v[8];
+        unpack8<FP16>(x[k], v);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const float d = v[i] - mu[i % W];
+            acc[i % W] = __builtin_fmaf(d, d, acc[i % W]);
+        }
+        one_at_a_time();
+    }
+    group_sums<W>(a, s, acc, red, sums);
+    keep_packed(x);
+#pragma unroll
+    for (int i = 0; i < W; ++i) rs[i] = 1.0f / __builtin_sqrtf(sums[gi[i]] * rn + a.eps);
+    if (s.on && s.p == 0 && a.mean) {
+#pragma unroll
+        for (int i = 0; i < W; ++i)
+            if ((s.c + i) % a.cpg == 0) a.mean[s.n * a.G + s.g0 + gi[i]] = mu[i];
+    }
+    if (s.on && s.p == 0 && a.rstd) {
+#pragma unroll
+        for (int i = 0; i < W; ++i)
+            if ((s.c + i) % a.cpg == 0) a.rstd[s.n * a.G + s.g0 + gi[i]] = rs[i];
+    }
+    if (!s.on) return;
+    char* out = (char*)a.out + ((int64_t)s.n * a.HW * a.ldo + s.c) * 2;
+    with_act(a.act, [&](auto A) __attribute__((always_inline)) {
+        constexpr int ACT = decltype(A)::value;
+#pragma unroll
+        for (int k = 0; k < NV; ++k) {
+            const int p = s.p + k * a.pl;
+            if (p >= a.HW) break;
+            float v[8];
+            unpack8<FP16>(x[k], v);
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                v[i] = act_of<ACT>(__builtin_fmaf((v[i] - mu[i % W]) * rs[i % W], ga[i], be[i]));
+            *(u32x4s_t*)(out + p * a.ldo * 2) = pack8<FP16>(v);
+            one_at_a_time();
+        }
+    });
+}
+
+// The gradient of the same: x and dy once in, dx once out.  The sums of each
+// channel go to `sums` for dgamma and dbeta, a group's to its two means.
+template <bool FP16, int NV, bool SINGLE>
+__global__ __launch_bounds__(kGnMaxThreads) void gn_backward_resident_kernel(const GnArgs a) {
+    constexpr int W = SINGLE ? 1 : 8;
+    __shared__ float red[kGnMaxThreads * 8];
+    __shared__ float chan[2 * 8 * kGnMaxVecs];  // the slab's channels, both sums
+    const GnSlab s(a);
+    const char* img = (const char*)a.x + ((int64_t)s.n * a.HW * a.ldx + s.c) * 2;
+    const char* grad = (const char*)a.dy + ((int64_t)s.n * a.HW * a.lddy + s.c) * 2;
+    u32x4s_t x[NV], d[NV];
+#pragma unroll
+    for (int k = 0; k < NV; ++k) {
+        const int p = s.p + k * a.pl;
+        x[k] = d[k] = u32x4s_t{0, 0, 0, 0};
+        if (s.on && p < a.HW) {
+            x[k] = *(const u32x4s_t*)(img + p * a.ldx * 2);
+            d[k] = *(const u32x4s_t*)(grad + p * a.lddy * 2);
+        }
+    }
+    float mu[W], rs[W], ga[8], be[8], s1[8], s2[8];
+#pragma unroll
+    for (int i = 0; i < W; ++i) {
+        const int g = s.on ? s.n * a.G + (s.c + i) / a.cpg : 0;
+        mu[i] = a.mean[g];
+        rs[i] = a.rstd[g];
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        ga[i] = s.on && a.gamma ? load_kind(a.gamma, s.c + i, a.param_kind) : 1.0f;
+        be[i] = s.on && a.beta ? load_kind(a.beta, s.c + i, a.param_kind) : 0.0f;
+        s1[i] = s2[i] = 0.0f;
+    }
+    with_act(a.act, [&](auto A) __attribute__((always_inline)) {
+        constexpr int ACT = decltype(A)::value;
+#pragma unroll
+        for (int k = 0; k < NV; ++k) {
+            if (s.p + k * a.pl >= a.HW) break;
+            float v[8], e[8];
+            unpack8<FP16>(x[k], v);
+            unpack8<FP16>(d[k], e);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const float xh = (v[i] - mu[i % W]) * rs[i % W];
+                const float dz = e[i] * act_grad_of<ACT>(__builtin_fmaf(xh, ga[i], be[i]));
+                s1[i] += dz;
+                s2[i] = __builtin_fmaf(dz, xh, s2[i]);
+            }
+            one_at_a_time();
+        }
+    });
+    const int lane = (int)threadIdx.x & 63, waves = (int)(blockDim.x >> 6), nch = s.sv * 8;
+    for (int turn = 0; turn < 2; ++turn) {
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < 8; ++i) red[threadIdx.x * 8 + i] = s.on ? (turn ? s2[i] : s1[i]) : 0.0f;
+        __syncthreads();
+        if (a.pl >= 64) {  // a wave a channel
+            for (int c = (int)(threadIdx.x >> 6); c < nch; c += waves) {
+                float t = 0.0f;
+                for (int p = lane; p < a.pl; p += 64) t += red[p * a.sv * 8 + c];
+#pragma unroll
+                for (int m = 32; m >= 1; m >>= 1) t += __shfl_xor(t, m);
+                if (lane == 0) chan[2 * c + turn] = t;
+            }
+        } else {  // a thread a channel
+            for (int c = (int)threadIdx.x; c < nch; c += (int)blockDim.x) {
+                float t = 0.0f;
+                for (int p = 0; p < a.pl; ++p) t += red[p * a.sv * 8 + c];
+                chan[2 * c + turn] = t;
+            }
+        }
+    }
+    __syncthreads();
+    const int c0 = s.g0 * a.cpg;  // the slab's first channel
+    if (a.dgamma || a.dbeta)
+        for (int i = (int)threadIdx.x; i < 2 * nch; i += (int)blockDim.x)
+            a.sums[((int64_t)s.n * a.C + c0) * 2 + i] = chan[i];
+    // a wave a group: its two means, into `red`
+    const float rn = 1.0f / ((float)a.HW * (float)a.cpg);
+    for (int g = (int)(threadIdx.x >> 6); g < s.groups; g += waves) {
+        float t1 = 0.0f, t2 = 0.0f;
+        for (int c = g * a.cpg + lane; c < (g + 1) * a.cpg; c += 64) {
+            const float w = a.gamma ? load_kind(a.gamma, c0 + c, a.param_kind) : 1.0f;
+            t1 = __builtin_fmaf(w, chan[2 * c], t1);
+            t2 = __builtin_fmaf(w, chan[2 * c + 1], t2);
+        }
+#pragma unroll
+        for (int m = 32; m >= 1; m >>= 1) {
+            t1 += __shfl_xor(t1, m);
+            t2 += __shfl_xor(t2, m);
+        }
+        if (lane == 0) {
+            red[2 * g] = t1 * rn;
+            red[2 * g + 1] = t2 * rn;
+        }
+    }
+    __syncthreads();
+    if (!s.on) return;
+    keep_packed(x);
+    keep_packed(d);
+    float c1[W], c2[W];
+#pragma unroll
+    for (int i = 0; i < W; ++i) {
+        const int g = (s.c + i) / a.cpg - s.g0;
+        c1[i] = red[2 * g];
+        c2[i] = red[2 * g + 1];
+    }
+    char* out = (char*)a.out + ((int64_t)s.n * a.HW * a.ldo + s.c) * 2;
+    with_act(a.act, [&](auto A) __attribute__((always_inline)) {
+        constexpr int ACT = decltype(A)::value;
+#pragma unroll
+        for (int k = 0; k < NV; ++k) {
+            const int p = s.p + k * a.pl;
+            if (p >= a.HW) break;
+            float v[8], e[8];
+            unpack8<FP16>(x[k], v);
+            unpack8<FP16>(d[k], e);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const float xh = (v[i] - mu[i % W]) * rs[i % W];
+                const float dz = e[i] * act_grad_of<ACT>(__builtin_fmaf(xh, ga[i], be[i]));
+                v[i] = rs[i % W] * (__builtin_fmaf(ga[i], dz, -c1[i % W]) - xh * c2[i % W]);
+            }
+            *(u32x4s_t*)(out + p * a.ldo * 2) = pack8<FP16>(v);
+            one_at_a_time();
+        }
+    });
+}
+
 // ---- host -----------------------------------------------------------------
 
 struct GnPlan {
+    int nv;  // resident: vectors a thread holds; 0: chunks
     int sv, pl, slabs, threads, chunks, pixels;
-    int64_t part_bytes, stat_bytes, bytes;
+    int64_t part_bytes, stat_bytes, sum_bytes, bytes;
 };
 
-static GnPlan gn_plan(int64_t N, int64_t HW, int64_t C, int64_t G) {
+// The on-chip form: a slab of sv vectors (whole groups) of an image in one
+// workgroup of up to 1024 threads, `most` vectors a thread at most.
+static bool resident_plan(GnPlan& p, int64_t N, int64_t HW, int64_t C, int64_t G, int most) {
+    const int64_t vecs = C / 8, cpg = C / G;
+    int64_t base = cpg;  // lcm(cpg, 8) / 8 vectors: the narrowest slab of whole vectors and groups
+    while (base % 8 != 0) base *= 2;
+    base /= 8;
+    auto fits = [&](int64_t sv) { return sv <= kGnMaxVecs && sv <= vecs && HW <= most * (kGnMaxThreads / sv); };
+    if (!fits(base)) return false;
+    int64_t sv = base;
+    auto slabs = [&](int64_t v) { return N * ((vecs + v - 1) / v); };
+    // wider slabs read and write longer pieces of a pixel (up to the 128-byte line), while every CU keeps one
+    while (sv < 8 && fits(2 * sv) && slabs(2 * sv) >= 256) sv *= 2;
+    p.sv = (int)sv;
+    p.slabs = (int)((vecs + sv - 1) / sv);
+    int64_t threads = (HW * sv + 63) / 64 * 64;
+    p.threads = (int)(threads < kGnMaxThreads ? threads : kGnMaxThreads);
+    p.pl = (int)(p.threads / sv);
+    if (p.pl > HW) p.pl = (int)HW;
+    p.nv = 1;
+    while (p.nv * (int64_t)p.pl < HW) p.nv *= 2;
+    return p.nv <= most;
+}
+
+static GnPlan gn_plan(int64_t N, int64_t HW, int64_t C, int64_t G, int most) {
     GnPlan p{};
+    if (resident_plan(p, N, HW, C, G, most)) {
+        p.sum_bytes = round_up(N * C * 8, 256);
+        p.bytes = p.sum_bytes;
+        return p;
+    }
+    p = GnPlan{};
     const int64_t vecs = C / 8;
     p.sv = (int)(vecs < kGnThreads ? vecs : kGnThreads);
     p.slabs = (int)((vecs + p.sv - 1) / p.sv);
@@ -383,16 +722,20 @@ static GnPlan gn_plan(int64_t N, int64_t HW, int64_t C, int64_t G) {
     p.threads = (p.pl * p.sv + 63) / 64 * 64;
     // about eight workgroups a CU, each with at least four pixels a lane
     int64_t chunks = N > 0 ? (2048 + N * p.slabs - 1) / (N * p.slabs) : 1;
-    const int64_t most = (HW + 4 * p.pl - 1) / (4 * p.pl);
-    if (chunks > most) chunks = most;
+    const int64_t top = (HW + 4 * p.pl - 1) / (4 * p.pl);
+    if (chunks > top) chunks = top;
     if (chunks < 1) chunks = 1;
     p.pixels = (int)((HW + chunks - 1) / chunks);
     p.chunks = (int)((HW + p.pixels - 1) / p.pixels);
     p.part_bytes = round_up(N * p.chunks * C * 8, 256);
     p.stat_bytes = round_up(N * G * 8, 256);  // mean and rstd, or the two means of the backward pass
-    p.bytes = p.part_bytes + p.stat_bytes;
+    p.sum_bytes = round_up(N * C * 8, 256);
+    p.bytes = p.part_bytes + p.stat_bytes + p.sum_bytes;
     return p;
 }
+
+// Most vectors a thread of the resident kernels holds (of each tensor): what 128 registers leave room for.
+constexpr int kGnMostForward = 16, kGnMostBackward = 8;
 
 // What every entry point checks of an image tensor; 0 pixels never come here.
 static igc_status_t check_image(const void* ptr, int64_t ld, int64_t C) {
@@ -409,6 +752,28 @@ static igc_status_t check_shape(int N, int H, int W, int C, int G, igc_out_t pt,
 }
 static bool aligned_params(const void* p, igc_out_t t) { return reinterpret_cast<uintptr_t>(p) % out_size(t) == 0; }
 
+template <bool FP16, bool SINGLE>
+static void launch_resident(const GnArgs& a, const GnPlan& pl, hipStream_t stream) {
+    const dim3 grid((unsigned)a.grid), block(pl.threads);
+    switch (pl.nv) {
+        case 1: hipLaunchKernelGGL((gn_resident_kernel<FP16, 1, SINGLE>), grid, block, 0, stream, a); break;
+        case 2: hipLaunchKernelGGL((gn_resident_kernel<FP16, 2, SINGLE>), grid, block, 0, stream, a); break;
+        case 4: hipLaunchKernelGGL((gn_resident_kernel<FP16, 4, SINGLE>), grid, block, 0, stream, a); break;
+        case 8: hipLaunchKernelGGL((gn_resident_kernel<FP16, 8, SINGLE>), grid, block, 0, stream, a); break;
+        default: hipLaunchKernelGGL((gn_resident_kernel<FP16, 16, SINGLE>), grid, block, 0, stream, a); break;
+    }
+}
+template <bool FP16, bool SINGLE>
+static void launch_backward_resident(const GnArgs& a, const GnPlan& pl, hipStream_t stream) {
+    const dim3 grid((unsigned)a.grid), block(pl.threads);
+    switch (pl.nv) {
+        case 1: hipLaunchKernelGGL((gn_backward_resident_kernel<FP16, 1, SINGLE>), grid, block, 0, stream, a); break;
+        case 2: hipLaunchKernelGGL((gn_backward_resident_kernel<FP16, 2, SINGLE>), grid, block, 0, stream, a); break;
+        case 4: hipLaunchKernelGGL((gn_backward_resident_kernel<FP16, 4, SINGLE>), grid, block, 0, stream, a); break;
+        default: hipLaunchKernelGGL((gn_backward_resident_kernel<FP16, 8, SINGLE>), grid, block, 0, stream, a); break;
+    }
+}
+
 static GnArgs gn_args(const GnPlan& pl, int N, int64_t HW, int C, int G, const void* gamma, const void* beta,
                       igc_out_t pt, igc_act_t act, const Workspace& ws) {
     GnArgs a{};
@@ -424,6 +789,7 @@ static GnArgs gn_args(const GnPlan& pl, int N, int64_t HW, int C, int G, const v
     a.act = (int)act;
     a.chunks = pl.chunks;
     a.pixels = pl.pixels;
+    a.grid = (int)((int64_t)N * (pl.nv ? 1 : pl.chunks) * pl.slabs);
     a.sv = pl.sv;
     a.pl = pl.pl;
     a.slabs = pl.slabs;
@@ -443,24 +809,34 @@ static igc_status_t gn_forward(int N, int H, int W, int C, int G, const void* x,
         !aligned_params(rstd, IGC_OUT_F32))
         return IGC_ERR_MISALIGNED;
     const int64_t HW = (int64_t)H * W;
-    const GnPlan pl = gn_plan(N, HW, C, G);
-    const int64_t grid = (int64_t)N * pl.chunks * pl.slabs;
-    if (grid > 0x7fffffff) return IGC_ERR_UNSUPPORTED;
+    const GnPlan pl = gn_plan(N, HW, C, G, kGnMostForward);
+    if ((int64_t)N * (pl.nv ? 1 : pl.chunks) * pl.slabs > 0x7fffffff) return IGC_ERR_UNSUPPORTED;
     Workspace ws;
-    if (const igc_status_t st = ws.take(pl.bytes, user_ws, user_ws_bytes, stream)) return st;
+    if (const igc_status_t st = ws.take(pl.nv ? 0 : pl.bytes, user_ws, user_ws_bytes, stream)) return st;
     (void)hipGetLastError();
     GnArgs a = gn_args(pl, N, HW, C, G, gamma, beta, pt, act, ws);
-    float* stats = (float*)((char*)ws.ptr + pl.part_bytes);
     a.x = x;
     a.out = y;
     a.ldx = ldx;
     a.ldo = ldy;
+    if (pl.nv) {
+        a.mean = mean;
+        a.rstd = rstd;
+        a.eps = eps;
+        if (a.cpg % 8 == 0)
+            launch_resident<FP16, true>(a, pl, stream);
+        else
+            launch_resident<FP16, false>(a, pl, stream);
+        return hipGetLastError() == hipSuccess ? IGC_OK : IGC_ERR_HIP;
+    }
+    float* stats = (float*)((char*)ws.ptr + pl.part_bytes);
+    const unsigned grid = (unsigned)a.grid;
     a.mean = mean ? mean : stats;
     a.rstd = rstd ? rstd : stats + (int64_t)N * G;
     a.eps = eps;
-    hipLaunchKernelGGL(gn_partial_kernel<FP16>, dim3((unsigned)grid), dim3(pl.threads), 0, stream, a);
+    hipLaunchKernelGGL(gn_partial_kernel<FP16>, dim3(grid), dim3(pl.threads), 0, stream, a);
     hipLaunchKernelGGL(gn_finish_kernel, dim3((unsigned)(N * G)), dim3(256), 0, stream, a);
-    hipLaunchKernelGGL(gn_apply_kernel<FP16>, dim3((unsigned)grid), dim3(pl.threads), 0, stream, a);
+    hipLaunchKernelGGL(gn_apply_kernel<FP16>, dim3(grid), dim3(pl.threads), 0, stream, a);
     return hipGetLastError() == hipSuccess ? IGC_OK : IGC_ERR_HIP;
 }
 
@@ -481,9 +857,8 @@ static igc_status_t gn_backward(int N, int H, int W, int C, int G, const void* x
         if (!mean || !rstd) return IGC_ERR_INVALID_VALUE;
     }
     const int64_t HW = (int64_t)H * W;
-    const GnPlan pl = gn_plan(N, HW, C, G);
-    const int64_t grid = (int64_t)N * pl.chunks * pl.slabs;
-    if (grid > 0x7fffffff) return IGC_ERR_UNSUPPORTED;
+    const GnPlan pl = gn_plan(N, HW, C, G, kGnMostBackward);
+    if ((int64_t)N * (pl.nv ? 1 : pl.chunks) * pl.slabs > 0x7fffffff - (C + 31) / 32) return IGC_ERR_UNSUPPORTED;
     Workspace ws;
     if (const igc_status_t st = ws.take(N > 0 ? pl.bytes : 0, user_ws, user_ws_bytes, stream)) return st;
     (void)hipGetLastError();
@@ -497,12 +872,22 @@ static igc_status_t gn_backward(int N, int H, int W, int C, int G, const void* x
     a.mean = const_cast<float*>(mean);
     a.rstd = const_cast<float*>(rstd);
     a.joined = (float*)((char*)ws.ptr + pl.part_bytes);
+    a.sums = (float*)((char*)ws.ptr + pl.part_bytes + pl.stat_bytes);
     a.dgamma = dgamma;
     a.dbeta = dbeta;
-    if (grid > 0) hipLaunchKernelGGL(gn_backward_partial_kernel<FP16>, dim3((unsigned)grid), dim3(pl.threads), 0, stream, a);
     const unsigned params = dgamma || dbeta ? (unsigned)((C + 31) / 32) : 0;
-    hipLaunchKernelGGL(gn_backward_finish_kernel, dim3((unsigned)(N * G) + params), dim3(256), 0, stream, a);
-    if (grid > 0) hipLaunchKernelGGL(gn_backward_apply_kernel<FP16>, dim3((unsigned)grid), dim3(pl.threads), 0, stream, a);
+    if (N > 0 && !pl.nv) {
+        hipLaunchKernelGGL(gn_backward_partial_kernel<FP16>, dim3((unsigned)a.grid), dim3(pl.threads), 0, stream, a);
+        hipLaunchKernelGGL(gn_backward_finish_kernel, dim3((unsigned)(N * G)), dim3(256), 0, stream, a);
+        hipLaunchKernelGGL(gn_backward_apply_kernel<FP16>, dim3((unsigned)a.grid + params), dim3(pl.threads), 0, stream,
+                           a);
+    } else {
+        if (N > 0 && a.cpg % 8 == 0)
+            launch_backward_resident<FP16, true>(a, pl, stream);
+        else if (N > 0)
+            launch_backward_resident<FP16, false>(a, pl, stream);
+        if (params) hipLaunchKernelGGL(gn_param_kernel, dim3(params), dim3(256), 0, stream, a);
+    }
     return hipGetLastError() == hipSuccess ? IGC_OK : IGC_ERR_HIP;
 }
 
@@ -548,7 +933,10 @@ IGC_GN_BACKWARD(group_norm_nhwc_backward_fp16, true)
 
 int64_t igc_group_norm_workspace_bytes(int N, int H, int W, int C, int G) {
     if (check_shape(N, H, W, C, G, IGC_OUT_F32, IGC_ACT_NONE) != IGC_OK) return -1;
-    return N == 0 ? 0 : gn_plan(N, (int64_t)H * W, C, G).bytes;
+    if (N == 0) return 0;
+    const int64_t forward = gn_plan(N, (int64_t)H * W, C, G, kGnMostForward).bytes;
+    const int64_t backward = gn_plan(N, (int64_t)H * W, C, G, kGnMostBackward).bytes;
+    return forward > backward ? forward : backward;
 }
 
 }  // extern "C"

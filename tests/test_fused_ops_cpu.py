@@ -156,4 +156,5 @@ def test_binding():
     with pytest.raises(KeyError):
         igc.Epilogue(act="tanh")
     assert igc.Epilogue(residual=P, ldr=8, residual_type=1).c.ldr == 8
-    assert ctypes.sizeof(igc.CEpilogue) == 72
+    assert ctypes.sizeof(igc.CEpilogue) == 72 and len(e.raw) == 72
+    assert bytes(e.c) == e.raw
