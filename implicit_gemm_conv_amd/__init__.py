@@ -235,11 +235,11 @@ def lib():
 
 
 def _ptr(x):
-    if x is None:
-        return None
-    if hasattr(x, "data_ptr"):
-        return ctypes.c_void_p(x.data_ptr())
-    return ctypes.c_void_p(int(x))
+    """A tensor's device address, or an address as it is."""
+    try:
+        return x.data_ptr()
+    except AttributeError:
+        return None if x is None else int(x)
 
 
 def _nbytes(x):
@@ -250,19 +250,10 @@ def _nbytes(x):
     raise TypeError("pass workspace_bytes with a raw workspace address")
 
 
-def _stream(stream):
-    if stream is None:
-        import torch
-        return ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)
-    if hasattr(stream, "cuda_stream"):
-        return ctypes.c_void_p(stream.cuda_stream)
-    return ctypes.c_void_p(int(stream))
-
-
 _current_handle = None
 
 
-def _raw_stream(stream):
+def _stream(stream):
     """The handle of `stream`, or of torch's current one, as an integer.  (torch.cuda.current_stream() builds a Stream
     object, 2.8 us a call; torch's own generated code asks for the handle alone, 0.2 us.)"""
     if stream is None:
@@ -352,14 +343,6 @@ def _epi(e):
     return e.raw if isinstance(e, Epilogue) else None if e is None else bytes(e)
 
 
-def _address(x):
-    """A tensor's device address, or an address as it is."""
-    try:
-        return x.data_ptr()
-    except AttributeError:
-        return None if x is None else int(x)
-
-
 def _entry(name):
     """The C function, looked up once, at the first call."""
     found = []
@@ -371,21 +354,20 @@ def _entry(name):
     return get
 
 
-# The calls of small operators are bound by their host side, so these look their C function up once, pass plain
-# addresses and take the raw stream handle.
+# The calls of small operators are bound by their host side, so these look their C function up once.
 
 def _gemm_epilogue(name):
     plain, ex = _entry(name), _entry(name + "_ex")
 
     def call(M, N, K, A, lda, la, B, ldb, lb, D, ldd, d_type, epilogue, stream=None):
-        return plain()(M, N, K, _address(A), lda, la, _address(B), ldb, lb, _address(D), ldd, d_type, _epi(epilogue),
-                       _raw_stream(stream))
+        return plain()(M, N, K, _ptr(A), lda, la, _ptr(B), ldb, lb, _ptr(D), ldd, d_type, _epi(epilogue),
+                       _stream(stream))
 
     def call_ex(M, N, K, A, lda, la, B, ldb, lb, D, ldd, d_type, epilogue, tune=None, workspace=None,
                 workspace_bytes=None, stream=None):
         wsb = workspace_bytes if workspace_bytes is not None else _nbytes(workspace)
-        return ex()(M, N, K, _address(A), lda, la, _address(B), ldb, lb, _address(D), ldd, d_type, _epi(epilogue),
-                    _tune(tune), _address(workspace), wsb, _raw_stream(stream))
+        return ex()(M, N, K, _ptr(A), lda, la, _ptr(B), ldb, lb, _ptr(D), ldd, d_type, _epi(epilogue),
+                    _tune(tune), _ptr(workspace), wsb, _stream(stream))
     call.__name__, call_ex.__name__ = name, name + "_ex"
     return call, call_ex
 
@@ -395,14 +377,14 @@ def _conv_epilogue(name):
 
     def call(N, H, W, C, K, R, S, stride_h, stride_w, pad_h, pad_w, dil_h, dil_w, x, w, y, y_type, epilogue,
              stream=None):
-        return plain()(N, H, W, C, K, R, S, stride_h, stride_w, pad_h, pad_w, dil_h, dil_w, _address(x), _address(w),
-                       _address(y), y_type, _epi(epilogue), _raw_stream(stream))
+        return plain()(N, H, W, C, K, R, S, stride_h, stride_w, pad_h, pad_w, dil_h, dil_w, _ptr(x), _ptr(w),
+                       _ptr(y), y_type, _epi(epilogue), _stream(stream))
 
     def call_ex(N, H, W, C, K, R, S, stride_h, stride_w, pad_h, pad_w, dil_h, dil_w, x, w, y, y_type, epilogue,
                 tune=None, workspace=None, workspace_bytes=None, stream=None):
         wsb = workspace_bytes if workspace_bytes is not None else _nbytes(workspace)
-        return ex()(N, H, W, C, K, R, S, stride_h, stride_w, pad_h, pad_w, dil_h, dil_w, _address(x), _address(w),
-                    _address(y), y_type, _epi(epilogue), _tune(tune), _address(workspace), wsb, _raw_stream(stream))
+        return ex()(N, H, W, C, K, R, S, stride_h, stride_w, pad_h, pad_w, dil_h, dil_w, _ptr(x), _ptr(w),
+                    _ptr(y), y_type, _epi(epilogue), _tune(tune), _ptr(workspace), wsb, _stream(stream))
     call.__name__, call_ex.__name__ = name, name + "_ex"
     return call, call_ex
 
@@ -411,14 +393,14 @@ def _epilogue_backward(name):
     plain, ex = _entry(name), _entry(name + "_ex")
 
     def call(M, N, act, dD, ldd, pre, ldp, dz, ldz, dbias, dbias_type, stream=None):
-        return plain()(M, N, act_code(act), _address(dD), ldd, _address(pre), ldp, _address(dz), ldz, _address(dbias),
-                       dbias_type, _raw_stream(stream))
+        return plain()(M, N, act_code(act), _ptr(dD), ldd, _ptr(pre), ldp, _ptr(dz), ldz, _ptr(dbias),
+                       dbias_type, _stream(stream))
 
     def call_ex(M, N, act, dD, ldd, pre, ldp, dz, ldz, dbias, dbias_type, workspace=None, workspace_bytes=None,
                 stream=None):
         wsb = workspace_bytes if workspace_bytes is not None else _nbytes(workspace)
-        return ex()(M, N, act_code(act), _address(dD), ldd, _address(pre), ldp, _address(dz), ldz, _address(dbias),
-                    dbias_type, _address(workspace), wsb, _raw_stream(stream))
+        return ex()(M, N, act_code(act), _ptr(dD), ldd, _ptr(pre), ldp, _ptr(dz), ldz, _ptr(dbias),
+                    dbias_type, _ptr(workspace), wsb, _stream(stream))
     call.__name__, call_ex.__name__ = name, name + "_ex"
     return call, call_ex
 
@@ -427,14 +409,14 @@ def _group_norm(name):
     plain, ex = _entry(name), _entry(name + "_ex")
 
     def call(N, H, W, C, G, x, ldx, gamma, beta, param_type, eps, act, y, ldy, mean=None, rstd=None, stream=None):
-        return plain()(N, H, W, C, G, _address(x), ldx, _address(gamma), _address(beta), param_type, eps,
-                       act_code(act), _address(y), ldy, _address(mean), _address(rstd), _raw_stream(stream))
+        return plain()(N, H, W, C, G, _ptr(x), ldx, _ptr(gamma), _ptr(beta), param_type, eps,
+                       act_code(act), _ptr(y), ldy, _ptr(mean), _ptr(rstd), _stream(stream))
 
     def call_ex(N, H, W, C, G, x, ldx, gamma, beta, param_type, eps, act, y, ldy, mean=None, rstd=None,
                 workspace=None, workspace_bytes=None, stream=None):
         wsb = workspace_bytes if workspace_bytes is not None else _nbytes(workspace)
-        return ex()(N, H, W, C, G, _address(x), ldx, _address(gamma), _address(beta), param_type, eps, act_code(act),
-                    _address(y), ldy, _address(mean), _address(rstd), _address(workspace), wsb, _raw_stream(stream))
+        return ex()(N, H, W, C, G, _ptr(x), ldx, _ptr(gamma), _ptr(beta), param_type, eps, act_code(act),
+                    _ptr(y), ldy, _ptr(mean), _ptr(rstd), _ptr(workspace), wsb, _stream(stream))
     call.__name__, call_ex.__name__ = name, name + "_ex"
     return call, call_ex
 
@@ -444,16 +426,16 @@ def _group_norm_backward(name):
 
     def call(N, H, W, C, G, x, ldx, gamma, beta, param_type, mean, rstd, act, dy, lddy, dx, lddx, dgamma=None,
              dbeta=None, stream=None):
-        return plain()(N, H, W, C, G, _address(x), ldx, _address(gamma), _address(beta), param_type, _address(mean),
-                       _address(rstd), act_code(act), _address(dy), lddy, _address(dx), lddx, _address(dgamma),
-                       _address(dbeta), _raw_stream(stream))
+        return plain()(N, H, W, C, G, _ptr(x), ldx, _ptr(gamma), _ptr(beta), param_type, _ptr(mean),
+                       _ptr(rstd), act_code(act), _ptr(dy), lddy, _ptr(dx), lddx, _ptr(dgamma),
+                       _ptr(dbeta), _stream(stream))
 
     def call_ex(N, H, W, C, G, x, ldx, gamma, beta, param_type, mean, rstd, act, dy, lddy, dx, lddx, dgamma=None,
                 dbeta=None, workspace=None, workspace_bytes=None, stream=None):
         wsb = workspace_bytes if workspace_bytes is not None else _nbytes(workspace)
-        return ex()(N, H, W, C, G, _address(x), ldx, _address(gamma), _address(beta), param_type, _address(mean),
-                    _address(rstd), act_code(act), _address(dy), lddy, _address(dx), lddx, _address(dgamma),
-                    _address(dbeta), _address(workspace), wsb, _raw_stream(stream))
+        return ex()(N, H, W, C, G, _ptr(x), ldx, _ptr(gamma), _ptr(beta), param_type, _ptr(mean),
+                    _ptr(rstd), act_code(act), _ptr(dy), lddy, _ptr(dx), lddx, _ptr(dgamma),
+                    _ptr(dbeta), _ptr(workspace), wsb, _stream(stream))
     call.__name__, call_ex.__name__ = name, name + "_ex"
     return call, call_ex
 

@@ -432,22 +432,69 @@ struct GnSlab {
     }
 };
 
-// Sums over the slab's groups: `w` values a thread (one, all its channels being
-// of one group, or its eight channels apart), to out[group].  `red` holds
-// threads * w floats.  Every thread calls it.
+// Sum of each of the slab's channels over the workgroup's pixel lanes, to
+// chan[channel]: up to 16 threads a channel, whose lanes lie along the channels
+// (consecutive LDS words), then one.  `red` holds 8 floats a thread.  Every
+// thread calls it.
+__device__ __forceinline__ void channel_sums(const GnArgs& a, const GnSlab& s, const float (&val)[8], float* red,
+                                             float* chan) {
+    const int t = (int)threadIdx.x, row = a.sv * 8;  // channels of a full slab: a row of `red`
+    __syncthreads();                                 // `red` and `chan` of an earlier call have been read
+    if (s.on) {
+        float* dst = red + s.p * row + s.v * 8;
+        *(f32x4s_t*)dst = f32x4s_t{val[0], val[1], val[2], val[3]};
+        *(f32x4s_t*)(dst + 4) = f32x4s_t{val[4], val[5], val[6], val[7]};
+    }
+    __syncthreads();
+    const int nch = s.sv * 8, turn = (int)blockDim.x < nch ? (int)blockDim.x : nch;
+    int per = (int)blockDim.x / turn;  // threads a channel
+    per = per > 16 ? 16 : per;
+    if (per > 1) {  // one turn covers every channel
+        const int q = t / nch, c = t - q * nch;
+        float sum = 0.0f;
+        if (q < per)
+            for (int p = q; p < a.pl; p += per) sum += red[p * row + c];
+        __syncthreads();
+        if (q < per) red[q * nch + c] = sum;
+        __syncthreads();
+        if (t < nch) {
+            sum = red[t];
+            for (int k = 1; k < per; ++k) sum += red[k * nch + t];
+            chan[t] = sum;
+        }
+    } else {
+        for (int c = t; c < nch; c += turn) {
+            float sum = 0.0f;
+            for (int p = 0; p < a.pl; ++p) sum += red[p * row + c];
+            chan[c] = sum;
+        }
+    }
+    __syncthreads();
+}
+
+// Sums over the slab's groups, to out[group]: W values a thread, one (all its
+// channels being of one group) or its eight channels apart.  `red` holds W
+// floats a thread, `chan` (W == 8) the slab's channels.  Every thread calls it.
 template <int W>
 __device__ __forceinline__ void group_sums(const GnArgs& a, const GnSlab& s, const float (&val)[W], float* red,
-                                           float* out) {
-    __syncthreads();  // `red` and `out` of an earlier call have been read
-#pragma unroll
-    for (int i = 0; i < W; ++i) red[threadIdx.x * W + i] = s.on ? val[i] : 0.0f;
-    __syncthreads();
+                                           float* chan, float* out) {
     const int lane = (int)threadIdx.x & 63, waves = (int)(blockDim.x >> 6);
-    const int per = W == 1 ? a.cpg / 8 : a.cpg;  // entries of a group in one pixel lane
-    for (int g = (int)(threadIdx.x >> 6); g < s.groups; g += waves) {
+    if constexpr (W == 1) {
+        __syncthreads();  // `red` and `out` of an earlier call have been read
+        if (s.on) red[s.p * a.sv + s.v] = val[0];
+        __syncthreads();
+    } else {
+        channel_sums(a, s, val, red, chan);
+    }
+    for (int g = (int)(threadIdx.x >> 6); g < s.groups; g += waves) {  // a wave a group
         float t = 0.0f;
-        for (int e = 0; e < per; ++e)
-            for (int p = lane; p < a.pl; p += 64) t += red[p * a.sv * W + g * per + e];
+        if constexpr (W == 1) {
+            const int per = a.cpg / 8;
+            for (int e = 0; e < per; ++e)
+                for (int p = lane; p < a.pl; p += 64) t += red[p * a.sv + g * per + e];
+        } else {
+            for (int c = lane; c < a.cpg; c += 64) t += chan[g * a.cpg + c];
+        }
 #pragma unroll
         for (int d = 32; d >= 1; d >>= 1) t += __shfl_xor(t, d);
         if (lane == 0) out[g] = t;
@@ -460,8 +507,9 @@ constexpr int kGnMaxThreads = 1024, kGnMaxVecs = 256;  // of a workgroup of the 
 template <bool FP16, int NV, bool SINGLE>
 __global__ __launch_bounds__(kGnMaxThreads) void gn_resident_kernel(const GnArgs a) {
     constexpr int W = SINGLE ? 1 : 8;
-    __shared__ float red[kGnMaxThreads * W];
+    __shared__ __attribute__((aligned(16))) float red[kGnMaxThreads * W];
     __shared__ float sums[kGnMaxVecs * W];  // by group of the slab
+    __shared__ float chan[SINGLE ? 1 : kGnMaxVecs * 8];
     const GnSlab s(a);
     const char* img = (const char*)a.x + ((int64_t)s.n * a.HW * a.ldx + s.c) * 2;
     u32x4s_t x[NV];
@@ -492,7 +540,7 @@ __global__ __launch_bounds__(kGnMaxThreads) void gn_resident_kernel(const GnArgs
         for (int i = 0; i < 8; ++i) acc[i % W] += v[i];
         one_at_a_time();
     }
-    group_sums<W>(a, s, acc, red, sums);
+    group_sums<W>(a, s, acc, red, chan, sums);
     keep_packed(x);
 #pragma unroll
     for (int i = 0; i < W; ++i) {
@@ -511,7 +559,7 @@ __global__ __launch_bounds__(kGnMaxThreads) void gn_resident_kernel(const GnArgs
         }
         one_at_a_time();
     }
-    group_sums<W>(a, s, acc, red, sums);
+    group_sums<W>(a, s, acc, red, chan, sums);
     keep_packed(x);
 #pragma unroll
     for (int i = 0; i < W; ++i) rs[i] = 1.0f / __builtin_sqrtf(sums[gi[i]] * rn + a.eps);
@@ -549,7 +597,7 @@ __global__ __launch_bounds__(kGnMaxThreads) void gn_resident_kernel(const GnArgs
 template <bool FP16, int NV, bool SINGLE>
 __global__ __launch_bounds__(kGnMaxThreads) void gn_backward_resident_kernel(const GnArgs a) {
     constexpr int W = SINGLE ? 1 : 8;
-    __shared__ float red[kGnMaxThreads * 8];
+    __shared__ __attribute__((aligned(16))) float red[kGnMaxThreads * 8];
     __shared__ float chan[2 * 8 * kGnMaxVecs];  // the slab's channels, both sums
     const GnSlab s(a);
     const char* img = (const char*)a.x + ((int64_t)s.n * a.HW * a.ldx + s.c) * 2;
@@ -596,40 +644,23 @@ __global__ __launch_bounds__(kGnMaxThreads) void gn_backward_resident_kernel(con
         }
     });
     const int lane = (int)threadIdx.x & 63, waves = (int)(blockDim.x >> 6), nch = s.sv * 8;
-    for (int turn = 0; turn < 2; ++turn) {
-        __syncthreads();
-#pragma unroll
-        for (int i = 0; i < 8; ++i) red[threadIdx.x * 8 + i] = s.on ? (turn ? s2[i] : s1[i]) : 0.0f;
-        __syncthreads();
-        if (a.pl >= 64) {  // a wave a channel
-            for (int c = (int)(threadIdx.x >> 6); c < nch; c += waves) {
-                float t = 0.0f;
-                for (int p = lane; p < a.pl; p += 64) t += red[p * a.sv * 8 + c];
-#pragma unroll
-                for (int m = 32; m >= 1; m >>= 1) t += __shfl_xor(t, m);
-                if (lane == 0) chan[2 * c + turn] = t;
-            }
-        } else {  // a thread a channel
-            for (int c = (int)threadIdx.x; c < nch; c += (int)blockDim.x) {
-                float t = 0.0f;
-                for (int p = 0; p < a.pl; ++p) t += red[p * a.sv * 8 + c];
-                chan[2 * c + turn] = t;
-            }
-        }
-    }
-    __syncthreads();
+    channel_sums(a, s, s1, red, chan);
+    channel_sums(a, s, s2, red, chan + nch);
     const int c0 = s.g0 * a.cpg;  // the slab's first channel
     if (a.dgamma || a.dbeta)
-        for (int i = (int)threadIdx.x; i < 2 * nch; i += (int)blockDim.x)
-            a.sums[((int64_t)s.n * a.C + c0) * 2 + i] = chan[i];
+        for (int i = (int)threadIdx.x; i < nch; i += (int)blockDim.x) {
+            float* dst = a.sums + ((int64_t)s.n * a.C + c0 + i) * 2;
+            dst[0] = chan[i];
+            dst[1] = chan[nch + i];
+        }
     // a wave a group: its two means, into `red`
     const float rn = 1.0f / ((float)a.HW * (float)a.cpg);
     for (int g = (int)(threadIdx.x >> 6); g < s.groups; g += waves) {
         float t1 = 0.0f, t2 = 0.0f;
         for (int c = g * a.cpg + lane; c < (g + 1) * a.cpg; c += 64) {
             const float w = a.gamma ? load_kind(a.gamma, c0 + c, a.param_kind) : 1.0f;
-            t1 = __builtin_fmaf(w, chan[2 * c], t1);
-            t2 = __builtin_fmaf(w, chan[2 * c + 1], t2);
+            t1 = __builtin_fmaf(w, chan[c], t1);
+            t2 = __builtin_fmaf(w, chan[nch + c], t2);
         }
 #pragma unroll
         for (int m = 32; m >= 1; m >>= 1) {
