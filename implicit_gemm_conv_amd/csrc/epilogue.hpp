@@ -87,17 +87,74 @@ __device__ __forceinline__ void epi_element(const Epi& e, void* out, int64_t ldc
 // segments, and everything up to the one rounding happens in fp32.  The
 // activation needs the accumulators out of their statically indexed registers
 // anyway: it runs in a loop over the staged rows, UQ row groups a turn, and so
-// is compiled once per kernel half instead of once per register.  What bounds
-// it: one workgroup holds a CU, so nothing covers the tile's 128 KB of output
-// and of residual but the other waves' activations; the residual of the next
-// UQ row groups is in flight while a turn computes.
+// is compiled once per pass instead of once per register.  What bounds it: one
+// workgroup holds a CU, so nothing covers the tile's output and residual but
+// the other waves of the same tile.  Rows and columns outside are left out by
+// buffer offsets past the end, not by branches: loads and stores retire in one
+// order, and with a known number of stores between, the wait for the next
+// turn's residual, requested before them, leaves them in flight.
 //
 // Chunk c (16 bytes, four columns) of staged row r lies at c ^ (r & (CPR-1)):
 // the 16 rows of an accumulator block are written to distinct banks, and the
 // two chunks a lane reads back stay distinct over the lanes of a phase.
+typedef __attribute__((ext_vector_type(4))) int i32x4e_t;
+
+// One of the matrices beside the product: a buffer at the wave's sub-tile and
+// the byte distance of its rows and of eight columns.
+struct EpiMatrix {
+    __amdgpu_buffer_rsrc_t rs;
+    uint32_t first, step;  // the lane's offset in row group 0, and from one group to the next
+    int kind;
+    __device__ __forceinline__ EpiMatrix(const void* base, int64_t ld, int kind_, int64_t m, int64_t n, int row, int col,
+                                         int rpi)
+        : kind(kind_) {
+        const int esz = kind == KIND_F32 ? 4 : 2;
+        rs = make_rsrc_u((const char*)base + (m * ld + n) * esz);
+        first = (uint32_t)((row * ld + col) * esz);
+        step = (uint32_t)(rpi * ld * esz);
+    }
+    __device__ __forceinline__ u32x4s_t load(int q, bool in, int half) const {
+        return __builtin_bit_cast(u32x4s_t, __builtin_amdgcn_raw_buffer_load_b128(
+                                                rs, in ? first + q * step + 16 * half : kOob, 0, 0));
+    }
+    __device__ __forceinline__ void store(int q, bool in, int half, u32x4s_t w) const {
+        __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(i32x4e_t, w), rs,
+                                               in ? first + q * step + 16 * half : kOob, 0, 0);
+    }
+    // eight values of row group q; `left` of them lie in the row
+    __device__ __forceinline__ void load8(int q, bool in, int left, float (&v)[8]) const {
+        if (kind == KIND_F32) {
+            const f32x4s_t lo = __builtin_bit_cast(f32x4s_t, load(q, in, 0));
+            const f32x4s_t hi = __builtin_bit_cast(f32x4s_t, load(q, in && left > 4, 1));
+#pragma unroll
+            for (int i = 0; i < 4; ++i) v[i] = lo[i], v[4 + i] = hi[i];
+        } else {
+            decode8(load(q, in, 0), kind, v);
+        }
+    }
+    __device__ __forceinline__ void store8(void* base, int64_t off, int q, bool in, int left, const float (&v)[8]) const {
+        const bool whole = in && left >= 8;
+        if (kind == KIND_F32) {
+            store(q, whole, 0, __builtin_bit_cast(u32x4s_t, f32x4s_t{v[0], v[1], v[2], v[3]}));
+            store(q, whole, 1, __builtin_bit_cast(u32x4s_t, f32x4s_t{v[4], v[5], v[6], v[7]}));
+        } else {
+            store(q, whole, 0, kind == KIND_BF16 ? pack8<false>(v) : pack8<true>(v));
+        }
+        if (in && left < 8) {  // the piece that straddles the end of the row
+            float z[7] = {v[0], v[1], v[2], v[3], v[4], v[5], v[6]};
+#pragma unroll 1
+            for (int i = 0; i < left; ++i) {
+                store_kind(base, off + i, kind, z[0]);
+#pragma unroll
+                for (int k = 0; k < 6; ++k) z[k] = z[k + 1];
+            }
+        }
+    }
+};
+
 template <class C, int I0, int NI, bool BWD, class ML>
 __device__ __forceinline__ void epi_rows(ML& ml, const typename C::Acc (&acc)[C::FM][C::FN], IGC_LDS char* reg,
-                                         const Params& p, const Epi& e, const float (&bias)[8], int lane, bool vec) {
+                                         const Params& p, const Epi& e, const float (&bias)[8], int lane) {
     constexpr int RB = C::WTN * 4, CPR = RB / 16;
     constexpr int LPR = C::WTN / 8;  // lanes per row
     constexpr int RPI = 64 / LPR;    // rows per group
@@ -111,24 +168,30 @@ __device__ __forceinline__ void epi_rows(ML& ml, const typename C::Acc (&acc)[C:
             const int row = 16 * i + (lane & 15), c = 4 * j + (lane >> 4);
             *(IGC_LDS f32x4_t*)(reg + row * RB + ((c ^ (row & (CPR - 1))) << 4)) = acc[I0 + i][j];
         }
-    const int col = (lane % LPR) * 8;
-    const int64_t m0 = ml.m0 + ml.wm * C::WTM + 16 * I0 + lane / LPR, n0 = ml.n0 + ml.wn * C::WTN + col;
-    const int64_t rows = p.M - m0;  // row group q of this lane is inside while q * RPI < rows
-    const int left = p.N - n0 >= 8 ? 8 : (int)(p.N - n0);
-    const bool res_raw = e.res && vec && e.res_kind != KIND_F32;
-    const bool pre_raw = BWD && e.pre && vec && e.pre_kind != KIND_F32;
+    const int row0 = lane / LPR, col = (lane % LPR) * 8;
+    const int64_t m0 = ml.m0 + ml.wm * C::WTM + 16 * I0, n0 = ml.n0 + ml.wn * C::WTN;
+    const int left = p.N - (n0 + col) >= 8 ? 8 : (int)(p.N - (n0 + col));
+    // row group q of this lane is inside while q * RPI < rows
+    const int rows = left > 0 ? (p.M - (m0 + row0) < 4096 ? (int)(p.M - (m0 + row0)) : 4096) : 0;
+    const EpiMatrix out(p.C, p.ldc, p.out_kind, m0, n0, row0, col, RPI);
+    const EpiMatrix res(e.res ? e.res : p.C, e.ldr, e.res_kind, m0, n0, row0, col, RPI);
+    const EpiMatrix pre(e.pre ? e.pre : p.C, e.ldp, e.pre_kind, m0, n0, row0, col, RPI);
+    const bool res_raw = e.res && e.res_kind != KIND_F32;
+    const bool pre_raw = BWD && e.pre && e.pre_kind != KIND_F32;
     u32x4s_t rv[UQ], gv[UQ];
-    auto fetch = [&](int q, int u) __attribute__((always_inline)) {
-        const bool in = left > 0 && q * RPI < rows;
-        if (res_raw && in) rv[u] = raw8(e.res, (m0 + q * RPI) * e.ldr + n0);
-        if (pre_raw && in) gv[u] = raw8(e.pre, (m0 + q * RPI) * e.ldp + n0);
+    auto fetch = [&](int q) __attribute__((always_inline)) {
+        if (res_raw) {
+#pragma unroll
+            for (int u = 0; u < UQ; ++u) rv[u] = res.load(q + u, (q + u) * RPI < rows, 0);
+        }
+        if (pre_raw) {
+#pragma unroll
+            for (int u = 0; u < UQ; ++u) gv[u] = pre.load(q + u, (q + u) * RPI < rows, 0);
+        }
     };
 #pragma unroll
-    for (int u = 0; u < UQ; ++u) {
-        rv[u] = u32x4s_t{0, 0, 0, 0};
-        gv[u] = u32x4s_t{0, 0, 0, 0};
-        fetch(u, u);
-    }
+    for (int u = 0; u < UQ; ++u) rv[u] = gv[u] = u32x4s_t{0, 0, 0, 0};
+    fetch(0);
     // the wave's own writes, read back by other lanes of the same wave
     wait_lgkmcnt0();
     compiler_fence();
@@ -137,7 +200,7 @@ __device__ __forceinline__ void epi_rows(ML& ml, const typename C::Acc (&acc)[C:
         float v[UQ][8];
 #pragma unroll
         for (int u = 0; u < UQ; ++u) {
-            const int row = (q0 + u) * RPI + lane / LPR, c = col / 4, x = row & (CPR - 1);
+            const int row = (q0 + u) * RPI + row0, c = col / 4, x = row & (CPR - 1);
             const f32x4_t lo = *(const IGC_LDS f32x4_t*)(reg + row * RB + ((c ^ x) << 4));
             const f32x4_t hi = *(const IGC_LDS f32x4_t*)(reg + row * RB + (((c + 1) ^ x) << 4));
 #pragma unroll
@@ -148,14 +211,10 @@ __device__ __forceinline__ void epi_rows(ML& ml, const typename C::Acc (&acc)[C:
                 float g[UQ][8];
 #pragma unroll
                 for (int u = 0; u < UQ; ++u) {
-                    if (pre_raw) {
+                    if (pre_raw)
                         decode8(gv[u], e.pre_kind, g[u]);
-                    } else {
-#pragma unroll
-                        for (int i = 0; i < 8; ++i) g[u][i] = 0.0f;
-                        if (left > 0 && (q0 + u) * RPI < rows)
-                            load8(e.pre, (m0 + (q0 + u) * RPI) * e.ldp + n0, e.pre_kind, left, vec, g[u]);
-                    }
+                    else
+                        pre.load8(q0 + u, (q0 + u) * RPI < rows, left, g[u]);
                 }
                 with_act(e.act, [&](auto A) __attribute__((always_inline)) {
 #pragma unroll
@@ -168,8 +227,8 @@ __device__ __forceinline__ void epi_rows(ML& ml, const typename C::Acc (&acc)[C:
             if (e.pre) {
 #pragma unroll
                 for (int u = 0; u < UQ; ++u)
-                    if (left > 0 && (q0 + u) * RPI < rows)
-                        store8(e.pre, (m0 + (q0 + u) * RPI) * e.ldp + n0, e.pre_kind, left, vec, v[u]);
+                    pre.store8(e.pre, (m0 + row0 + (q0 + u) * RPI) * e.ldp + n0 + col, q0 + u, (q0 + u) * RPI < rows, left,
+                               v[u]);
             }
             with_act(e.act, [&](auto A) __attribute__((always_inline)) {
 #pragma unroll
@@ -178,26 +237,22 @@ __device__ __forceinline__ void epi_rows(ML& ml, const typename C::Acc (&acc)[C:
                     for (int i = 0; i < 8; ++i) v[u][i] = act_of<decltype(A)::value>(v[u][i]);
             });
         }
+        if (e.res) {
 #pragma unroll
-        for (int u = 0; u < UQ; ++u) {
-            const bool in = left > 0 && (q0 + u) * RPI < rows;
-            if (e.res) {
+            for (int u = 0; u < UQ; ++u) {
                 float r[8];
-                if (res_raw) {
+                if (res_raw)
                     decode8(rv[u], e.res_kind, r);
-                } else {
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) r[i] = 0.0f;
-                    if (in) load8(e.res, (m0 + (q0 + u) * RPI) * e.ldr + n0, e.res_kind, left, vec, r);
-                }
+                else
+                    res.load8(q0 + u, (q0 + u) * RPI < rows, left, r);
 #pragma unroll
                 for (int i = 0; i < 8; ++i) v[u][i] += r[i];
             }
-            if (in) store8(p.C, (m0 + (q0 + u) * RPI) * p.ldc + n0, p.out_kind, left, vec, v[u]);
         }
+        if (q0 + UQ < NQ) fetch(q0 + UQ);
 #pragma unroll
         for (int u = 0; u < UQ; ++u)
-            if (q0 + UQ + u < NQ) fetch(q0 + UQ + u, u);
+            out.store8(p.C, (m0 + row0 + (q0 + u) * RPI) * p.ldc + n0 + col, q0 + u, (q0 + u) * RPI < rows, left, v[u]);
     }
     // reads done before the piece is written again
     wait_lgkmcnt0();
@@ -207,11 +262,11 @@ __device__ __forceinline__ void epi_rows(ML& ml, const typename C::Acc (&acc)[C:
 // Every pass of a wave's sub-tile, at most four block rows each.
 template <class C, int I0, bool BWD, class ML>
 __device__ __forceinline__ void epi_passes(ML& ml, const typename C::Acc (&acc)[C::FM][C::FN], IGC_LDS char* reg,
-                                           const Params& p, const Epi& e, const float (&bias)[8], int lane, bool vec) {
+                                           const Params& p, const Epi& e, const float (&bias)[8], int lane) {
     if constexpr (I0 < C::FM) {
         constexpr int NI = C::FM - I0 < 4 ? C::FM - I0 : 4;
-        epi_rows<C, I0, NI, BWD>(ml, acc, reg, p, e, bias, lane, vec);
-        epi_passes<C, I0 + NI, BWD>(ml, acc, reg, p, e, bias, lane, vec);
+        epi_rows<C, I0, NI, BWD>(ml, acc, reg, p, e, bias, lane);
+        epi_passes<C, I0 + NI, BWD>(ml, acc, reg, p, e, bias, lane);
     }
 }
 
@@ -230,13 +285,12 @@ __global__ __launch_bounds__(C::NT) void gemm_epi_kernel(const Params p, const E
         // opaque copy of the lane: nothing derived from it is computed before, and kept through, the K loop
         int lane = ml.lane;
         asm volatile("" : "+v"(lane));
-        const bool vec = p.vec_ok;
         float bias[8];
         const int64_t n0 = ml.n0 + ml.wn * C::WTN + (lane % (C::WTN / 8)) * 8;
 #pragma unroll
         for (int i = 0; i < 8; ++i) bias[i] = e.bias && n0 + i < p.N ? load_kind(e.bias, n0 + i, e.bias_kind) : 0.0f;
         ring_barrier();  // every wave has finished reading the ring
-        epi_passes<C, 0, BWD>(ml, acc, stage_piece<C, PIECE>(ml.wave), p, e, bias, lane, vec);
+        epi_passes<C, 0, BWD>(ml, acc, stage_piece<C, PIECE>(ml.wave), p, e, bias, lane);
     });
 }
 

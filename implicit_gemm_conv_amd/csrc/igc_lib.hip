@@ -177,11 +177,18 @@ struct Layout {
     int64_t part_bytes = 0, flag_off = 0, bytes = 0;
 };
 
-static Layout layout_of(const Plan& pl, int64_t M, int64_t N, int64_t K) {
+// loose: an epilogue over rows that are not 16-byte multiples (a convolution
+// whose filter count is not a multiple of 8).  Its product goes to the
+// workspace in fp32, as one split, and the split epilogue writes the output.
+static Layout layout_of(const Plan& pl, int64_t M, int64_t N, int64_t K, bool loose = false) {
     Layout L;
     const Instance* inst = pl.inst;
     L.tiles = ((M + inst->bm - 1) / inst->bm) * ((N + inst->bn - 1) / inst->bn);
     if (L.tiles <= 0) return L;
+    if (loose) {
+        L.ldws = (N + 3) / 4 * 4;
+        L.bytes = round_up(M * L.ldws * 4, 256);
+    }
     const int64_t unit = (int64_t)inst->bk * Ring::period(Ring::units(inst->d, inst->half));
     if (pl.tune.stream_k > 0 && K > 0) {
         const int64_t G0 = pl.tune.stream_k;
@@ -229,14 +236,20 @@ static int loop_variant(const Params& p, const Instance* inst) {
 static igc_status_t launch(const Plan& pl, Params p, const Epi* epi, void* user_ws, int64_t user_ws_bytes,
                            hipStream_t stream) {
     const Instance* inst = pl.inst;
-    const Layout L = layout_of(pl, p.M, p.N, p.K);
+    const bool loose = epi && !p.vec_ok;
+    const Layout L = layout_of(pl, p.M, p.N, p.K, loose);
     if (L.tiles <= 0) return IGC_OK;
     if (L.tiles * L.S > 0x7fffffff) return IGC_ERR_UNSUPPORTED;
     // a configuration built without this loop variant or without stream-K kernels
     const int v = loop_variant(p, inst);
     const void* fn = L.G > 0 ? inst->fn_sk[v] : inst->fn[v];
     if (epi && L.G > 0) return IGC_ERR_UNSUPPORTED;
-    if (epi && L.S == 1) {
+    if (epi && L.S == 1 && !loose) {
+        // the kernel's offsets within a tile are 32-bit
+        const auto span = [&](int64_t ld, int kind) { return inst->bm * ld * (kind == OUT_F32 ? 4 : 2) >= 0x7fff0000LL; };
+        if (span(p.ldc, p.out_kind) || (epi->res && span(epi->ldr, epi->res_kind)) ||
+            (epi->pre && span(epi->ldp, epi->pre_kind)))
+            return IGC_ERR_UNSUPPORTED;
         const EpiInstance* ei = find_epilogue(*inst);
         fn = ei ? ei->fn[epi->backward ? 1 : 0][v] : nullptr;
     }
@@ -282,10 +295,18 @@ static igc_status_t launch(const Plan& pl, Params p, const Epi* epi, void* user_
     }
     if (e == hipSuccess) {
         Params arg = p;
+        if (loose && L.S == 1) {
+            arg.C = ws;
+            arg.ldc = L.ldws;
+            arg.out_kind = OUT_F32;
+            arg.vec_ok = 1;
+        }
         Epi earg = epi ? *epi : Epi{};
         void* args[] = {&arg, &earg};  // (the plain kernels take the first alone)
         e = hipLaunchKernel(fn, dim3(grid), dim3(64 * inst->waves), args, 0, stream);
     }
+    if (e == hipSuccess && loose && L.S == 1)
+        e = launch_split_epilogue((const float*)ws, 1, 0, p.M, p.N, L.ldws, p.C, p.ldc, p.out_kind, false, *epi, stream);
     if (e == hipSuccess && L.G == 0 && L.S > 1)
         e = epi ? launch_split_epilogue(p.ws, L.S, p.ws_stride, p.M, p.N, p.ldws, p.C, p.ldc, p.out_kind, p.vec_ok, *epi,
                                         stream)
@@ -755,7 +776,7 @@ int64_t igc_epilogue_workspace_bytes(igc_op_t op, int64_t M, int64_t N, int64_t 
     const Plan pl = pick(tune, false, true, true, (int)op, M, N, K, true);
     if (!pl.valid || !pl.inst) return -1;
     if (M == 0 || N == 0) return 0;
-    int64_t bytes = layout_of(pl, M, N, K).bytes;
+    int64_t bytes = layout_of(pl, M, N, K, op == IGC_OP_CONV_FPROP && N % 8 != 0).bytes;
     if (op == IGC_OP_GEMM && !tune && M <= kFewRows)  // the operand layouts decide which kernel runs: room for either
         for (const bool b_kc : {false, true}) {
             const int64_t few = few_rows_bytes(few_rows_plan(M, N, K, b_kc), M, N);
