@@ -62,23 +62,30 @@ __device__ __forceinline__ void store8(void* base, int64_t off, int kind, int le
     }
 }
 
-// Epilogue of one element whose product is `acc`.
-__device__ __forceinline__ void epi_element(const Epi& e, void* out, int64_t ldc, int out_kind, int64_t m, int64_t n,
-                                            float acc) {
-    float z = acc + (e.bias ? load_kind(e.bias, n, e.bias_kind) : 0.0f);
-    const float r = e.res ? load_kind(e.res, m * e.ldr + n, e.res_kind) : 0.0f;
-    float y = z;
-    if (e.backward) {
-        if (e.pre) {
-            const float g = load_kind(e.pre, m * e.ldp + n, e.pre_kind);
-            with_act(e.act, [&](auto A) __attribute__((always_inline)) { y = z * act_grad_of<decltype(A)::value>(g); });
-        }
-    } else {
-        if (e.pre) store_kind(e.pre, m * e.ldp + n, e.pre_kind, z);
-        with_act(e.act, [&](auto A) __attribute__((always_inline)) { y = act_of<decltype(A)::value>(z); });
+// Epilogue of one element: what it reads, then the rest.
+struct EpiElement {
+    float bias = 0.0f, res = 0.0f, pre = 0.0f;
+    __device__ __forceinline__ void fetch(const Epi& e, int64_t m, int64_t n) {
+        if (e.bias) bias = load_kind(e.bias, n, e.bias_kind);
+        if (e.res) res = load_kind(e.res, m * e.ldr + n, e.res_kind);
+        if (e.backward && e.pre) pre = load_kind(e.pre, m * e.ldp + n, e.pre_kind);
     }
-    store_kind(out, m * ldc + n, out_kind, e.res ? y + r : y);
-}
+    __device__ __forceinline__ void finish(const Epi& e, void* out, int64_t ldc, int out_kind, int64_t m, int64_t n,
+                                           float acc) const {
+        const float z = acc + bias;
+        float y = z;
+        if (e.backward) {
+            if (e.pre)
+                with_act(e.act, [&](auto A) __attribute__((always_inline)) {
+                    y = z * act_grad_of<decltype(A)::value>(pre);
+                });
+        } else {
+            if (e.pre) store_kind(e.pre, m * e.ldp + n, e.pre_kind, z);
+            with_act(e.act, [&](auto A) __attribute__((always_inline)) { y = act_of<decltype(A)::value>(z); });
+        }
+        store_kind(out, m * ldc + n, out_kind, e.res ? y + res : y);
+    }
+};
 
 // Epilogue of a tile.  Each wave passes its sub-tile through a private piece
 // of the drained ring as fp32, NI block rows at a time (16 KB a wave for the

@@ -130,6 +130,16 @@ __global__ __launch_bounds__(64 * kFewWaves) void few_rows_kernel(const FewRowsA
 #pragma unroll
     for (int i = 0; i < MT; ++i) aoff[i] = (uint32_t)((16 * i + r < a.M ? 16 * i + r : a.M - 1) * a.lda + 8 * g) * 2;
 
+    // element x = thread + 512 t of the workgroup is (x / COLS, x % COLS): what its epilogue reads comes first
+    EpiElement el[EPT];
+    if (a.splits == 1) {
+#pragma unroll
+        for (int t = 0; t < EPT; ++t) {
+            const int x = (int)threadIdx.x + t * 64 * kFewWaves, m = x / COLS, c = x % COLS;
+            if (x < E && m < a.M && c < left) el[t].fetch(e, m, n0 + c);
+        }
+    }
+
     f32x4_t acc[MT][NB];
 #pragma unroll
     for (int i = 0; i < MT; ++i)
@@ -190,7 +200,7 @@ __global__ __launch_bounds__(64 * kFewWaves) void few_rows_kernel(const FewRowsA
     for (int t = 0; t < EPT; ++t) {
         const int x = (int)threadIdx.x + t * 64 * kFewWaves;
         const int m = x / COLS, c = x % COLS;
-        if (m >= a.M || n0 + c >= a.N || x >= E) continue;
+        if (m >= a.M || c >= left || x >= E) continue;
         const int j = c % NB, q = c / NB;
         const float* src = &red[((m >> 4) * NB + j) * 256 + ((q >> 2) * 16 + (m & 15)) * 4 + (q & 3)];
         float s = src[0];
@@ -199,7 +209,7 @@ __global__ __launch_bounds__(64 * kFewWaves) void few_rows_kernel(const FewRowsA
         if (a.splits > 1)
             a.ws[((int64_t)split * a.M + m) * a.ldws + n0 + c] = s;
         else
-            epi_element(e, a.C, a.ldc, a.out_kind, m, n0 + c, s);
+            el[t].finish(e, a.C, a.ldc, a.out_kind, m, n0 + c, s);
     }
 }
 

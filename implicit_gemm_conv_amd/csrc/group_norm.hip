@@ -23,6 +23,7 @@
 #include <stdint.h>
 
 #include "epilogue.hpp"
+#include "fastdiv.hpp"
 #include "host.hpp"
 
 namespace igc {
@@ -35,17 +36,22 @@ struct GnArgs {
     const void* beta;      // nullptr: 0
     float *mean, *rstd;    // N x G
     float* part;           // N x chunks x C pairs: (mean, M2), or (sum dz, sum dz xh)
-    float* joined;         // backward: N x G pairs (mean of gamma dz, mean of gamma dz xh)
+    float* coef;           // planes of N x C: mean, rstd gamma, beta; backward also -rstd^2 c2 and -rstd c1 (the two means)
     float* sums;           // backward: N x C pairs (sum dz, sum dz xh)
     void *dgamma, *dbeta;  // nullptr: not wanted
     int64_t ldx, lddy, ldo;
     int64_t HW;
     int N, C, G, cpg, param_kind, act;
+    uint32_t cpg_magic;    // fastdiv multiplier of cpg
     int chunks, pixels;    // chunks of an image and pixels per chunk
     int grid;              // workgroups over the images
     int sv, pl, slabs;     // vectors (8 channels) a workgroup covers, its pixel lanes, slabs of an image's channels
     float eps;
 };
+
+__device__ __forceinline__ int group_of(const GnArgs& a, int channel) {
+    return (int)fastdiv((uint32_t)channel, (uint32_t)a.cpg, a.cpg_magic);
+}
 
 constexpr int kGnThreads = 256;  // at most
 
@@ -133,64 +139,83 @@ __global__ __launch_bounds__(kGnThreads) void gn_partial_kernel(const GnArgs a) 
     }
 }
 
-// Sum over a workgroup of 256 threads, in a fixed order; every thread gets it.
+// Sum over a workgroup (at most 16 waves), in a fixed order; every thread gets it.
 __device__ __forceinline__ float block_sum(float v, float* red) {
 #pragma unroll
     for (int d = 32; d >= 1; d >>= 1) v += __shfl_xor(v, d);
     __syncthreads();  // an earlier sum has been read
     if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = v;
     __syncthreads();
-    return (red[0] + red[1]) + (red[2] + red[3]);
+    float t = red[0];
+    for (int w = 1; w < (int)(blockDim.x >> 6); ++w) t += red[w];
+    return t;
 }
 
-// Joins the chunks and channels of one group of one image into its statistics.
-__global__ __launch_bounds__(256) void gn_finish_kernel(const GnArgs a) {
-    __shared__ float red[4];
-    const int n = (int)blockIdx.x / a.G, g = (int)blockIdx.x % a.G;
-    const float* part = a.part + ((int64_t)n * a.chunks * a.C + (int64_t)g * a.cpg) * 2;
-    const int items = a.chunks * a.cpg;
-    const float total = (float)a.HW * (float)a.cpg;
-    float s = 0.0f;
-    for (int i = (int)threadIdx.x; i < items; i += 256) {
-        const int k = i / a.cpg, c = i - k * a.cpg;
-        const int64_t cnt = a.HW - (int64_t)k * a.pixels < a.pixels ? a.HW - (int64_t)k * a.pixels : a.pixels;
-        s = __builtin_fmaf((float)cnt, part[((int64_t)k * a.C + c) * 2], s);
-    }
-    const float mean = block_sum(s, red) / total;
-    s = 0.0f;
-    for (int i = (int)threadIdx.x; i < items; i += 256) {
-        const int k = i / a.cpg, c = i - k * a.cpg;
-        const int64_t cnt = a.HW - (int64_t)k * a.pixels < a.pixels ? a.HW - (int64_t)k * a.pixels : a.pixels;
-        const float d = part[((int64_t)k * a.C + c) * 2] - mean;
-        s += part[((int64_t)k * a.C + c) * 2 + 1] + (float)cnt * d * d;
-    }
-    const float var = block_sum(s, red) / total;
-    if (threadIdx.x == 0) {
-        a.mean[blockIdx.x] = mean;
-        a.rstd[blockIdx.x] = 1.0f / __builtin_sqrtf(var + a.eps);
-    }
-}
-
-// A thread's channels: mean, rstd * gamma (or rstd and gamma apart) and beta.
-struct GnChannels {
-    float mu[8], rs[8], ga[8], be[8];
-    __device__ __forceinline__ GnChannels(const GnArgs& a, int n, int c) {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const int g = n * a.G + (c + i) / a.cpg;
-            mu[i] = a.mean[g];
-            rs[i] = a.rstd[g];
-            ga[i] = a.gamma ? load_kind(a.gamma, c + i, a.param_kind) : 1.0f;
-            be[i] = a.beta ? load_kind(a.beta, c + i, a.param_kind) : 0.0f;
-        }
+// Lanes of a workgroup over a group's channels (consecutive ones, so that a
+// chunk's pairs are read together) and, beyond them, over the chunks.
+struct GnJoin {
+    int cw, lanes, cl, kl;
+    __device__ __forceinline__ explicit GnJoin(int cpg) {
+        cw = 1;
+        while (cw < cpg && cw < (int)blockDim.x) cw *= 2;
+        lanes = (int)blockDim.x / cw;
+        cl = (int)threadIdx.x & (cw - 1);
+        kl = (int)threadIdx.x / cw;
     }
 };
+
+constexpr int kGnJoinThreads = 512;
+
+// Joins the chunks and channels of one group of one image into its statistics,
+// and writes what the apply kernel needs of each channel: mean, rstd gamma, beta.
+__global__ __launch_bounds__(kGnJoinThreads) void gn_finish_kernel(const GnArgs a) {
+    __shared__ float red[16];
+    const int n = (int)blockIdx.x / a.G, g = (int)blockIdx.x % a.G;
+    const GnJoin j(a.cpg);
+    const float* part = a.part + ((int64_t)n * a.chunks * a.C + (int64_t)g * a.cpg) * 2;
+    const float total = (float)a.HW * (float)a.cpg;
+    const int last = (int)(a.HW - (int64_t)(a.chunks - 1) * a.pixels);  // pixels of the last chunk
+    float s = 0.0f;
+    for (int c = j.cl; c < a.cpg; c += j.cw)
+        for (int k = j.kl; k < a.chunks; k += j.lanes)
+            s = __builtin_fmaf((float)(k + 1 < a.chunks ? a.pixels : last), part[((int64_t)k * a.C + c) * 2], s);
+    const float mean = block_sum(s, red) / total;
+    s = 0.0f;
+    for (int c = j.cl; c < a.cpg; c += j.cw)
+        for (int k = j.kl; k < a.chunks; k += j.lanes) {
+            const float* src = part + ((int64_t)k * a.C + c) * 2;
+            const float d = src[0] - mean;
+            s += src[1] + (float)(k + 1 < a.chunks ? a.pixels : last) * d * d;
+        }
+    const float var = block_sum(s, red) / total;
+    const float rstd = 1.0f / __builtin_sqrtf(var + a.eps);
+    if (threadIdx.x == 0 && a.mean) a.mean[blockIdx.x] = mean;
+    if (threadIdx.x == 0 && a.rstd) a.rstd[blockIdx.x] = rstd;
+    const int64_t plane = (int64_t)a.N * a.C;
+    for (int c = (int)threadIdx.x; c < a.cpg; c += (int)blockDim.x) {
+        const int64_t ch = (int64_t)g * a.cpg + c, at = (int64_t)n * a.C + ch;
+        a.coef[at] = mean;
+        a.coef[plane + at] = rstd * (a.gamma ? load_kind(a.gamma, ch, a.param_kind) : 1.0f);
+        a.coef[2 * plane + at] = a.beta ? load_kind(a.beta, ch, a.param_kind) : 0.0f;
+    }
+}
+
+// Plane k of the joined coefficients of a thread's channels.
+__device__ __forceinline__ void load_coef(const GnArgs& a, int n, int c, int k, float (&v)[8]) {
+    const float* src = a.coef + (k * (int64_t)a.N + n) * a.C + c;
+    const f32x4s_t lo = *(const f32x4s_t*)src, hi = *(const f32x4s_t*)(src + 4);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = lo[i], v[4 + i] = hi[i];
+}
 
 template <bool FP16>
 __global__ __launch_bounds__(kGnThreads) void gn_apply_kernel(const GnArgs a) {
     const GnSpot s(a);
     if (!s.on) return;
-    const GnChannels k(a, s.n, s.c);
+    float mu[8], ga[8], be[8];
+    load_coef(a, s.n, s.c, 0, mu);
+    load_coef(a, s.n, s.c, 1, ga);
+    load_coef(a, s.n, s.c, 2, be);
     const char* img = (const char*)a.x + ((int64_t)s.n * a.HW * a.ldx + s.c) * 2;
     char* out = (char*)a.out + ((int64_t)s.n * a.HW * a.ldo + s.c) * 2;
     with_act(a.act, [&](auto A) __attribute__((always_inline)) {
@@ -208,7 +233,7 @@ __global__ __launch_bounds__(kGnThreads) void gn_apply_kernel(const GnArgs a) {
                 unpack8<FP16>(w[u], v);
 #pragma unroll
                 for (int i = 0; i < 8; ++i)
-                    v[i] = act_of<ACT>(__builtin_fmaf((v[i] - k.mu[i]) * k.rs[i], k.ga[i], k.be[i]));
+                    v[i] = act_of<ACT>(__builtin_fmaf(v[i] - mu[i], ga[i], be[i]));
                 *(u32x4s_t*)(out + (p + u * a.pl) * a.ldo * 2) = pack8<FP16>(v);
             }
         }
@@ -221,10 +246,16 @@ __global__ __launch_bounds__(kGnThreads) void gn_backward_partial_kernel(const G
     __shared__ float s1[kGnThreads * 8], s2[kGnThreads * 8];
     const GnSpot s(a);
     if (s.on) {
-        const GnChannels k(a, s.n, s.c);
-        float sz[8], sx[8];
+        float mu[8], rs[8], ga[8], be[8], sz[8], sx[8];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) sz[i] = sx[i] = 0.0f;
+        for (int i = 0; i < 8; ++i) {
+            const int g = s.n * a.G + group_of(a, s.c + i);
+            mu[i] = a.mean[g];
+            rs[i] = a.rstd[g];
+            ga[i] = rs[i] * (a.gamma ? load_kind(a.gamma, s.c + i, a.param_kind) : 1.0f);
+            be[i] = a.beta ? load_kind(a.beta, s.c + i, a.param_kind) : 0.0f;
+            sz[i] = sx[i] = 0.0f;
+        }
         const char* img = (const char*)a.x + ((int64_t)s.n * a.HW * a.ldx + s.c) * 2;
         const char* grad = (const char*)a.dy + ((int64_t)s.n * a.HW * a.lddy + s.c) * 2;
         with_act(a.act, [&](auto A) __attribute__((always_inline)) {
@@ -246,10 +277,10 @@ __global__ __launch_bounds__(kGnThreads) void gn_backward_partial_kernel(const G
                     unpack8<FP16>(d[u], e);
 #pragma unroll
                     for (int i = 0; i < 8; ++i) {
-                        const float xh = (v[i] - k.mu[i]) * k.rs[i];
-                        const float dz = e[i] * act_grad_of<ACT>(__builtin_fmaf(xh, k.ga[i], k.be[i]));
+                        const float c = v[i] - mu[i];
+                        const float dz = e[i] * act_grad_of<ACT>(__builtin_fmaf(c, ga[i], be[i]));
                         sz[i] += dz;
-                        sx[i] = __builtin_fmaf(dz, xh, sx[i]);
+                        sx[i] = __builtin_fmaf(dz, c, sx[i]);
                     }
                 }
             }
@@ -257,7 +288,7 @@ __global__ __launch_bounds__(kGnThreads) void gn_backward_partial_kernel(const G
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
             s1[(s.p * a.sv + s.v) * 8 + i] = sz[i];
-            s2[(s.p * a.sv + s.v) * 8 + i] = sx[i];
+            s2[(s.p * a.sv + s.v) * 8 + i] = sx[i] * rs[i];
         }
     }
     __syncthreads();
@@ -277,31 +308,29 @@ __global__ __launch_bounds__(kGnThreads) void gn_backward_partial_kernel(const G
 }
 
 // One group of one image: its channels' sums over the chunks (kept for dgamma
-// and dbeta) and its two means.  Lanes run over channels first, then chunks.
-__global__ __launch_bounds__(256) void gn_backward_finish_kernel(const GnArgs a) {
-    __shared__ float red[2 * 256];
+// and dbeta), its two means, and the apply kernel's coefficients.
+__global__ __launch_bounds__(kGnJoinThreads) void gn_backward_finish_kernel(const GnArgs a) {
+    __shared__ float red[2 * kGnJoinThreads];
     const int n = (int)blockIdx.x / a.G, g = (int)blockIdx.x % a.G;
-    int cw = 1;
-    while (cw < a.cpg && cw < 256) cw *= 2;
-    const int lanes = 256 / cw, cl = (int)threadIdx.x % cw, kl = (int)threadIdx.x / cw;
+    const GnJoin j(a.cpg);
     const float* part = a.part + ((int64_t)n * a.chunks * a.C + (int64_t)g * a.cpg) * 2;
     float m1 = 0.0f, m2 = 0.0f;
-    for (int c0 = 0; c0 < a.cpg; c0 += cw) {
-        const int c = c0 + cl;
+    for (int c0 = 0; c0 < a.cpg; c0 += j.cw) {
+        const int c = c0 + j.cl;
         float t1 = 0.0f, t2 = 0.0f;
         if (c < a.cpg)
-            for (int k = kl; k < a.chunks; k += lanes) {
+            for (int k = j.kl; k < a.chunks; k += j.lanes) {
                 t1 += part[((int64_t)k * a.C + c) * 2];
                 t2 += part[((int64_t)k * a.C + c) * 2 + 1];
             }
         __syncthreads();
         red[threadIdx.x] = t1;
-        red[256 + threadIdx.x] = t2;
+        red[kGnJoinThreads + threadIdx.x] = t2;
         __syncthreads();
-        if (kl == 0 && c < a.cpg) {
-            for (int l = 1; l < lanes; ++l) {
-                t1 += red[l * cw + cl];
-                t2 += red[256 + l * cw + cl];
+        if (j.kl == 0 && c < a.cpg) {
+            for (int l = 1; l < j.lanes; ++l) {
+                t1 += red[l * j.cw + j.cl];
+                t2 += red[kGnJoinThreads + l * j.cw + j.cl];
             }
             const int64_t ch = (int64_t)g * a.cpg + c;
             float* dst = a.sums + ((int64_t)n * a.C + ch) * 2;
@@ -313,18 +342,23 @@ __global__ __launch_bounds__(256) void gn_backward_finish_kernel(const GnArgs a)
         }
     }
     __syncthreads();
-    const float total = (float)a.HW * (float)a.cpg;
+    const float total = (float)a.HW * (float)a.cpg, mean = a.mean[blockIdx.x], rstd = a.rstd[blockIdx.x];
     m1 = block_sum(m1, red) / total;
     m2 = block_sum(m2, red) / total;
-    if (threadIdx.x == 0) {
-        a.joined[blockIdx.x * 2] = m1;
-        a.joined[blockIdx.x * 2 + 1] = m2;
+    const int64_t plane = (int64_t)a.N * a.C;
+    for (int c = (int)threadIdx.x; c < a.cpg; c += (int)blockDim.x) {
+        const int64_t ch = (int64_t)g * a.cpg + c, at = (int64_t)n * a.C + ch;
+        a.coef[at] = mean;
+        a.coef[plane + at] = rstd * (a.gamma ? load_kind(a.gamma, ch, a.param_kind) : 1.0f);
+        a.coef[2 * plane + at] = a.beta ? load_kind(a.beta, ch, a.param_kind) : 0.0f;
+        a.coef[3 * plane + at] = -rstd * rstd * m2;
+        a.coef[4 * plane + at] = -rstd * m1;
     }
 }
 
 // dgamma and dbeta of 32 channels: the images' sums, added in order by 8 lanes a channel.
 __device__ __forceinline__ void gn_param_sums(const GnArgs& a, int block, int threads, float* red) {
-    const int t = (int)threadIdx.x, lanes = threads / 32;
+    const int t = (int)threadIdx.x, lanes = threads / 32;  // whole rows of 32 threads
     const int c = block * 32 + (t & 31), l = t >> 5;
     float t1 = 0.0f, t2 = 0.0f;
     if (c < a.C)
@@ -344,9 +378,9 @@ __device__ __forceinline__ void gn_param_sums(const GnArgs& a, int block, int th
         if (a.dgamma) store_kind(a.dgamma, c, a.param_kind, t2);
     }
 }
-__global__ __launch_bounds__(256) void gn_param_kernel(const GnArgs a) {
-    __shared__ float red[2 * 256];
-    gn_param_sums(a, (int)blockIdx.x, 256, red);
+__global__ __launch_bounds__(kGnJoinThreads) void gn_param_kernel(const GnArgs a) {
+    __shared__ float red[2 * kGnJoinThreads];
+    gn_param_sums(a, (int)blockIdx.x, kGnJoinThreads, red);
 }
 
 template <bool FP16>
@@ -358,14 +392,12 @@ __global__ __launch_bounds__(kGnThreads) void gn_backward_apply_kernel(const GnA
     }
     const GnSpot s(a);
     if (!s.on) return;
-    const GnChannels k(a, s.n, s.c);
-    float c1[8], c2[8];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        const int g = s.n * a.G + (s.c + i) / a.cpg;
-        c1[i] = a.joined[g * 2];
-        c2[i] = a.joined[g * 2 + 1];
-    }
+    float mu[8], ga[8], be[8], c2[8], c1[8];
+    load_coef(a, s.n, s.c, 0, mu);
+    load_coef(a, s.n, s.c, 1, ga);
+    load_coef(a, s.n, s.c, 2, be);
+    load_coef(a, s.n, s.c, 3, c2);
+    load_coef(a, s.n, s.c, 4, c1);
     const char* img = (const char*)a.x + ((int64_t)s.n * a.HW * a.ldx + s.c) * 2;
     const char* grad = (const char*)a.dy + ((int64_t)s.n * a.HW * a.lddy + s.c) * 2;
     char* out = (char*)a.out + ((int64_t)s.n * a.HW * a.ldo + s.c) * 2;
@@ -388,9 +420,9 @@ __global__ __launch_bounds__(kGnThreads) void gn_backward_apply_kernel(const GnA
                 unpack8<FP16>(d[u], e);
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
-                    const float xh = (v[i] - k.mu[i]) * k.rs[i];
-                    const float dz = e[i] * act_grad_of<ACT>(__builtin_fmaf(xh, k.ga[i], k.be[i]));
-                    v[i] = k.rs[i] * (__builtin_fmaf(k.ga[i], dz, -c1[i]) - xh * c2[i]);
+                    const float c = v[i] - mu[i];
+                    const float dz = e[i] * act_grad_of<ACT>(__builtin_fmaf(c, ga[i], be[i]));
+                    v[i] = __builtin_fmaf(ga[i], dz, __builtin_fmaf(c, c2[i], c1[i]));
                 }
                 *(u32x4s_t*)(out + (p + u * a.pl) * a.ldo * 2) = pack8<FP16>(v);
             }
@@ -527,7 +559,7 @@ __global__ __launch_bounds__(kGnMaxThreads) void gn_resident_kernel(const GnArgs
         be[i] = s.on && a.beta ? load_kind(a.beta, s.c + i, a.param_kind) : 0.0f;
     }
 #pragma unroll
-    for (int i = 0; i < W; ++i) gi[i] = s.on ? (s.c + i) / a.cpg - s.g0 : 0;
+    for (int i = 0; i < W; ++i) gi[i] = s.on ? group_of(a, s.c + i) - s.g0 : 0;
     const float rn = 1.0f / ((float)a.HW * (float)a.cpg);
     float acc[W], mu[W], rs[W];
 #pragma unroll
@@ -566,12 +598,12 @@ __global__ __launch_bounds__(kGnMaxThreads) void gn_resident_kernel(const GnArgs
     if (s.on && s.p == 0 && a.mean) {
 #pragma unroll
         for (int i = 0; i < W; ++i)
-            if ((s.c + i) % a.cpg == 0) a.mean[s.n * a.G + s.g0 + gi[i]] = mu[i];
+            if (s.c + i == (s.g0 + gi[i]) * a.cpg) a.mean[s.n * a.G + s.g0 + gi[i]] = mu[i];
     }
     if (s.on && s.p == 0 && a.rstd) {
 #pragma unroll
         for (int i = 0; i < W; ++i)
-            if ((s.c + i) % a.cpg == 0) a.rstd[s.n * a.G + s.g0 + gi[i]] = rs[i];
+            if (s.c + i == (s.g0 + gi[i]) * a.cpg) a.rstd[s.n * a.G + s.g0 + gi[i]] = rs[i];
     }
     if (!s.on) return;
     char* out = (char*)a.out + ((int64_t)s.n * a.HW * a.ldo + s.c) * 2;
@@ -592,60 +624,77 @@ __global__ __launch_bounds__(kGnMaxThreads) void gn_resident_kernel(const GnArgs
     });
 }
 
-// The gradient of the same: x and dy once in, dx once out.  The sums of each
-// channel go to `sums` for dgamma and dbeta, a group's to its two means.
+// The gradient, one workgroup for an image's slab of whole groups.  The sums of
+// each channel go to `sums` for dgamma and dbeta, a group's to its two means.
+// NV > 0: x and dy stay in registers between the two passes (8 bytes read, 4
+// written a pair); NV == 0: both are read again, from the caches as far as they
+// go, any number of pixels.  Work per value (two exponentials and reciprocals
+// among about 35 operations) is as long as the memory's: with registers full one
+// workgroup has the CU to itself and the two add up, so beyond four vectors a
+// thread the second form, which overlaps them, is the faster one.
 template <bool FP16, int NV, bool SINGLE>
-__global__ __launch_bounds__(kGnMaxThreads) void gn_backward_resident_kernel(const GnArgs a) {
+__global__ __launch_bounds__(kGnMaxThreads) void gn_backward_slab_kernel(const GnArgs a) {
     constexpr int W = SINGLE ? 1 : 8;
+    constexpr int U = NV > 0 ? NV : 2;  // pixels in flight
     __shared__ __attribute__((aligned(16))) float red[kGnMaxThreads * 8];
     __shared__ float chan[2 * 8 * kGnMaxVecs];  // the slab's channels, both sums
     const GnSlab s(a);
     const char* img = (const char*)a.x + ((int64_t)s.n * a.HW * a.ldx + s.c) * 2;
     const char* grad = (const char*)a.dy + ((int64_t)s.n * a.HW * a.lddy + s.c) * 2;
-    u32x4s_t x[NV], d[NV];
+    u32x4s_t x[U], d[U];
+    auto load = [&](int p0) __attribute__((always_inline)) {
 #pragma unroll
-    for (int k = 0; k < NV; ++k) {
-        const int p = s.p + k * a.pl;
-        x[k] = d[k] = u32x4s_t{0, 0, 0, 0};
-        if (s.on && p < a.HW) {
-            x[k] = *(const u32x4s_t*)(img + p * a.ldx * 2);
-            d[k] = *(const u32x4s_t*)(grad + p * a.lddy * 2);
+        for (int k = 0; k < U; ++k) {
+            const int p = p0 + k * a.pl;
+            x[k] = d[k] = u32x4s_t{0, 0, 0, 0};
+            if (s.on && p < a.HW) {
+                x[k] = *(const u32x4s_t*)(img + p * a.ldx * 2);
+                d[k] = *(const u32x4s_t*)(grad + p * a.lddy * 2);
+            }
         }
-    }
-    float mu[W], rs[W], ga[8], be[8], s1[8], s2[8];
+    };
+    load(s.p);
+    float mu[W], rs[W], ga[8], be[8], s1[8], s2[8];  // ga: rstd gamma, so z = (x - mu) ga + beta
 #pragma unroll
     for (int i = 0; i < W; ++i) {
-        const int g = s.on ? s.n * a.G + (s.c + i) / a.cpg : 0;
+        const int g = s.on ? s.n * a.G + group_of(a, s.c + i) : 0;
         mu[i] = a.mean[g];
         rs[i] = a.rstd[g];
     }
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-        ga[i] = s.on && a.gamma ? load_kind(a.gamma, s.c + i, a.param_kind) : 1.0f;
+        ga[i] = rs[i % W] * (s.on && a.gamma ? load_kind(a.gamma, s.c + i, a.param_kind) : 1.0f);
         be[i] = s.on && a.beta ? load_kind(a.beta, s.c + i, a.param_kind) : 0.0f;
         s1[i] = s2[i] = 0.0f;
     }
     with_act(a.act, [&](auto A) __attribute__((always_inline)) {
         constexpr int ACT = decltype(A)::value;
+        for (int p0 = s.p; p0 < a.HW; p0 += U * a.pl) {
+            if (NV == 0 && p0 != s.p) load(p0);
 #pragma unroll
-        for (int k = 0; k < NV; ++k) {
-            if (s.p + k * a.pl >= a.HW) break;
-            float v[8], e[8];
-            unpack8<FP16>(x[k], v);
-            unpack8<FP16>(d[k], e);
+            for (int k = 0; k < U; ++k) {
+                if (p0 + k * a.pl >= a.HW) break;
+                float v[8], e[8];
+                unpack8<FP16>(x[k], v);
+                unpack8<FP16>(d[k], e);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const float xh = (v[i] - mu[i % W]) * rs[i % W];
-                const float dz = e[i] * act_grad_of<ACT>(__builtin_fmaf(xh, ga[i], be[i]));
-                s1[i] += dz;
-                s2[i] = __builtin_fmaf(dz, xh, s2[i]);
+                for (int i = 0; i < 8; ++i) {
+                    const float c = v[i] - mu[i % W];
+                    const float dz = e[i] * act_grad_of<ACT>(__builtin_fmaf(c, ga[i], be[i]));
+                    s1[i] += dz;
+                    s2[i] = __builtin_fmaf(dz, c, s2[i]);
+                }
+                one_at_a_time();
             }
-            one_at_a_time();
+            if (NV > 0) break;
         }
     });
+#pragma unroll
+    for (int i = 0; i < 8; ++i) s2[i] *= rs[i % W];
     const int lane = (int)threadIdx.x & 63, waves = (int)(blockDim.x >> 6), nch = s.sv * 8;
     channel_sums(a, s, s1, red, chan);
     channel_sums(a, s, s2, red, chan + nch);
+    if (NV == 0) load(s.p);  // on its way during the rest of the join
     const int c0 = s.g0 * a.cpg;  // the slab's first channel
     if (a.dgamma || a.dbeta)
         for (int i = (int)threadIdx.x; i < nch; i += (int)blockDim.x) {
@@ -676,70 +725,96 @@ __global__ __launch_bounds__(kGnMaxThreads) void gn_backward_resident_kernel(con
     if (!s.on) return;
     keep_packed(x);
     keep_packed(d);
+    // dx = ga dz - (x - mu) rs^2 c2 - rs c1
     float c1[W], c2[W];
 #pragma unroll
     for (int i = 0; i < W; ++i) {
-        const int g = (s.c + i) / a.cpg - s.g0;
-        c1[i] = red[2 * g];
-        c2[i] = red[2 * g + 1];
+        const int g = group_of(a, s.c + i) - s.g0;
+        c1[i] = -rs[i] * red[2 * g];
+        c2[i] = -rs[i] * rs[i] * red[2 * g + 1];
     }
     char* out = (char*)a.out + ((int64_t)s.n * a.HW * a.ldo + s.c) * 2;
     with_act(a.act, [&](auto A) __attribute__((always_inline)) {
         constexpr int ACT = decltype(A)::value;
+        for (int p0 = s.p; p0 < a.HW; p0 += U * a.pl) {
+            if (NV == 0 && p0 != s.p) load(p0);
 #pragma unroll
-        for (int k = 0; k < NV; ++k) {
-            const int p = s.p + k * a.pl;
-            if (p >= a.HW) break;
-            float v[8], e[8];
-            unpack8<FP16>(x[k], v);
-            unpack8<FP16>(d[k], e);
+            for (int k = 0; k < U; ++k) {
+                const int p = p0 + k * a.pl;
+                if (p >= a.HW) break;
+                float v[8], e[8];
+                unpack8<FP16>(x[k], v);
+                unpack8<FP16>(d[k], e);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const float xh = (v[i] - mu[i % W]) * rs[i % W];
-                const float dz = e[i] * act_grad_of<ACT>(__builtin_fmaf(xh, ga[i], be[i]));
-                v[i] = rs[i % W] * (__builtin_fmaf(ga[i], dz, -c1[i % W]) - xh * c2[i % W]);
+                for (int i = 0; i < 8; ++i) {
+                    const float c = v[i] - mu[i % W];
+                    const float dz = e[i] * act_grad_of<ACT>(__builtin_fmaf(c, ga[i], be[i]));
+                    v[i] = __builtin_fmaf(ga[i], dz, __builtin_fmaf(c, c2[i % W], c1[i % W]));
+                }
+                *(u32x4s_t*)(out + p * a.ldo * 2) = pack8<FP16>(v);
+                one_at_a_time();
             }
-            *(u32x4s_t*)(out + p * a.ldo * 2) = pack8<FP16>(v);
-            one_at_a_time();
+            if (NV > 0) break;
         }
     });
 }
 
 // ---- host -----------------------------------------------------------------
 
+// Most vectors a thread of the resident kernels holds (of each tensor): forward
+// what 128 registers leave room for; backward a larger slab is faster read twice.
+constexpr int kGnMostForward = 16, kGnMostBackward = 4;
+constexpr int64_t kGnSlabs = 128;
+
 struct GnPlan {
-    int nv;  // resident: vectors a thread holds; 0: chunks
+    bool slab;      // one workgroup for an image's slab of groups; otherwise chunks of pixels
+    bool resident;  // the slab stays in registers
+    int nv;         // vectors a thread holds; 0: not resident
     int sv, pl, slabs, threads, chunks, pixels;
-    int64_t part_bytes, stat_bytes, sum_bytes, bytes;
+    int64_t part_bytes, coef_bytes, sum_bytes, bytes;
 };
 
-// The on-chip form: a slab of sv vectors (whole groups) of an image in one
-// workgroup of up to 1024 threads, `most` vectors a thread at most.
-static bool resident_plan(GnPlan& p, int64_t N, int64_t HW, int64_t C, int64_t G, int most) {
+// One workgroup of up to 1024 threads for an image's slab of sv vectors (whole
+// groups).  Resident where `most` vectors a thread hold it; otherwise, with
+// `stream`, read twice, if there are enough slabs for the CUs.
+static bool slab_plan(GnPlan& p, int64_t N, int64_t HW, int64_t C, int64_t G, int most, bool stream) {
     const int64_t vecs = C / 8, cpg = C / G;
     int64_t base = cpg;  // lcm(cpg, 8) / 8 vectors: the narrowest slab of whole vectors and groups
     while (base % 8 != 0) base *= 2;
     base /= 8;
-    auto fits = [&](int64_t sv) { return sv <= kGnMaxVecs && sv <= vecs && HW <= most * (kGnMaxThreads / sv); };
-    if (!fits(base)) return false;
-    int64_t sv = base;
+    if (base > kGnMaxVecs) return false;
     auto slabs = [&](int64_t v) { return N * ((vecs + v - 1) / v); };
-    // wider slabs read and write longer pieces of a pixel (up to the 128-byte line), while every CU keeps one
-    while (sv < 8 && fits(2 * sv) && slabs(2 * sv) >= 256) sv *= 2;
+    auto fits = [&](int64_t sv) { return HW <= most * (kGnMaxThreads / sv); };
+    // Wider slabs read and write longer pieces of a pixel, as long as every CU
+    // keeps one; read twice, they have 64-byte pieces at least.
+    int64_t sv = base;
+    if (!fits(base)) {
+        while (stream && sv < 4 && 2 * sv <= vecs) sv *= 2;
+        if (!stream) return false;
+    }
+    while (2 * sv <= vecs && 2 * sv <= kGnMaxVecs && slabs(2 * sv) >= 256 && (stream || fits(2 * sv))) sv *= 2;
+    // A slab of over 64 KB takes its workgroup longer than the chunks' extra
+    // launches take, unless half the CUs have one and its pieces fill half a
+    // line (forward of 8 images of 128 x 128 x 128 in 32 groups, 16-byte
+    // pieces: 66 us, chunks 30; of 32 of 56 x 56 x 256, 64-byte pieces: 26, chunks 53).
+    if (HW * sv > 4096 && (sv < 4 || slabs(sv) < kGnSlabs)) return false;
+    p.resident = fits(sv);
+    p.slab = true;
     p.sv = (int)sv;
     p.slabs = (int)((vecs + sv - 1) / sv);
-    int64_t threads = (HW * sv + 63) / 64 * 64;
+    const int64_t threads = (HW * sv + 63) / 64 * 64;
     p.threads = (int)(threads < kGnMaxThreads ? threads : kGnMaxThreads);
     p.pl = (int)(p.threads / sv);
     if (p.pl > HW) p.pl = (int)HW;
     p.nv = 1;
-    while (p.nv * (int64_t)p.pl < HW) p.nv *= 2;
-    return p.nv <= most;
+    while (p.resident && p.nv * (int64_t)p.pl < HW) p.nv *= 2;
+    if (!p.resident) p.nv = 0;
+    return true;
 }
 
-static GnPlan gn_plan(int64_t N, int64_t HW, int64_t C, int64_t G, int most) {
+static GnPlan gn_plan(int64_t N, int64_t HW, int64_t C, int64_t G, bool backward) {
     GnPlan p{};
-    if (resident_plan(p, N, HW, C, G, most)) {
+    if (slab_plan(p, N, HW, C, G, backward ? kGnMostBackward : kGnMostForward, backward)) {
         p.sum_bytes = round_up(N * C * 8, 256);
         p.bytes = p.sum_bytes;
         return p;
@@ -751,22 +826,19 @@ static GnPlan gn_plan(int64_t N, int64_t HW, int64_t C, int64_t G, int most) {
     p.pl = kGnThreads / p.sv;
     if (p.pl > HW) p.pl = (int)HW;
     p.threads = (p.pl * p.sv + 63) / 64 * 64;
-    // about eight workgroups a CU, each with at least four pixels a lane
-    int64_t chunks = N > 0 ? (2048 + N * p.slabs - 1) / (N * p.slabs) : 1;
-    const int64_t top = (HW + 4 * p.pl - 1) / (4 * p.pl);
+    // about four workgroups a CU, each with at least eight pixels a lane
+    int64_t chunks = N > 0 ? (1024 + N * p.slabs - 1) / (N * p.slabs) : 1;
+    const int64_t top = (HW + 8 * p.pl - 1) / (8 * p.pl);
     if (chunks > top) chunks = top;
     if (chunks < 1) chunks = 1;
     p.pixels = (int)((HW + chunks - 1) / chunks);
     p.chunks = (int)((HW + p.pixels - 1) / p.pixels);
     p.part_bytes = round_up(N * p.chunks * C * 8, 256);
-    p.stat_bytes = round_up(N * G * 8, 256);  // mean and rstd, or the two means of the backward pass
-    p.sum_bytes = round_up(N * C * 8, 256);
-    p.bytes = p.part_bytes + p.stat_bytes + p.sum_bytes;
+    p.coef_bytes = round_up(N * C * 4 * (backward ? 5 : 3), 256);
+    p.sum_bytes = backward ? round_up(N * C * 8, 256) : 0;
+    p.bytes = p.part_bytes + p.coef_bytes + p.sum_bytes;
     return p;
 }
-
-// Most vectors a thread of the resident kernels holds (of each tensor): what 128 registers leave room for.
-constexpr int kGnMostForward = 16, kGnMostBackward = 8;
 
 // What every entry point checks of an image tensor; 0 pixels never come here.
 static igc_status_t check_image(const void* ptr, int64_t ld, int64_t C) {
@@ -795,13 +867,13 @@ static void launch_resident(const GnArgs& a, const GnPlan& pl, hipStream_t strea
     }
 }
 template <bool FP16, bool SINGLE>
-static void launch_backward_resident(const GnArgs& a, const GnPlan& pl, hipStream_t stream) {
+static void launch_backward_slab(const GnArgs& a, const GnPlan& pl, hipStream_t stream) {
     const dim3 grid((unsigned)a.grid), block(pl.threads);
     switch (pl.nv) {
-        case 1: hipLaunchKernelGGL((gn_backward_resident_kernel<FP16, 1, SINGLE>), grid, block, 0, stream, a); break;
-        case 2: hipLaunchKernelGGL((gn_backward_resident_kernel<FP16, 2, SINGLE>), grid, block, 0, stream, a); break;
-        case 4: hipLaunchKernelGGL((gn_backward_resident_kernel<FP16, 4, SINGLE>), grid, block, 0, stream, a); break;
-        default: hipLaunchKernelGGL((gn_backward_resident_kernel<FP16, 8, SINGLE>), grid, block, 0, stream, a); break;
+        case 1: hipLaunchKernelGGL((gn_backward_slab_kernel<FP16, 1, SINGLE>), grid, block, 0, stream, a); break;
+        case 2: hipLaunchKernelGGL((gn_backward_slab_kernel<FP16, 2, SINGLE>), grid, block, 0, stream, a); break;
+        case 4: hipLaunchKernelGGL((gn_backward_slab_kernel<FP16, 4, SINGLE>), grid, block, 0, stream, a); break;
+        default: hipLaunchKernelGGL((gn_backward_slab_kernel<FP16, 0, SINGLE>), grid, block, 0, stream, a); break;
     }
 }
 
@@ -816,11 +888,12 @@ static GnArgs gn_args(const GnPlan& pl, int N, int64_t HW, int C, int G, const v
     a.C = C;
     a.G = G;
     a.cpg = C / G;
+    a.cpg_magic = fastdiv_magic((uint32_t)a.cpg);
     a.param_kind = (int)pt;
     a.act = (int)act;
     a.chunks = pl.chunks;
     a.pixels = pl.pixels;
-    a.grid = (int)((int64_t)N * (pl.nv ? 1 : pl.chunks) * pl.slabs);
+    a.grid = (int)((int64_t)N * (pl.slab ? 1 : pl.chunks) * pl.slabs);
     a.sv = pl.sv;
     a.pl = pl.pl;
     a.slabs = pl.slabs;
@@ -840,17 +913,17 @@ static igc_status_t gn_forward(int N, int H, int W, int C, int G, const void* x,
         !aligned_params(rstd, IGC_OUT_F32))
         return IGC_ERR_MISALIGNED;
     const int64_t HW = (int64_t)H * W;
-    const GnPlan pl = gn_plan(N, HW, C, G, kGnMostForward);
-    if ((int64_t)N * (pl.nv ? 1 : pl.chunks) * pl.slabs > 0x7fffffff) return IGC_ERR_UNSUPPORTED;
+    const GnPlan pl = gn_plan(N, HW, C, G, false);
+    if ((int64_t)N * (pl.slab ? 1 : pl.chunks) * pl.slabs > 0x7fffffff) return IGC_ERR_UNSUPPORTED;
     Workspace ws;
-    if (const igc_status_t st = ws.take(pl.nv ? 0 : pl.bytes, user_ws, user_ws_bytes, stream)) return st;
+    if (const igc_status_t st = ws.take(pl.slab ? 0 : pl.bytes, user_ws, user_ws_bytes, stream)) return st;
     (void)hipGetLastError();
     GnArgs a = gn_args(pl, N, HW, C, G, gamma, beta, pt, act, ws);
     a.x = x;
     a.out = y;
     a.ldx = ldx;
     a.ldo = ldy;
-    if (pl.nv) {
+    if (pl.slab) {
         a.mean = mean;
         a.rstd = rstd;
         a.eps = eps;
@@ -860,13 +933,13 @@ static igc_status_t gn_forward(int N, int H, int W, int C, int G, const void* x,
             launch_resident<FP16, false>(a, pl, stream);
         return hipGetLastError() == hipSuccess ? IGC_OK : IGC_ERR_HIP;
     }
-    float* stats = (float*)((char*)ws.ptr + pl.part_bytes);
     const unsigned grid = (unsigned)a.grid;
-    a.mean = mean ? mean : stats;
-    a.rstd = rstd ? rstd : stats + (int64_t)N * G;
+    a.coef = (float*)((char*)ws.ptr + pl.part_bytes);
+    a.mean = mean;
+    a.rstd = rstd;
     a.eps = eps;
     hipLaunchKernelGGL(gn_partial_kernel<FP16>, dim3(grid), dim3(pl.threads), 0, stream, a);
-    hipLaunchKernelGGL(gn_finish_kernel, dim3((unsigned)(N * G)), dim3(256), 0, stream, a);
+    hipLaunchKernelGGL(gn_finish_kernel, dim3((unsigned)(N * G)), dim3(kGnJoinThreads), 0, stream, a);
     hipLaunchKernelGGL(gn_apply_kernel<FP16>, dim3(grid), dim3(pl.threads), 0, stream, a);
     return hipGetLastError() == hipSuccess ? IGC_OK : IGC_ERR_HIP;
 }
@@ -888,8 +961,8 @@ static igc_status_t gn_backward(int N, int H, int W, int C, int G, const void* x
         if (!mean || !rstd) return IGC_ERR_INVALID_VALUE;
     }
     const int64_t HW = (int64_t)H * W;
-    const GnPlan pl = gn_plan(N, HW, C, G, kGnMostBackward);
-    if ((int64_t)N * (pl.nv ? 1 : pl.chunks) * pl.slabs > 0x7fffffff - (C + 31) / 32) return IGC_ERR_UNSUPPORTED;
+    const GnPlan pl = gn_plan(N, HW, C, G, true);
+    if ((int64_t)N * (pl.slab ? 1 : pl.chunks) * pl.slabs > 0x7fffffff - (C + 31) / 32) return IGC_ERR_UNSUPPORTED;
     Workspace ws;
     if (const igc_status_t st = ws.take(N > 0 ? pl.bytes : 0, user_ws, user_ws_bytes, stream)) return st;
     (void)hipGetLastError();
@@ -902,22 +975,22 @@ static igc_status_t gn_backward(int N, int H, int W, int C, int G, const void* x
     a.ldo = lddx;
     a.mean = const_cast<float*>(mean);
     a.rstd = const_cast<float*>(rstd);
-    a.joined = (float*)((char*)ws.ptr + pl.part_bytes);
-    a.sums = (float*)((char*)ws.ptr + pl.part_bytes + pl.stat_bytes);
+    a.coef = (float*)((char*)ws.ptr + pl.part_bytes);
+    a.sums = (float*)((char*)ws.ptr + pl.part_bytes + pl.coef_bytes);
     a.dgamma = dgamma;
     a.dbeta = dbeta;
     const unsigned params = dgamma || dbeta ? (unsigned)((C + 31) / 32) : 0;
-    if (N > 0 && !pl.nv) {
+    if (N > 0 && !pl.slab) {
         hipLaunchKernelGGL(gn_backward_partial_kernel<FP16>, dim3((unsigned)a.grid), dim3(pl.threads), 0, stream, a);
-        hipLaunchKernelGGL(gn_backward_finish_kernel, dim3((unsigned)(N * G)), dim3(256), 0, stream, a);
+        hipLaunchKernelGGL(gn_backward_finish_kernel, dim3((unsigned)(N * G)), dim3(kGnJoinThreads), 0, stream, a);
         hipLaunchKernelGGL(gn_backward_apply_kernel<FP16>, dim3((unsigned)a.grid + params), dim3(pl.threads), 0, stream,
                            a);
     } else {
         if (N > 0 && a.cpg % 8 == 0)
-            launch_backward_resident<FP16, true>(a, pl, stream);
+            launch_backward_slab<FP16, true>(a, pl, stream);
         else if (N > 0)
-            launch_backward_resident<FP16, false>(a, pl, stream);
-        if (params) hipLaunchKernelGGL(gn_param_kernel, dim3(params), dim3(256), 0, stream, a);
+            launch_backward_slab<FP16, false>(a, pl, stream);
+        if (params) hipLaunchKernelGGL(gn_param_kernel, dim3(params), dim3(kGnJoinThreads), 0, stream, a);
     }
     return hipGetLastError() == hipSuccess ? IGC_OK : IGC_ERR_HIP;
 }
@@ -965,8 +1038,8 @@ IGC_GN_BACKWARD(group_norm_nhwc_backward_fp16, true)
 int64_t igc_group_norm_workspace_bytes(int N, int H, int W, int C, int G) {
     if (check_shape(N, H, W, C, G, IGC_OUT_F32, IGC_ACT_NONE) != IGC_OK) return -1;
     if (N == 0) return 0;
-    const int64_t forward = gn_plan(N, (int64_t)H * W, C, G, kGnMostForward).bytes;
-    const int64_t backward = gn_plan(N, (int64_t)H * W, C, G, kGnMostBackward).bytes;
+    const int64_t forward = gn_plan(N, (int64_t)H * W, C, G, false).bytes;
+    const int64_t backward = gn_plan(N, (int64_t)H * W, C, G, true).bytes;
     return forward > backward ? forward : backward;
 }
 
