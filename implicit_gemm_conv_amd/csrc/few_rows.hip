@@ -4,16 +4,22 @@
 // straight into MFMA operands in registers, with no LDS on the way, and A,
 // small enough to stay in the caches, is read beside it.
 //
-// A workgroup's eight waves cut its K range among them in turns of UK and add
-// their fp32 sums through LDS; where N alone gives too few workgroups K is cut
-// across workgroups too (splits), and the split epilogue adds those partials.
+// A workgroup's waves cut its K range among them in turns of UK and add their
+// fp32 sums through LDS; where N alone gives too few workgroups K is cut across
+// workgroups too (splits), and the split epilogue adds those partials.
 //
-// B column-major (K contiguous): 16 columns a workgroup; a lane loads eight
-// consecutive k of one column, which is an operand of the 16x16x32 MFMA as it
-// lies.  B row-major (N contiguous): 16*VC columns a workgroup; a lane loads VC
-// consecutive columns of eight k rows and turns them into VC operands with one
+// A workgroup covers 16*NB columns.  B column-major (K contiguous): NB blocks
+// of 16; a lane loads eight consecutive k of one column, which is an operand of
+// the 16x16x32 MFMA as it lies.  B row-major (N contiguous): a lane loads NB
+// consecutive columns of eight k rows and turns them into NB operands with one
 // byte permute per register (two k of one column from two rows), so the MFMA's
-// column index is every VC-th column.
+// column index is every NB-th column.
+//
+// Measured (weights from memory, not the caches): 1 x 4096 x 4096 8.0 us
+// column-major and 12.0 row-major (33.6 MB), 1 x 16384 x 4096 21.5 and 22.3 (6.2
+// TB/s); the 128 x 128 tiles take 36, 35, 24 and 24.  What is left at 4096 is a
+// launch, a first load and the join: 2 us beyond the bytes.  A through LDS
+// instead of straight from the caches measured no faster.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
@@ -22,7 +28,6 @@
 
 namespace igc {
 
-constexpr int kFewWaves = 8;
 
 typedef __attribute__((ext_vector_type(2))) unsigned u32x2f_t;
 
@@ -47,32 +52,35 @@ __device__ __forceinline__ u32x4s_t load_k8(const char* base, uint32_t off, int6
     }
 }
 
-// One 32-deep step of B for a wave: NB operands of 8 k per lane.
-template <bool B_KC, int VC>
+// One 32-deep step of B for a wave: NB operands of 8 k per lane.  B_KC: NB
+// blocks of 16 columns; else the NB neighbouring columns of one load.
+template <bool B_KC, int NB>
 struct BStep {
-    static constexpr int NB = B_KC ? 1 : VC;
-    static constexpr int NW = B_KC ? 4 : 4 * VC;  // 32-bit words per lane
-    unsigned w[NW];
+    unsigned w[4 * NB];
 
-    // `base`: the step's first k in column n0; `off`: the lane's eight k and its column, or first of its VC columns.
-    // k: the lane's first k
+    // `base`: the step's first k in column n0; off[j]: the lane's eight k and its column of block j (B_KC), off[0]:
+    // its eight k and first column.  k: the lane's first k
     template <bool MASKED>
-    __device__ __forceinline__ void load(const char* base, uint32_t off, int64_t ldb, int64_t k, int64_t end) {
+    __device__ __forceinline__ void load(const char* base, const uint32_t (&off)[B_KC ? NB : 1], int64_t ldb, int64_t k,
+                                         int64_t end) {
         if constexpr (B_KC) {
-            const u32x4s_t v = load_k8<MASKED>(base, off, k, end);
 #pragma unroll
-            for (int i = 0; i < 4; ++i) w[i] = v[i];
+            for (int j = 0; j < NB; ++j) {
+                const u32x4s_t v = load_k8<MASKED>(base, off[j], k, end);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) w[4 * j + i] = v[i];
+            }
         } else {
 #pragma unroll
             for (int kk = 0; kk < 8; ++kk) {
                 const bool in = !MASKED || k + kk < end;
-                const char* r = base + kk * ldb * 2 + off;
-                if constexpr (VC == 8) {
+                const char* r = base + kk * ldb * 2 + off[0];
+                if constexpr (NB == 8) {
                     u32x4s_t v{0, 0, 0, 0};
                     if (in) v = *(const u32x4s_t*)r;
 #pragma unroll
                     for (int i = 0; i < 4; ++i) w[kk * 4 + i] = v[i];
-                } else if constexpr (VC == 4) {
+                } else if constexpr (NB == 4) {
                     u32x2f_t v{0, 0};
                     if (in) v = *(const u32x2f_t*)r;
                     w[kk * 2] = v[0], w[kk * 2 + 1] = v[1];
@@ -86,27 +94,26 @@ struct BStep {
     __device__ __forceinline__ i16x8_t operand(int j) const {
         u32x4s_t v;
         if constexpr (B_KC) {
-            v = u32x4s_t{w[0], w[1], w[2], w[3]};
+            v = u32x4s_t{w[4 * j], w[4 * j + 1], w[4 * j + 2], w[4 * j + 3]};
         } else {
             const unsigned sel = j & 1 ? 0x07060302u : 0x05040100u;
 #pragma unroll
             for (int i = 0; i < 4; ++i)
-                v[i] = __builtin_amdgcn_perm(w[(2 * i + 1) * (VC / 2) + j / 2], w[2 * i * (VC / 2) + j / 2], sel);
+                v[i] = __builtin_amdgcn_perm(w[(2 * i + 1) * (NB / 2) + j / 2], w[2 * i * (NB / 2) + j / 2], sel);
         }
         return __builtin_bit_cast(i16x8_t, v);
     }
 };
 
-template <bool FP16, bool B_KC, int MT, int VC>
-__global__ __launch_bounds__(64 * kFewWaves) void few_rows_kernel(const FewRowsArgs a, const Epi e) {
-    using Step = BStep<B_KC, VC>;
-    constexpr int NB = Step::NB;
+// MT: 16-row blocks of A; WAVES; U: 32-deep steps a turn.
+template <bool FP16, bool B_KC, int MT, int NB, int WAVES, int U>
+__global__ __launch_bounds__(64 * WAVES) void few_rows_kernel(const FewRowsArgs a, const Epi e) {
+    using Step = BStep<B_KC, NB>;
     constexpr int COLS = 16 * NB;            // columns of the workgroup
-    constexpr int U = B_KC ? 4 : (VC == 8 ? 1 : (VC == 4 ? 2 : 4));  // 32-deep steps a turn
     constexpr int UK = 32 * U;
     constexpr int E = MT * 16 * COLS;        // elements of the workgroup
-    constexpr int EPT = (E + 64 * kFewWaves - 1) / (64 * kFewWaves);
-    __shared__ float red[kFewWaves * E];     // [wave][operand block][lane][4]
+    constexpr int EPT = (E + 64 * WAVES - 1) / (64 * WAVES);
+    __shared__ __attribute__((aligned(16))) float red[WAVES * E];  // [wave][operand block][lane][4]
 
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int r = lane & 15, g = lane >> 4;
@@ -120,11 +127,13 @@ __global__ __launch_bounds__(64 * kFewWaves) void few_rows_kernel(const FewRowsA
     const char* bbase = (const char*)a.B + (B_KC ? n0 * a.ldb : n0) * 2;
     const int64_t bstep = B_KC ? 2 : a.ldb * 2;  // bytes from one k to the next
     const int left = a.N - n0 < COLS ? (int)(a.N - n0) : COLS;
-    uint32_t boff;
+    uint32_t boff[B_KC ? NB : 1];
     if constexpr (B_KC) {
-        boff = (uint32_t)((r < left ? r : left - 1) * a.ldb + 8 * g) * 2;
+#pragma unroll
+        for (int j = 0; j < NB; ++j)
+            boff[j] = (uint32_t)((16 * j + r < left ? 16 * j + r : left - 1) * a.ldb + 8 * g) * 2;
     } else {
-        boff = (uint32_t)(8 * g * a.ldb + (VC * r < left ? VC * r : (left - 1) / VC * VC)) * 2;
+        boff[0] = (uint32_t)(8 * g * a.ldb + (NB * r < left ? NB * r : (left - 1) / NB * NB)) * 2;
     }
     uint32_t aoff[MT];
 #pragma unroll
@@ -135,7 +144,7 @@ __global__ __launch_bounds__(64 * kFewWaves) void few_rows_kernel(const FewRowsA
     if (a.splits == 1) {
 #pragma unroll
         for (int t = 0; t < EPT; ++t) {
-            const int x = (int)threadIdx.x + t * 64 * kFewWaves, m = x / COLS, c = x % COLS;
+            const int x = (int)threadIdx.x + t * 64 * WAVES, m = x / COLS, c = x % COLS;
             if (x < E && m < a.M && c < left) el[t].fetch(e, m, n0 + c);
         }
     }
@@ -146,6 +155,7 @@ __global__ __launch_bounds__(64 * kFewWaves) void few_rows_kernel(const FewRowsA
 #pragma unroll
         for (int j = 0; j < NB; ++j) acc[i][j] = f32x4_t{0, 0, 0, 0};
 
+    // B of two turns in flight
     Step cur[U], nxt[U];
     auto load_b = [&](Step (&s)[U], int64_t k) __attribute__((always_inline)) {
         const char* base = bbase + k * bstep;
@@ -161,30 +171,29 @@ __global__ __launch_bounds__(64 * kFewWaves) void few_rows_kernel(const FewRowsA
     };
     int64_t k = kbase + (int64_t)wave * UK;
     load_b(cur, k);
-    for (; k < kend; k += kFewWaves * UK) {
-        i16x8_t fa[U][MT];
-        const char* abase = (const char*)a.A + k * 2;
+    for (; k < kend; k += WAVES * UK) {
+        u32x4s_t fa[U][MT];
+        const char* base = (const char*)a.A + k * 2;
         if (k + UK <= kend) {
 #pragma unroll
             for (int u = 0; u < U; ++u)
 #pragma unroll
-                for (int i = 0; i < MT; ++i)
-                    fa[u][i] = __builtin_bit_cast(i16x8_t, load_k8<false>(abase + 64 * u, aoff[i], 0, 0));
+                for (int i = 0; i < MT; ++i) fa[u][i] = load_k8<false>(base + 64 * u, aoff[i], 0, 0);
         } else {
 #pragma unroll
             for (int u = 0; u < U; ++u)
 #pragma unroll
-                for (int i = 0; i < MT; ++i)
-                    fa[u][i] = __builtin_bit_cast(i16x8_t, load_k8<true>(abase + 64 * u, aoff[i], k + 32 * u + 8 * g, kend));
+                for (int i = 0; i < MT; ++i) fa[u][i] = load_k8<true>(base + 64 * u, aoff[i], k + 32 * u + 8 * g, kend);
         }
-        load_b(nxt, k + kFewWaves * UK);
+        load_b(nxt, k + WAVES * UK);
 #pragma unroll
         for (int u = 0; u < U; ++u)
 #pragma unroll
             for (int j = 0; j < NB; ++j) {
                 const i16x8_t fb = cur[u].operand(j);
 #pragma unroll
-                for (int i = 0; i < MT; ++i) acc[i][j] = mfma<FP16>(fb, fa[u][i], acc[i][j]);
+                for (int i = 0; i < MT; ++i)
+                    acc[i][j] = mfma<FP16>(fb, __builtin_bit_cast(i16x8_t, fa[u][i]), acc[i][j]);
             }
 #pragma unroll
         for (int u = 0; u < U; ++u) cur[u] = nxt[u];
@@ -195,17 +204,18 @@ __global__ __launch_bounds__(64 * kFewWaves) void few_rows_kernel(const FewRowsA
 #pragma unroll
         for (int j = 0; j < NB; ++j) *(f32x4_t*)&red[((wave * MT + i) * NB + j) * 256 + lane * 4] = acc[i][j];
     __syncthreads();
-    // element (m, c) of the workgroup: block (m/16, j), lane 16*(q/4) + m%16, word q%4, with c = NB*q + j
+    // element (m, c) of the workgroup: block (m/16, j), lane 16*(q/4) + m%16, word q%4, where column c is number q of
+    // operand j: c = 16*j + q (B_KC) or NB*q + j
 #pragma unroll
     for (int t = 0; t < EPT; ++t) {
-        const int x = (int)threadIdx.x + t * 64 * kFewWaves;
+        const int x = (int)threadIdx.x + t * 64 * WAVES;
         const int m = x / COLS, c = x % COLS;
         if (m >= a.M || c >= left || x >= E) continue;
-        const int j = c % NB, q = c / NB;
+        const int j = B_KC ? c / 16 : c % NB, q = B_KC ? c % 16 : c / NB;
         const float* src = &red[((m >> 4) * NB + j) * 256 + ((q >> 2) * 16 + (m & 15)) * 4 + (q & 3)];
         float s = src[0];
 #pragma unroll
-        for (int w = 1; w < kFewWaves; ++w) s += src[w * E];
+        for (int w = 1; w < WAVES; ++w) s += src[w * E];
         if (a.splits > 1)
             a.ws[((int64_t)split * a.M + m) * a.ldws + n0 + c] = s;
         else
@@ -217,16 +227,20 @@ FewRowsPlan few_rows_plan(int64_t M, int64_t N, int64_t K, bool b_kc) {
     constexpr int64_t kCUs = 256;
     const int64_t mt = (M + 15) / 16;
     FewRowsPlan pl{};
-    pl.vc = 1;
-    if (!b_kc) {
-        // the widest loads that still give every CU a workgroup; MT * VC blocks of sums share 64 KB of LDS
-        pl.vc = mt == 1 ? 8 : (mt == 2 ? 4 : 2);
-        while (pl.vc > 2 && (N + 16 * pl.vc - 1) / (16 * pl.vc) < kCUs) pl.vc /= 2;
-    }
-    pl.cols = (N + 16 * pl.vc - 1) / (16 * pl.vc);
-    // K is cut across workgroups while CUs are idle and every part keeps 1024
+    // The widest operand blocks that still give every CU a workgroup: B
+    // row-major reads longer pieces of its rows, and with several blocks of A
+    // each is read for more columns (64 x 16384 x 4096: 55 us with two blocks,
+    // 82 with one).  One block of A gains nothing from more columns of B.
+    pl.nb = b_kc ? (mt == 1 ? 1 : (mt == 2 ? 4 : 2)) : (mt == 1 ? 8 : (mt == 2 ? 4 : 2));
+    while (pl.nb > (b_kc ? 1 : 2) && (N + 16 * pl.nb - 1) / (16 * pl.nb) < kCUs) pl.nb /= 2;
+    pl.cols = (N + 16 * pl.nb - 1) / (16 * pl.nb);
+    // K is cut across workgroups while CUs are idle and every part is long
+    // enough to pay for the second launch (1 x 1024 x 4096: column-major 7.0 us
+    // whole, 7.7 in four; row-major, whose workgroups are twice as wide, 11.3
+    // whole, 9.4 in four; 64 x 1024 x 16384 93 whole, 23 in eight).
     int64_t s = pl.cols > 0 ? kCUs / pl.cols : 1;
-    if (s > K / 1024) s = K / 1024;
+    const int64_t part = b_kc ? 4096 : 1024;
+    if (s > K / part) s = K / part;
     if (s < 1) s = 1;
     const int64_t per = (K + s - 1) / s;
     pl.per = (per + 127) / 128 * 128;
@@ -235,34 +249,40 @@ FewRowsPlan few_rows_plan(int64_t M, int64_t N, int64_t K, bool b_kc) {
     return pl;
 }
 
-template <bool FP16, bool B_KC, int MT, int VC>
+template <bool FP16, bool B_KC, int MT, int NB>
 static hipError_t go(const FewRowsArgs& a, const Epi& e, hipStream_t stream) {
-    hipLaunchKernelGGL((few_rows_kernel<FP16, B_KC, MT, VC>), dim3((unsigned)(a.cols * a.splits)),
-                       dim3(64 * kFewWaves), 0, stream, a, e);
+    // Eight waves; sixteen for B row-major where 128 registers hold their operands, whose smaller turns spread
+    // better (17 x 8192 x 2048 12.3 -> 11.1 us).  A turn holds 16 to 32 KB of B a workgroup.
+    constexpr int W = !B_KC && MT <= 2 && NB <= 4 ? 16 : 8;
+    constexpr int U = B_KC ? 4 / NB : (W == 16 ? 4 / NB : 8 / NB);
+    hipLaunchKernelGGL((few_rows_kernel<FP16, B_KC, MT, NB, W, U>), dim3((unsigned)(a.cols * a.splits)), dim3(64 * W), 0,
+                       stream, a, e);
     return hipGetLastError();
 }
 
-template <bool FP16>
-static hipError_t pick_few(const FewRowsArgs& a, const Epi& e, bool b_kc, int vc, hipStream_t st) {
+template <bool FP16, bool B_KC>
+static hipError_t pick_few(const FewRowsArgs& a, const Epi& e, int nb, hipStream_t st) {
     const int mt = (a.M + 15) / 16;
-    if (b_kc) {
-        switch (mt) {
-            case 1: return go<FP16, true, 1, 1>(a, e, st);
-            case 2: return go<FP16, true, 2, 1>(a, e, st);
-            case 3: return go<FP16, true, 3, 1>(a, e, st);
-            default: return go<FP16, true, 4, 1>(a, e, st);
+    if constexpr (B_KC) {
+        if (mt == 1) return go<FP16, true, 1, 1>(a, e, st);
+        if (nb == 1) {
+            if (mt == 2) return go<FP16, true, 2, 1>(a, e, st);
+            if (mt == 3) return go<FP16, true, 3, 1>(a, e, st);
+            return go<FP16, true, 4, 1>(a, e, st);
         }
+    } else if (mt == 1) {
+        if (nb == 8) return go<FP16, false, 1, 8>(a, e, st);
+        if (nb == 4) return go<FP16, false, 1, 4>(a, e, st);
+        return go<FP16, false, 1, 2>(a, e, st);
     }
-    if (mt == 1)
-        return vc == 8 ? go<FP16, false, 1, 8>(a, e, st)
-                       : (vc == 4 ? go<FP16, false, 1, 4>(a, e, st) : go<FP16, false, 1, 2>(a, e, st));
-    if (mt == 2) return vc == 4 ? go<FP16, false, 2, 4>(a, e, st) : go<FP16, false, 2, 2>(a, e, st);
-    if (mt == 3) return go<FP16, false, 3, 2>(a, e, st);
-    return go<FP16, false, 4, 2>(a, e, st);
+    if (mt == 2) return nb == 4 ? go<FP16, B_KC, 2, 4>(a, e, st) : go<FP16, B_KC, 2, 2>(a, e, st);
+    if (mt == 3) return go<FP16, B_KC, 3, 2>(a, e, st);
+    return go<FP16, B_KC, 4, 2>(a, e, st);
 }
 
-hipError_t launch_few_rows(const FewRowsArgs& a, const Epi& e, bool fp16, bool b_kc, int vc, hipStream_t stream) {
-    return fp16 ? pick_few<true>(a, e, b_kc, vc, stream) : pick_few<false>(a, e, b_kc, vc, stream);
+hipError_t launch_few_rows(const FewRowsArgs& a, const Epi& e, bool fp16, bool b_kc, int nb, hipStream_t stream) {
+    if (fp16) return b_kc ? pick_few<true, true>(a, e, nb, stream) : pick_few<true, false>(a, e, nb, stream);
+    return b_kc ? pick_few<false, true>(a, e, nb, stream) : pick_few<false, false>(a, e, nb, stream);
 }
 
 }  // namespace igc

@@ -8,11 +8,15 @@ namespace igc {
 struct Epi;
 
 constexpr int64_t kFewRows = 64;  // most rows the kernel takes
+// Beyond 16 rows every workgroup's reads of A weigh as much as its columns of
+// B, and with many columns the 128 x 128 tiles, which share them, are faster:
+// 48 x 8192 x 4096 24 us against 30 on tiles, 32 x 16384 x 4096 32 against 27.
+constexpr int64_t kFewRowsColumns = 400000;  // largest M * N with more than 16 rows
 
-// How a product of M <= kFewRows rows is cut: VC columns a lane (B row-major),
+// How a product of M <= kFewRows rows is cut: NB operands of 16 columns a wave,
 // `cols` workgroups across N, `splits` along K (each `per` of K).
 struct FewRowsPlan {
-    int vc;
+    int nb;
     int64_t cols;
     int splits;
     int64_t per;
@@ -27,6 +31,6 @@ struct FewRowsArgs {
     int64_t N, K, lda, ldb, ldc, ldws, per;
     int M, cols, splits, out_kind;
 };
-hipError_t launch_few_rows(const FewRowsArgs& a, const Epi& e, bool fp16, bool b_kc, int vc, hipStream_t stream);
+hipError_t launch_few_rows(const FewRowsArgs& a, const Epi& e, bool fp16, bool b_kc, int nb, hipStream_t stream);
 
 }  // namespace igc

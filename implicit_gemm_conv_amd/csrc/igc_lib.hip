@@ -355,8 +355,8 @@ static igc_status_t check_epilogue(const igc_epilogue_t* q, int64_t N, bool dens
 // Whether a product runs on the kernel of few_rows.hip: at most kFewRows rows,
 // row-major A, and the 32-bit lane offsets of its loads in range.
 static bool takes_few_rows(int64_t M, int64_t N, int64_t K, int64_t lda, bool a_kc, int64_t ldb, bool b_kc) {
-    return a_kc && M >= 1 && M <= kFewRows && N < (1ll << 30) && K < (1ll << 31) && M * lda * 2 < 0x7fffffffLL &&
-           ((b_kc ? 16 : 32) * ldb + 256) * 2 < 0x7fffffffLL;
+    return a_kc && M >= 1 && M <= kFewRows && (M <= 16 || M * N <= kFewRowsColumns) && N < (1ll << 30) && K < (1ll << 31) && M * lda * 2 < 0x7fffffffLL &&
+           (64 * ldb + 256) * 2 < 0x7fffffffLL;
 }
 static int64_t few_rows_bytes(const FewRowsPlan& pl, int64_t M, int64_t N) {
     return pl.splits > 1 ? round_up(pl.splits * M * round_up(N, 4) * 4, 256) : 0;
@@ -386,7 +386,7 @@ static igc_status_t few_rows(bool fp16, int64_t M, int64_t N, int64_t K, const v
     a.cols = (int)pl.cols;
     a.splits = pl.splits;
     a.out_kind = (int)ct;
-    hipError_t err = launch_few_rows(a, e, fp16, b_kc, pl.vc, stream);
+    hipError_t err = launch_few_rows(a, e, fp16, b_kc, pl.nb, stream);
     if (err == hipSuccess && pl.splits > 1)
         err = launch_split_epilogue(a.ws, pl.splits, M * a.ldws, M, N, a.ldws, C, ldc, (int)ct, true, e, stream);
     return err == hipSuccess ? IGC_OK : IGC_ERR_HIP;
