@@ -159,20 +159,38 @@ igc_tune_t default_tune(int64_t M, int64_t N, int64_t K, int op) {
     return small;
 }
 
-// As default_tune, except that the shapes it gives to stream-K (128 x 128 tiles
-// that leave CUs idle, a deep K, and no even split) split K instead: the split
-// count that leaves the fewest CU rounds for one part's share, at least 1024 of
-// K a part, with the smaller count (fewer partial sums) on a tie.
+// As default_tune, except for the 128 x 128 tiles, which give way to 256 x 128
+// where those need half the rounds, never run as stream-K, and split K where the parts and their join cost less than the whole: a K tile
+// of 64 takes 0.3 us with half of the CUs busy and 0.5 with all of them, a join
+// a launch (3.6 us) and the partials twice through memory at 3 TB/s.  Measured
+// with the epilogue, whole against the count taken: 128 x 1024 x 2048 14.6 and
+// 11.8 us (4 parts), 1000 x 512 x 8192 43.4 and 24.5 (4), 200 x 4096 x 2048 15.5
+// whole and 19.6 in two.
 igc_tune_t epilogue_tune(int64_t M, int64_t N, int64_t K, int op) {
     igc_tune_t t = default_tune(M, N, K, op);
-    if (t.stream_k <= 0) return t;
+    if (t.bm != 128 || t.bn != 128) return t;
     constexpr int64_t kCUs = 256;
-    const int64_t tiles = ((M + t.bm - 1) / t.bm) * ((N + t.bn - 1) / t.bn);
+    // Two rounds of 128 x 128 tiles against one of 256 x 128: 1024 x 8192 x 1024 27 and 22 us, 1536 x 4096 x 4096
+    // 63 and 50 (192 tiles); with 160 tiles they tie or lose (1000 x 5000 x 1024 23 and 25).
+    const int64_t tall = ((M + 255) / 256) * ((N + 127) / 128), rounds_tall = (tall + kCUs - 1) / kCUs;
+    if (op == IGC_OP_GEMM && t.stream_k == 0 && t.k_splits <= 1 && tall * 10 >= rounds_tall * kCUs * 7 &&
+        (((M + 127) / 128) * ((N + 127) / 128) + kCUs - 1) / kCUs >= 2 * rounds_tall)
+        return igc_tune_t{256, 128, 64, 3, 8, 16, 0, 4, 1, 0, 0, 0};
+    const int64_t tiles = ((M + 127) / 128) * ((N + 127) / 128), steps = (K + 63) / 64;
     t.stream_k = 0;
-    int64_t best = 1;
-    for (int64_t s = 2; s <= 16 && K / s >= 1024; ++s)
-        if (((tiles * s + kCUs - 1) / kCUs) * best < ((tiles * best + kCUs - 1) / kCUs) * s) best = s;
-    t.k_splits = best > 1 ? (int)best : 0;
+    t.k_splits = 0;
+    double best = 0;
+    for (int64_t s = 1; s <= 16 && (s == 1 || (K / s >= 512 && tiles * s <= kCUs)); ++s) {
+        const int64_t rounds = (tiles * s + kCUs - 1) / kCUs;
+        const double busy = tiles * s >= kCUs ? 1.0 : (double)(tiles * s) / (double)kCUs;
+        const double step = busy <= 0.5 ? 0.3 : 0.1 + 0.4 * busy;
+        double cost = step * (double)((steps + s - 1) / s * rounds);
+        if (s > 1) cost += 3.6 + (double)s * (double)M * (double)N * 8.0 / 3e6;
+        if (s == 1 || cost < best) {
+            best = cost;
+            t.k_splits = s > 1 ? (int)s : 0;
+        }
+    }
     return t;
 }
 

@@ -297,6 +297,94 @@ def test_two_streams_at_once():
     b.check(db, "stream b")
 
 
+def test_two_threads_at_once():
+    """Calls from two host threads, each with its own stream and problem, plain entry points (pool workspaces)."""
+    import threading
+    problems = [Problem(30, 300, 9000, "bf16", lb="row", act="gelu", seed=41), Problem(400, 300, 8192, "fp16", seed=42)]
+    outs = [torch.full((p.dims[0] + 2, p.ldd), float("nan"), dtype=p.out, device="cuda") for p in problems]
+    torch.cuda.synchronize()
+    failed = []
+
+    def work(p, D, stream):
+        try:
+            for _ in range(20):
+                p.run(D=D, stream=stream)
+        except Exception as e:  # noqa: BLE001
+            failed.append(e)
+
+    threads = [threading.Thread(target=work, args=(p, D, torch.cuda.Stream())) for p, D in zip(problems, outs)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    assert not failed
+    for p, D in zip(problems, outs):
+        p.check(D, "threads")
+
+
+def test_built_in_choices():
+    """Sizes that the built-in choice gives to each kind of tile and schedule, ragged."""
+    for M, N, K in ((1300, 4104, 72), (4000, 4100, 40), (129, 1025, 2056), (60, 9000, 104), (16, 9001, 72), (64, 6250, 64)):
+        for lb in ("col", "row"):
+            say(f"built-in {M}x{N}x{K} {lb}")
+            p = Problem(M, N, K, "bf16", lb=lb, act="silu", pre="in" if M != 1300 else None, seed=M)
+            p.check(p.run(), f"{M}x{N}x{K} {lb}")
+
+
+def test_parameters_at_odd_addresses():
+    """bias needs only its own type's alignment."""
+    for M in (3, 100):
+        p = Problem(M, 72, 64, "fp16", bias="f16", seed=6)
+        shifted = torch.empty(80, dtype=torch.float16, device="cuda")
+        shifted[3:75] = p.bias
+        p.bias = shifted[3:75]
+        p.check(p.run(), "odd bias")
+
+
+def test_long_leading_dimensions():
+    """Rows so far apart that offsets within the output, residual and pre pass 32 bits, and within a tile nearly 31."""
+    M, N, K, ld = 600, 64, 64, (1 << 21) - 8
+    g = generator(8)
+    A, B = normal(g, M, K, dtype=torch.bfloat16).cuda(), normal(g, N, K, scale=0.125, dtype=torch.bfloat16).cuda()
+    R = normal(g, M, N, dtype=torch.bfloat16).cuda()
+    bufs = [torch.empty(M * ld, dtype=torch.bfloat16, device="cuda") for _ in range(3)]  # 2.5 GB each, hardly touched
+    res, pre, D = (b.view(M, ld) for b in bufs)
+    res[:, :N] = R
+    igc.check(igc.gemm_bf16_epilogue(M, N, K, A, K, 0, B, K, 1, D, ld, igc.OUT_BF16,
+                                     igc.Epilogue(act="silu", residual=res, pre=pre)))
+    synchronize()
+    a, b = A.double(), B.double()
+    z, S = a @ b.t(), a.abs() @ b.abs().t()
+    ez, y = (K + 2) * U32 * S, act64(z, "silu")
+    assert_within(pre[:, :N], z, ez, "pre")
+    assert_within(D[:, :N], y + R.double(), ez * ACT_LIP + ACT_REL * (1 + z * z) * y.abs() + U32 * (y.abs() + R.double().abs()))
+    far = (1 << 22)  # 256 rows of it pass 2^31 bytes: refused
+    tune = igc.tune((256, 256, 64, 2, 8, 16, 1, 4))
+    for e in (igc.Epilogue(residual=1 << 20, ldr=far, residual_type=igc.OUT_BF16), igc.Epilogue(pre=1 << 20, ldp=far, pre_type=1)):
+        assert igc.gemm_bf16_epilogue_ex(M, N, K, A, K, 0, B, K, 1, D, ld, igc.OUT_BF16, e, tune) == igc.IGC_ERR_UNSUPPORTED
+
+
+def test_long_weights_of_few_rows():
+    """Weights of more than 2^32 bytes in both layouts; the last rows and columns are checked."""
+    M, N, K = 2, 70000, 32768
+    A = normal(generator(1), M, K, dtype=torch.bfloat16).cuda()
+    for lb in ("col", "row"):
+        say(f"long weights {lb}")
+        B = torch.empty((N, K) if lb == "col" else (K, N), dtype=torch.bfloat16, device="cuda")
+        B.normal_(generator=torch.Generator(device="cuda").manual_seed(3))
+        D = torch.full((M, N), float("nan"), device="cuda")
+        igc.check(igc.gemm_bf16_epilogue(M, N, K, A, K, 0, B, B.stride(0), 1 if lb == "col" else 0, D, N, igc.OUT_F32,
+                                         igc.Epilogue(act="none")))
+        synchronize()
+        assert torch.isfinite(D).all()
+        for n0 in (0, 34990, N - 24):
+            b = (B[n0:n0 + 24] if lb == "col" else B[:, n0:n0 + 24].t()).double()
+            a = A.double()
+            assert_within(D[:, n0:n0 + 24].contiguous(), a @ b.t(), (K + 2) * U32 * (a.abs() @ b.abs().t()), f"{lb} {n0}")
+        del B
+
+
 # ---- convolution ------------------------------------------------------------------------------------------------------
 
 CONV = {"bf16": igc.conv2d_nhwc_implicit_gemm_epilogue_ex, "fp16": igc.conv2d_nhwc_implicit_gemm_epilogue_fp16_ex}

@@ -138,6 +138,7 @@ SHAPES = [
     (2, 8, 8, 1280, 32), (16, 3, 3, 320, 32), (1, 13, 17, 2056, 1),           # one group over more than one workgroup
     (2, 33, 31, 64, 8), (1, 100, 90, 32, 32), (1, 300, 211, 8, 2), (5, 56, 56, 256, 32), (1, 64, 64, 4096, 64),
     (2, 47, 53, 320, 32), (2, 70, 70, 96, 4), (1, 120, 130, 128, 1),
+    (40, 30, 34, 64, 8), (33, 61, 40, 48, 16), (16, 32, 32, 640, 32), (9, 128, 120, 64, 64), (130, 40, 33, 40, 4),
 ]
 
 
@@ -220,6 +221,28 @@ def test_in_place():
         p.x = keep.clone()
         out = p.backward(dx=p.x)
         p.check_backward(*out, "dx = x")
+
+
+def test_pixels_far_apart():
+    """A channel slice of a tensor so wide that offsets pass 32 bits, in one workgroup a slab and in chunks."""
+    for (N, H, W, C, G), ld in (((2, 64, 64, 32, 4), 300000), ((2, 40, 40, 64, 2), 700000)):
+        g = generator(3)
+        x = normal(g, N, H, W, C, dtype=torch.bfloat16).cuda()
+        wide = torch.empty(N * H * W * ld, dtype=torch.bfloat16, device="cuda").view(N, H, W, ld)  # hardly touched
+        wide[..., :C] = x
+        gamma = torch.ones(C, device="cuda")
+        y, z, dx, dz = (torch.empty_like(x) for _ in range(4))
+        mean, rstd = (torch.empty(N, G, device="cuda") for _ in range(2))
+        igc.check(igc.group_norm_nhwc_bf16(N, H, W, C, G, x, C, gamma, None, 0, EPS, "silu", y, C, mean, rstd))
+        igc.check(igc.group_norm_nhwc_bf16(N, H, W, C, G, wide, ld, gamma, None, 0, EPS, "silu", z, C))
+        igc.check(igc.group_norm_nhwc_backward_bf16(N, H, W, C, G, x, C, gamma, None, 0, mean, rstd, "silu", y, C, dx, C))
+        igc.check(igc.group_norm_nhwc_backward_bf16(N, H, W, C, G, wide, ld, gamma, None, 0, mean, rstd, "silu", y, C, dz, C))
+        synchronize()
+        assert torch.equal(y, z) and torch.equal(dx, dz)
+        igc.check(igc.group_norm_nhwc_bf16(N, H, W, C, G, wide, ld, gamma, None, 0, EPS, "silu", wide, ld))  # in place
+        synchronize()
+        assert torch.equal(wide[..., :C], y)
+        del wide
 
 
 def test_caller_workspace_gives_the_same_bits():
