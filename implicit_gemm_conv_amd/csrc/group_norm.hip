@@ -775,10 +775,9 @@ struct GnPlan {
 };
 
 // One workgroup of up to 1024 threads for an image's slab of sv vectors (whole
-// groups).  Resident where `most` vectors a thread hold it; otherwise, with
-// `stream`, read twice, if there are enough slabs for the CUs.
-static bool slab_plan(GnPlan& p, int64_t N, int64_t HW, int64_t C, int64_t G, int most, bool stream) {
-    const int64_t vecs = C / 8, cpg = C / G;
+// groups).  Resident where the threads can hold it; backward also read twice.
+static bool slab_plan(GnPlan& p, int64_t N, int64_t HW, int64_t C, int64_t G, bool backward) {
+    const int64_t vecs = C / 8, cpg = C / G, most = backward ? kGnMostBackward : kGnMostForward;
     int64_t base = cpg;  // lcm(cpg, 8) / 8 vectors: the narrowest slab of whole vectors and groups
     while (base % 8 != 0) base *= 2;
     base /= 8;
@@ -789,10 +788,10 @@ static bool slab_plan(GnPlan& p, int64_t N, int64_t HW, int64_t C, int64_t G, in
     // keeps one; read twice, they have 64-byte pieces at least.
     int64_t sv = base;
     if (!fits(base)) {
-        while (stream && sv < 4 && 2 * sv <= vecs) sv *= 2;
-        if (!stream) return false;
+        while (backward && sv < 4 && 2 * sv <= vecs) sv *= 2;
+        if (!backward) return false;
     }
-    while (2 * sv <= vecs && 2 * sv <= kGnMaxVecs && slabs(2 * sv) >= 256 && (stream || fits(2 * sv))) sv *= 2;
+    while (2 * sv <= vecs && 2 * sv <= kGnMaxVecs && slabs(2 * sv) >= 256 && (backward || fits(2 * sv))) sv *= 2;
     // A slab of over 64 KB takes its workgroup longer than the chunks' extra
     // launches take, unless half the CUs have one and its pieces fill half a
     // line (forward of 8 images of 128 x 128 x 128 in 32 groups, 16-byte
@@ -802,7 +801,16 @@ static bool slab_plan(GnPlan& p, int64_t N, int64_t HW, int64_t C, int64_t G, in
     p.slab = true;
     p.sv = (int)sv;
     p.slabs = (int)((vecs + sv - 1) / sv);
-    const int64_t threads = (HW * sv + 63) / 64 * 64;
+    // Several vectors a thread: what a thread does once (indexes, parameters,
+    // its part of the joins) costs as much as four vectors.  Eight forward and
+    // four backward, down to 256 threads (forward of 16 of 27 x 27 x 320 12.5
+    // us, 15.3 with 1024 threads; of 2 of 16 x 16 x 1280 7.2 and 9.9; backward
+    // of 16 of 16 x 16 x 512 13.2 and 15.2).
+    const int64_t held = HW * sv, least = backward ? (held < 256 ? held : 256) : (held < 512 ? held / 2 : 256);
+    int64_t threads = held / (backward ? 4 : 8);
+    threads = threads < least ? least : threads;
+    threads = threads < sv ? sv : threads;
+    threads = (threads + 63) / 64 * 64;
     p.threads = (int)(threads < kGnMaxThreads ? threads : kGnMaxThreads);
     p.pl = (int)(p.threads / sv);
     if (p.pl > HW) p.pl = (int)HW;
@@ -814,7 +822,7 @@ static bool slab_plan(GnPlan& p, int64_t N, int64_t HW, int64_t C, int64_t G, in
 
 static GnPlan gn_plan(int64_t N, int64_t HW, int64_t C, int64_t G, bool backward) {
     GnPlan p{};
-    if (slab_plan(p, N, HW, C, G, backward ? kGnMostBackward : kGnMostForward, backward)) {
+    if (slab_plan(p, N, HW, C, G, backward)) {
         p.sum_bytes = round_up(N * C * 8, 256);
         p.bytes = p.sum_bytes;
         return p;
