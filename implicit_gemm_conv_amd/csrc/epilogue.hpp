@@ -278,7 +278,7 @@ __device__ __forceinline__ void epi_passes(ML& ml, const typename C::Acc (&acc)[
 }
 
 // The data-parallel kernel of mainloop.hpp with the epilogue above.  (A K
-// split runs the plain kernel and applies the epilogue to the summed partials.)
+// split writes fp32 partials and applies the epilogue to their sum.)
 template <class C, int V, bool BWD>
 __global__ __launch_bounds__(C::NT) void gemm_epi_kernel(const Params p, const Epi e) {
     static_assert(variant_applies<C, V>(), "loop variant of another operation");
@@ -298,6 +298,57 @@ __global__ __launch_bounds__(C::NT) void gemm_epi_kernel(const Params p, const E
         for (int i = 0; i < 8; ++i) bias[i] = e.bias && n0 + i < p.N ? load_kind(e.bias, n0 + i, e.bias_kind) : 0.0f;
         ring_barrier();  // every wave has finished reading the ring
         epi_passes<C, 0, BWD>(ml, acc, stage_piece<C, PIECE>(ml.wave), p, e, bias, lane);
+    });
+}
+
+// One split of a K split: the fp32 partial tile to the workspace, staged like
+// the epilogue so that it is written as whole row segments whatever M and N
+// (the plain kernel's stores fall back to single elements in edge tiles: 100 x
+// 200 x 8192 in 16 parts 16.5 us with them, 11.4 staged; 1000 x 512 x 8192 in
+// 4 parts 24.4 and 20.1).  Columns up to ldws, N rounded up to 4, are the
+// workspace's own.  A kernel of its own: with the split's indexes in
+// gemm_epi_kernel the 256 x 256 tiles lost 1 us of 35.
+template <class C, int V>
+__global__ __launch_bounds__(C::NT) void gemm_part_kernel(const Params p) {
+    constexpr int PIECE = 4 * 16 * C::WTN * 4, RB = C::WTN * 4, CPR = RB / 16;
+    constexpr int RPI = 64 / CPR;  // rows a group: a lane holds one chunk
+    static_assert(stage_pieces<C, PIECE>() >= C::NW, "the ring holds every wave's staged rows");
+    const int T = p.tiles_m * p.tiles_n;
+    const int id = xcd_order((int)blockIdx.x, T * p.k_splits);
+    const int split = id / T;
+    int tm, tn;
+    group_coords(id - split * T, p.tiles_m, p.tiles_n, p.group_m, tm, tn);
+    const int64_t kbase = (int64_t)split * p.k_per_split;
+    const int64_t kend = kbase + p.k_per_split < p.K ? kbase + p.k_per_split : p.K;
+    run_tile<C, V>(p, tm, tn, kbase, kend, [&](auto& ml, auto& acc) __attribute__((always_inline)) {
+        int lane = ml.lane;
+        asm volatile("" : "+v"(lane));
+        IGC_LDS char* reg = stage_piece<C, PIECE>(ml.wave);
+        ring_barrier();  // every wave has finished reading the ring
+        static_for<0, (C::FM + 3) / 4>([&](auto PASS) __attribute__((always_inline)) {
+            constexpr int I0 = 4 * PASS, NI = C::FM - I0 < 4 ? C::FM - I0 : 4;
+#pragma unroll
+            for (int i = 0; i < NI; ++i)
+#pragma unroll
+                for (int j = 0; j < C::FN; ++j) {
+                    const int row = 16 * i + (lane & 15), c = 4 * j + (lane >> 4);
+                    *(IGC_LDS f32x4_t*)(reg + row * RB + ((c ^ (row & (CPR - 1))) << 4)) = acc[I0 + i][j];
+                }
+            const int row0 = lane / CPR, c = lane % CPR;
+            const int64_t m0 = ml.m0 + ml.wm * C::WTM + 16 * I0, n0 = ml.n0 + ml.wn * C::WTN;
+            const int rows = n0 + 4 * c < p.ldws ? (p.M - (m0 + row0) < 4096 ? (int)(p.M - (m0 + row0)) : 4096) : 0;
+            const EpiMatrix out(p.ws + (int64_t)split * p.ws_stride, p.ldws, KIND_F32, m0, n0, row0, 4 * c, RPI);
+            wait_lgkmcnt0();
+            compiler_fence();
+#pragma unroll
+            for (int q = 0; q < NI * 16 / RPI; ++q) {
+                const int row = q * RPI + row0;
+                const u32x4s_t v = *(const IGC_LDS u32x4s_t*)(reg + row * RB + ((c ^ (row & (CPR - 1))) << 4));
+                out.store(q, q * RPI < rows, 0, v);
+            }
+            wait_lgkmcnt0();
+            compiler_fence();
+        });
     });
 }
 

@@ -20,6 +20,16 @@ constexpr const void* kernel_of() {
         return reinterpret_cast<const void*>(&gemm_epi_kernel<C, V, BWD>);
 }
 
+// The built-in choice splits K on tiles of up to 256 x 128; larger ones, split
+// only by request, keep the plain kernel.
+template <class C, int V>
+constexpr const void* part_of() {
+    if constexpr (!variant_applies<C, V>() || C::BM * C::BN > 256 * 128)
+        return nullptr;
+    else
+        return reinterpret_cast<const void*>(&gemm_part_kernel<C, V>);
+}
+
 template <bool FP16, bool AKC, bool BKC, int OPK>
 EpiInstance entry() {
     using C = Here<FP16, AKC, BKC, OPK>;
@@ -27,7 +37,9 @@ EpiInstance entry() {
                        {{kernel_of<C, PLAIN, false>(), kernel_of<C, UNIFORM_TAP, false>(),
                          kernel_of<C, RAGGED, false>(), kernel_of<C, CONV_GENERIC, false>()},
                         {kernel_of<C, PLAIN, true>(), kernel_of<C, UNIFORM_TAP, true>(), kernel_of<C, RAGGED, true>(),
-                         kernel_of<C, CONV_GENERIC, true>()}}};
+                         kernel_of<C, CONV_GENERIC, true>()}},
+                       {part_of<C, PLAIN>(), part_of<C, UNIFORM_TAP>(), part_of<C, RAGGED>(),
+                        part_of<C, CONV_GENERIC>()}};
 }
 
 static const EpiInstance kTable[] = {

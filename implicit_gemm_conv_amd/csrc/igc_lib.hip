@@ -244,15 +244,17 @@ static igc_status_t launch(const Plan& pl, Params p, const Epi* epi, void* user_
     const int v = loop_variant(p, inst);
     const void* fn = L.G > 0 ? inst->fn_sk[v] : inst->fn[v];
     if (epi && L.G > 0) return IGC_ERR_UNSUPPORTED;
+    const EpiInstance* ei = epi ? find_epilogue(*inst) : nullptr;
     if (epi && L.S == 1 && !loose) {
         // the kernel's offsets within a tile are 32-bit
         const auto span = [&](int64_t ld, int kind) { return inst->bm * ld * (kind == OUT_F32 ? 4 : 2) >= 0x7fff0000LL; };
         if (span(p.ldc, p.out_kind) || (epi->res && span(epi->ldr, epi->res_kind)) ||
             (epi->pre && span(epi->ldp, epi->pre_kind)))
             return IGC_ERR_UNSUPPORTED;
-        const EpiInstance* ei = find_epilogue(*inst);
         fn = ei ? ei->fn[epi->backward ? 1 : 0][v] : nullptr;
     }
+    // parts of a K split through staged stores, where they are built and the sub-tile's offsets fit
+    if (ei && L.S > 1 && ei->part[v] && inst->bm * L.ldws * 4 < 0x7fff0000LL) fn = ei->part[v];
     if (!fn) return IGC_ERR_UNSUPPORTED;
     if (user_ws && (user_ws_bytes < L.bytes || (reinterpret_cast<uintptr_t>(user_ws) & 255u)))
         return IGC_ERR_INVALID_VALUE;

@@ -24,6 +24,7 @@ struct EpiInstance {
     int op;
     bool fp16, a_kc, b_kc;
     const void* fn[2][4];  // forward and backward, by loop variant; nullptr where not built
+    const void* part[4];   // one part of a K split, for the epilogue to follow
 };
 
 // Each compiled object (one configuration, one operation family) registers

@@ -160,12 +160,13 @@ igc_tune_t default_tune(int64_t M, int64_t N, int64_t K, int op) {
 }
 
 // As default_tune, except for the 128 x 128 tiles, which give way to 256 x 128
-// where those need half the rounds, never run as stream-K, and split K where the parts and their join cost less than the whole: a K tile
-// of 64 takes 0.3 us with half of the CUs busy and 0.5 with all of them, a join
-// a launch (3.6 us) and the partials twice through memory at 3 TB/s.  Measured
-// with the epilogue, whole against the count taken: 128 x 1024 x 2048 14.6 and
-// 11.8 us (4 parts), 1000 x 512 x 8192 43.4 and 24.5 (4), 200 x 4096 x 2048 15.5
-// whole and 19.6 in two.
+// where those need half the rounds, never run as stream-K, and split K where the
+// parts and their join cost less than the whole: a K tile of 64 takes 0.3 us
+// with half of the CUs busy and 0.5 with all of them, a join a launch (3.6 us)
+// and the partials twice through memory at 3 TB/s.  Measured with the epilogue,
+// whole against the count taken: 128 x 1024 x 2048 14.5 and 10.7 us (4 parts),
+// 1000 x 512 x 8192 43.1 and 20.0 (4), 200 x 4096 x 2048 14.9 whole and 16.3 in
+// two.
 igc_tune_t epilogue_tune(int64_t M, int64_t N, int64_t K, int op) {
     igc_tune_t t = default_tune(M, N, K, op);
     if (t.bm != 128 || t.bn != 128) return t;
