@@ -160,36 +160,52 @@ igc_tune_t default_tune(int64_t M, int64_t N, int64_t K, int op) {
 }
 
 // As default_tune, except for the 128 x 128 tiles, which give way to 256 x 128
-// where those need half the rounds, never run as stream-K, and split K where the
-// parts and their join cost less than the whole: a K tile of 64 takes 0.3 us
-// with half of the CUs busy and 0.5 with all of them, a join a launch (3.6 us)
-// and the partials twice through memory at 3 TB/s.  Measured with the epilogue,
-// whole against the count taken: 128 x 1024 x 2048 14.5 and 10.7 us (4 parts),
-// 1000 x 512 x 8192 43.1 and 20.0 (4), 200 x 4096 x 2048 14.9 whole and 16.3 in
-// two.
+// where those need half the rounds, to 64 x 64 and 64 x 128 where a round holds
+// their tiles, never run as stream-K, and split K where the parts and their join
+// cost less than the whole; and for the 64-column tiles of the convolution,
+// which give way to the same smaller tiles (7326 x 48 x 936, 58 tiles of 128 x
+// 64: 17.1 us, 115 of 64 x 64 9.4; 12032 x 72 x 192, 188 and 188 of 64 x 128: 7.7
+// and 6.5).
 igc_tune_t epilogue_tune(int64_t M, int64_t N, int64_t K, int op) {
     igc_tune_t t = default_tune(M, N, K, op);
-    if (t.bm != 128 || t.bn != 128) return t;
     constexpr int64_t kCUs = 256;
+    const bool narrow = t.bn == 64 && ((M + 63) / 64) * ((N + 127) / 128) <= kCUs;
+    if (!narrow && (t.bm != 128 || t.bn != 128)) return t;
     // Two rounds of 128 x 128 tiles against one of 256 x 128: 1024 x 8192 x 1024 27 and 22 us, 1536 x 4096 x 4096
     // 63 and 50 (192 tiles); with 160 tiles they tie or lose (1000 x 5000 x 1024 23 and 25).
     const int64_t tall = ((M + 255) / 256) * ((N + 127) / 128), rounds_tall = (tall + kCUs - 1) / kCUs;
     if (op == IGC_OP_GEMM && t.stream_k == 0 && t.k_splits <= 1 && tall * 10 >= rounds_tall * kCUs * 7 &&
         (((M + 127) / 128) * ((N + 127) / 128) + kCUs - 1) / kCUs >= 2 * rounds_tall)
         return igc_tune_t{256, 128, 64, 3, 8, 16, 0, 4, 1, 0, 0, 0};
-    const int64_t tiles = ((M + 127) / 128) * ((N + 127) / 128), steps = (K + 63) / 64;
-    t.stream_k = 0;
-    t.k_splits = 0;
-    double best = 0;
-    for (int64_t s = 1; s <= 16 && (s == 1 || (K / s >= 512 && tiles * s <= kCUs)); ++s) {
-        const int64_t rounds = (tiles * s + kCUs - 1) / kCUs;
-        const double busy = tiles * s >= kCUs ? 1.0 : (double)(tiles * s) / (double)kCUs;
-        const double step = busy <= 0.5 ? 0.3 : 0.1 + 0.4 * busy;
-        double cost = step * (double)((steps + s - 1) / s * rounds);
-        if (s > 1) cost += 3.6 + (double)s * (double)M * (double)N * 8.0 / 3e6;
-        if (s == 1 || cost < best) {
-            best = cost;
-            t.k_splits = s > 1 ? (int)s : 0;
+    // A convolution of shallow K in several rounds of 128 x 128 tiles is bound by its loads and stores, as with up to
+    // 256 filters: 22176 x 304 x 160 23.5 us and 15.7 with 64 columns, 25088 x 288 x 864 37.5 and 27.4,
+    // 20480 x 320 x 1024 29.3 and 26.5.
+    if (op == IGC_OP_CONV_FPROP && t.bn == 128 && K <= 1024 && ((M + 127) / 128) * ((N + 127) / 128) > kCUs)
+        return igc_tune_t{256, 64, 64, 2, 8, 16, 0, 4, 1, 0, 0, 0};
+    // What a schedule costs, in us: launch, first loads and epilogue; a 64-deep K tile, which the latency of its
+    // loads bounds, not its MFMAs, until half of the CUs are busy; for a split a second launch and the partials
+    // twice through memory at 3 TB/s.  Fitted to 39 shapes in two operand layouts, where the choice takes 1.1% more
+    // than the best of them all (geometric mean); 128 x 128 against the choice: 1024 x 1024 x 1024 10.6 and 7.1 us
+    // (64 x 64), 777 x 1336 x 520 8.9 and 7.4 (64 x 128), 2048 x 1024 x 4096 26.8 and 22.0 (64 x 128),
+    // 1000 x 512 x 8192 42.8 and 17.4 (64 x 128 in 4), 100 x 200 x 8192 38.3 and 9.6 (64 x 64 in 16).
+    constexpr struct {
+        int bm, bn;
+        double fixed, step, busier;  // step: a K tile with half of the CUs busy, plus up to busier / 2 beyond
+    } kinds[] = {{64, 64, 4.0, 0.18, 0.06}, {64, 128, 4.4, 0.24, 0.04}, {128, 128, 5.6, 0.3, 0.4}};
+    double best = -1;
+    for (const auto& q : kinds) {
+        const int64_t tiles = ((M + q.bm - 1) / q.bm) * ((N + q.bn - 1) / q.bn), steps = (K + 63) / 64;
+        if (q.bm == 64 ? tiles > kCUs : narrow) continue;
+        for (int64_t s = 1; s <= 16 && (s == 1 || (K / s >= 256 && tiles * s <= kCUs)); ++s) {
+            const int64_t rounds = (tiles * s + kCUs - 1) / kCUs;
+            const double busy = tiles * s >= kCUs ? 1.0 : (double)(tiles * s) / (double)kCUs;
+            const double step = q.step + (busy > 0.5 ? (busy - 0.5) * q.busier : 0.0);
+            double cost = q.fixed + step * (double)((steps + s - 1) / s * rounds);
+            if (s > 1) cost += 3.2 + (double)s * (double)M * (double)N * 8.0 / 3e6;
+            if (best < 0 || cost < best) {
+                best = cost;
+                t = igc_tune_t{q.bm, q.bn, 64, 4, 8, 16, 0, 4, s > 1 ? (int)s : 0, 0, 0, 0};
+            }
         }
     }
     return t;

@@ -25,6 +25,8 @@
     X(256, 256, 32, 4, 8, 16, 0, 4, 0, 3)     \
     X(128, 128, 64, 4, 4, 32, 0, 0, 0, 3)     \
     X(256, 128, 64, 3, 8, 16, 0, 4, 0, 11)    \
+    X(64, 64, 64, 4, 8, 16, 0, 4, 0, 9)       \
+    X(64, 128, 64, 4, 8, 16, 0, 4, 0, 9)      \
     X(256, 256, 32, 2, 8, 32, 0, 4, 0, 0)     \
     X(256, 256, 32, 3, 8, 32, 0, 4, 0, 0)     \
     X(256, 256, 32, 4, 8, 32, 0, 4, 0, 0)     \

@@ -540,3 +540,81 @@ def test_linear_layer_gradients_against_differences():
         diff = (loss(*up.values()) - loss(*down.values())) / (2 * h)
         got, tol = (grad.double() * v).sum(), (etol[name] * v.abs()).sum() + 1e-6 * diff.abs() + 1e-6
         assert (got - diff).abs() <= tol, (name, float(got), float(diff), float(tol))
+
+
+# ---- schedules in parts ---------------------------------------------------------------------------------------------
+
+GEMM_TILES = [c for c in igc.tunes(igc.SCOPE_EPILOGUE) if c in igc.tunes(igc.SCOPE_ALL)]
+
+
+@pytest.mark.parametrize("cfg", GEMM_TILES, ids=str)
+def test_parts_of_every_tile(cfg):
+    """K splits of each configuration: every operand layout, edge tiles, rows no vector fits, K not a multiple of 8."""
+    for M, N, K, la, lb, dtype in ((261, 133, 1030, "row", "col", "bf16"), (70, 300, 777, "row", "row", "fp16"),
+                                   (130, 68, 641, "col", "col", "bf16"), (200, 259, 1024, "col", "row", "fp16")):
+        for s in (2, 3):
+            say(f"parts {cfg} {M}x{N}x{K} {la} {lb} {dtype} {s}")
+            p = Problem(M, N, K, dtype, la=la, lb=lb, act="gelu_tanh", pre="out", seed=M + s)
+            p.check(p.run(tune=igc.tune(cfg, k_splits=s)), f"{cfg} {M}x{N}x{K} in {s}")
+
+
+@pytest.mark.parametrize("cfg", igc.tunes(igc.SCOPE_EPILOGUE), ids=str)
+def test_convolution_parts_of_every_tile(cfg):
+    """The same of the convolution, with filter counts that no vector fits."""
+    for geometry in ((2, 12, 12, 128, 13, 3, 3, 1, 1), (1, 17, 16, 72, 300, 3, 3, 1, 1), (2, 11, 9, 256, 72, 1, 1, 1, 0)):
+        for s in (1, 2, 3):
+            say(f"conv parts {cfg} {geometry} {s}")
+            conv_case(*geometry, "bf16", "silu", tune=igc.tune(cfg, k_splits=s if s > 1 else 0), seed=s)
+            conv_case(*geometry, "fp16", "relu", residual=False, tune=igc.tune(cfg, k_splits=s if s > 1 else 0), seed=s)
+
+
+def test_built_in_choices_of_small_outputs():
+    """Sizes that take 64-row tiles, whole and in parts, and the convolution's 64-column tiles."""
+    for M, N, K in ((200, 300, 100), (1000, 1500, 72), (65, 1, 8), (300, 300, 3001), (77, 6230, 3061), (1990, 1020, 136)):
+        for la, lb in (("row", "col"), ("row", "row"), ("col", "row"), ("col", "col")):
+            say(f"built-in {M}x{N}x{K} {la} {lb}")
+            p = Problem(M, N, K, "fp16", la=la, lb=lb, act="gelu", pre="in" if K == 100 else None, seed=K)
+            p.check(p.run(), f"{M}x{N}x{K} {la} {lb}")
+    for geometry in ((2, 30, 20, 48, 72, 3, 3, 1, 1), (1, 14, 14, 256, 264, 3, 3, 1, 1), (9, 57, 33, 40, 296, 1, 1, 1, 0),
+                     (3, 9, 9, 8, 5, 1, 1, 1, 0)):
+        say(f"built-in conv {geometry}")
+        conv_case(*geometry, "bf16", "gelu_tanh", seed=4)
+
+
+# ---- extreme values -------------------------------------------------------------------------------------------------
+
+@pytest.mark.parametrize("act", ACTS)
+def test_activation_over_the_whole_range(act):
+    """An empty sum leaves z = bias: every binade of fp32, both signs, and the neighbourhood of 0.
+
+    Forward, |error| <= ACT_REL * (1 + z^2) * |act(z)| where the exponential's rounding counts (|z| < 15; beyond it a
+    tail is below 2^-126 or the result is z to the last bit), plus |z| * 2^-125 for tails below the normal numbers, which
+    the hardware's exp2 and reciprocal flush.  Backward, GRAD_ABS and the same flushed tails (|z| * 2^-125 < 2^-120)."""
+    z = torch.cat([torch.ldexp(torch.linspace(1, 2, 9)[:-1].double(), torch.arange(-126, 127).double()[:, None]).reshape(-1),
+                   torch.linspace(0, 15, 4001).double()]).float()
+    z = torch.cat([z, -z, torch.tensor([float("nan"), float("inf")])]).contiguous()
+    N = z.numel()
+    zd = z.double()
+    A = torch.zeros(1, 8, dtype=torch.bfloat16, device="cuda")
+    D = torch.full((2, (N + 7) // 8 * 8), 7.0, device="cuda")
+    b = z.cuda()
+    igc.check(igc.gemm_bf16_epilogue(1, N, 0, A, 8, 0, A, D.stride(0), 0, D, D.stride(0), igc.OUT_F32,
+                                     igc.Epilogue(act=act, bias=b)))
+    synchronize()
+    got, want = D[0, :N].double().cpu(), act64(zd, act)
+    fin = torch.isfinite(zd) & torch.isfinite(want)
+    tol = ACT_REL * (1 + torch.clamp(zd.abs(), max=15) ** 2) * want.abs() + zd.abs() * 2.0 ** -125 + 2.0 ** -125
+    assert ((got - want).abs()[fin] <= (tol + U32 * want.abs())[fin]).all()
+    assert torch.isnan(got[-2]) and got[-1] == float("inf")
+    assert (D[0, N:] == 7.0).all() and (D[1] == 7.0).all()
+    pre = torch.zeros(1, D.stride(0), device="cuda")
+    pre[0, :N] = b
+    D.fill_(7.0)
+    ones = torch.ones(N, device="cuda")
+    igc.check(igc.gemm_bf16_epilogue(1, N, 0, A, 8, 0, A, D.stride(0), 0, D, D.stride(0), igc.OUT_F32,
+                                     igc.Epilogue(act=act, bias=ones, pre=pre, backward=True)))
+    synchronize()
+    got, want = D[0, :N].double().cpu(), act_grad64(torch.clamp(zd, -1e4, 1e4), act)
+    fin = torch.isfinite(zd)
+    assert ((got - want).abs()[fin] <= GRAD_ABS).all()
+    assert act == "none" or torch.isnan(got[-2])
