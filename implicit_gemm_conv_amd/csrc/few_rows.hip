@@ -1,4 +1,4 @@
-// few_rows.hip -- D = epilogue(A * B) for at most 64 rows of A, the products
+// few_rows.hip -- D = epilogue(A * B) for at most 32 rows of A, the products
 // of single tokens and small batches.  B, the weights, is read once and is all
 // that counts: every workgroup streams its own columns of B from memory
 // straight into MFMA operands in registers, with no LDS on the way, and A,
@@ -15,11 +15,11 @@
 // byte permute per register (two k of one column from two rows), so the MFMA's
 // column index is every NB-th column.
 //
-// Measured (weights from memory, not the caches): 1 x 4096 x 4096 8.0 us
-// column-major and 12.0 row-major (33.6 MB), 1 x 16384 x 4096 21.5 and 22.3 (6.2
-// TB/s); the 128 x 128 tiles take 36, 35, 24 and 24.  What is left at 4096 is a
-// launch, a first load and the join: 2 us beyond the bytes.  A through LDS
-// instead of straight from the caches measured no faster.
+// Measured (weights from memory, not the caches): 1 x 4096 x 4096 column-major
+// 9.2 us (33.6 MB, 3.6 TB/s), 1 x 16384 x 4096 32.2 and row-major 28.2 (4.8
+// TB/s), 1 x 1024 x 1024 3.7 and 5.5.  What is left at 4096 is a launch, a first
+// load and the join: 2 us beyond the bytes.  A through LDS instead of straight
+// from the caches measured no faster.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
@@ -27,7 +27,6 @@
 #include "few_rows.hpp"
 
 namespace igc {
-
 
 typedef __attribute__((ext_vector_type(2))) unsigned u32x2f_t;
 
@@ -223,25 +222,36 @@ __global__ __launch_bounds__(64 * WAVES) void few_rows_kernel(const FewRowsArgs 
     }
 }
 
+// Against the 64-row tiles of the fused epilogue, whose waves share a tile of A
+// and of B and which split K further (time here / time there, geometric means
+// over weights in and out of the caches):
+//   K <= 2048, N <= 8192, 12 shapes: column-major 0.58 with one row, 0.64 with
+//   16, 0.76 with 32; row-major 0.77, 0.89, 1.01 with 24 and 1.08 with 32;
+//   larger: column-major with K >= 2048 0.85 with one row, 0.92 with 8, 1.04
+//   with 16 (with a smaller K up to 1.28); row-major 0.99 and 1.04, but 0.90 and
+//   0.96 for N >= 16384, where a workgroup reads longer pieces of its rows.
+bool few_rows_faster(int64_t M, int64_t N, int64_t K, bool b_kc) {
+    if (K <= 2048 && N <= 8192) return M <= (b_kc ? kFewRows : 20);
+    return M <= 8 && (b_kc ? K >= 2048 : N >= 16384);
+}
+
 FewRowsPlan few_rows_plan(int64_t M, int64_t N, int64_t K, bool b_kc) {
     constexpr int64_t kCUs = 256;
-    const int64_t mt = (M + 15) / 16;
     FewRowsPlan pl{};
-    // The widest operand blocks that still give every CU a workgroup: B
-    // row-major reads longer pieces of its rows, and with several blocks of A
-    // each is read for more columns (64 x 16384 x 4096: 55 us with two blocks,
-    // 82 with one).  One block of A gains nothing from more columns of B.
-    pl.nb = b_kc ? (mt == 1 ? 1 : (mt == 2 ? 4 : 2)) : (mt == 1 ? 8 : (mt == 2 ? 4 : 2));
-    while (pl.nb > (b_kc ? 1 : 2) && (N + 16 * pl.nb - 1) / (16 * pl.nb) < kCUs) pl.nb /= 2;
-    pl.cols = (N + 16 * pl.nb - 1) / (16 * pl.nb);
-    // K is cut across workgroups while CUs are idle and every part is long
-    // enough to pay for the second launch (1 x 1024 x 4096: column-major 7.0 us
-    // whole, 7.7 in four; row-major, whose workgroups are twice as wide, 11.3
-    // whole, 9.4 in four; 64 x 1024 x 16384 93 whole, 23 in eight).
-    int64_t s = pl.cols > 0 ? kCUs / pl.cols : 1;
-    const int64_t part = b_kc ? 4096 : 1024;
-    if (s > K / part) s = K / part;
-    if (s < 1) s = 1;
+    const auto cols = [&](int64_t nb) { return (N + 16 * nb - 1) / (16 * nb); };
+    // B row-major: the widest operand blocks that still give every CU a
+    // workgroup (1 x 16384 x 4096: 28 us with four, 40 with two; 1 x 65536 x 1024:
+    // 28.5 with eight, 30.4 with four).  Column-major gains nothing from more.
+    pl.nb = b_kc ? 1 : (M <= 16 && cols(8) >= kCUs ? 8 : (M <= 16 && cols(4) >= kCUs ? 4 : 2));
+    pl.cols = cols(pl.nb);
+    // K is cut across workgroups while CUs are idle and the parts save more than
+    // the second launch costs (column-major 1 x 512 x 16000: 9.8 us in six or eight,
+    // 12.0 in three; 1 x 1000 x 4096 7.3 whole, 8.2 in two).
+    int64_t s = 1;
+    if (b_kc && K >= 6144 && pl.cols > 0) {
+        s = kCUs / pl.cols < K / 2048 ? kCUs / pl.cols : K / 2048;
+        if (s < 1) s = 1;
+    }
     const int64_t per = (K + s - 1) / s;
     pl.per = (per + 127) / 128 * 128;
     pl.splits = K > 0 ? (int)((K + pl.per - 1) / pl.per) : 1;
@@ -253,8 +263,8 @@ template <bool FP16, bool B_KC, int MT, int NB>
 static hipError_t go(const FewRowsArgs& a, const Epi& e, hipStream_t stream) {
     // Eight waves; sixteen for B row-major where 128 registers hold their operands, whose smaller turns spread
     // better (17 x 8192 x 2048 12.3 -> 11.1 us).  A turn holds 16 to 32 KB of B a workgroup.
-    constexpr int W = !B_KC && MT <= 2 && NB <= 4 ? 16 : 8;
-    constexpr int U = B_KC ? 4 / NB : (W == 16 ? 4 / NB : 8 / NB);
+    constexpr int W = !B_KC && NB <= 4 ? 16 : 8;
+    constexpr int U = B_KC ? 4 : (W == 16 ? 4 / NB : 8 / NB);
     hipLaunchKernelGGL((few_rows_kernel<FP16, B_KC, MT, NB, W, U>), dim3((unsigned)(a.cols * a.splits)), dim3(64 * W), 0,
                        stream, a, e);
     return hipGetLastError();
@@ -262,22 +272,13 @@ static hipError_t go(const FewRowsArgs& a, const Epi& e, hipStream_t stream) {
 
 template <bool FP16, bool B_KC>
 static hipError_t pick_few(const FewRowsArgs& a, const Epi& e, int nb, hipStream_t st) {
-    const int mt = (a.M + 15) / 16;
     if constexpr (B_KC) {
-        if (mt == 1) return go<FP16, true, 1, 1>(a, e, st);
-        if (nb == 1) {
-            if (mt == 2) return go<FP16, true, 2, 1>(a, e, st);
-            if (mt == 3) return go<FP16, true, 3, 1>(a, e, st);
-            return go<FP16, true, 4, 1>(a, e, st);
-        }
-    } else if (mt == 1) {
+        return a.M <= 16 ? go<FP16, true, 1, 1>(a, e, st) : go<FP16, true, 2, 1>(a, e, st);
+    } else {
+        if (a.M > 16) return go<FP16, false, 2, 2>(a, e, st);
         if (nb == 8) return go<FP16, false, 1, 8>(a, e, st);
-        if (nb == 4) return go<FP16, false, 1, 4>(a, e, st);
-        return go<FP16, false, 1, 2>(a, e, st);
+        return nb == 4 ? go<FP16, false, 1, 4>(a, e, st) : go<FP16, false, 1, 2>(a, e, st);
     }
-    if (mt == 2) return nb == 4 ? go<FP16, B_KC, 2, 4>(a, e, st) : go<FP16, B_KC, 2, 2>(a, e, st);
-    if (mt == 3) return go<FP16, B_KC, 3, 2>(a, e, st);
-    return go<FP16, B_KC, 4, 2>(a, e, st);
 }
 
 hipError_t launch_few_rows(const FewRowsArgs& a, const Epi& e, bool fp16, bool b_kc, int nb, hipStream_t stream) {

@@ -7,11 +7,10 @@ namespace igc {
 
 struct Epi;
 
-constexpr int64_t kFewRows = 64;  // most rows the kernel takes
-// Beyond 16 rows every workgroup's reads of A weigh as much as its columns of
-// B, and with many columns the 128 x 128 tiles, which share them, are faster:
-// 48 x 8192 x 4096 24 us against 30 on tiles, 32 x 16384 x 4096 32 against 27.
-constexpr int64_t kFewRowsColumns = 400000;  // largest M * N with more than 16 rows
+constexpr int64_t kFewRows = 32;  // most rows the kernel takes
+
+// Whether it is the faster one for M <= kFewRows rows.
+bool few_rows_faster(int64_t M, int64_t N, int64_t K, bool b_kc);
 
 // How a product of M <= kFewRows rows is cut: NB operands of 16 columns a wave,
 // `cols` workgroups across N, `splits` along K (each `per` of K).

@@ -357,8 +357,8 @@ static igc_status_t check_epilogue(const igc_epilogue_t* q, int64_t N, bool dens
 // Whether a product runs on the kernel of few_rows.hip: at most kFewRows rows,
 // row-major A, and the 32-bit lane offsets of its loads in range.
 static bool takes_few_rows(int64_t M, int64_t N, int64_t K, int64_t lda, bool a_kc, int64_t ldb, bool b_kc) {
-    return a_kc && M >= 1 && M <= kFewRows && (M <= 16 || M * N <= kFewRowsColumns) && N < (1ll << 30) && K < (1ll << 31) && M * lda * 2 < 0x7fffffffLL &&
-           (64 * ldb + 256) * 2 < 0x7fffffffLL;
+    return a_kc && M >= 1 && M <= kFewRows && few_rows_faster(M, N, K, b_kc) && N < (1ll << 30) && K < (1ll << 31) &&
+           M * lda * 2 < 0x7fffffffLL && (64 * ldb + 256) * 2 < 0x7fffffffLL;
 }
 static int64_t few_rows_bytes(const FewRowsPlan& pl, int64_t M, int64_t N) {
     return pl.splits > 1 ? round_up(pl.splits * M * round_up(N, 4) * 4, 256) : 0;

@@ -581,6 +581,16 @@ def test_built_in_choices_of_small_outputs():
         conv_case(*geometry, "bf16", "gelu_tanh", seed=4)
 
 
+def test_few_rows_and_tiles_meet():
+    """Row counts, widths and depths on both sides of where the kernel of few rows gives way to tiles."""
+    for M in (1, 8, 9, 16, 17, 20, 21, 32, 33):
+        for N, K in ((40, 2048), (40, 2056), (8200, 24), (16400, 16), (33000, 8), (24, 6200)):
+            for lb in ("col", "row"):
+                say(f"few rows {M}x{N}x{K} {lb}")
+                p = Problem(M, N, K, "bf16", lb=lb, act="silu", pre="in" if M in (9, 20) else None, seed=M)
+                p.check(p.run(), f"{M}x{N}x{K} {lb}")
+
+
 # ---- extreme values -------------------------------------------------------------------------------------------------
 
 @pytest.mark.parametrize("act", ACTS)
