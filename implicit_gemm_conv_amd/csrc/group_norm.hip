@@ -5,13 +5,21 @@
 //   dbeta = sum dz;  dgamma = sum dz xh;
 //   dx = rstd (gamma dz - mean(gamma dz) - xh mean(gamma dz xh))   (means over the group)
 //
-// Bound by memory: x in and y out, 4 bytes a value (backward: x, dy, dx, 6).
-// The pixels of an image are cut into chunks.  A first kernel reduces every
-// chunk per channel, a second joins the chunks (and a group's channels) in
-// order, a third reads the image again and writes the result.  A thread keeps
-// eight channels (16 bytes of a pixel) and walks over pixels, whatever the
-// group size: groups of any width, also those that no vector fits, differ only
-// in how the joined statistics are looked up.
+// Bound by memory: x in and y out, 4 bytes a value (backward: x, dy, dx, 6);
+// small ones by the latency of a launch and of a few dependent loads.  Two forms:
+//   - one workgroup for an image's slab of whole groups, in one launch: forward
+//     x stays in registers from the statistics to the output, backward x and dy
+//     do, or are read twice (gn_resident_kernel, gn_backward_slab_kernel);
+//   - chunks of an image's pixels, in two launches: the first reduces every
+//     chunk by group, the second joins the chunks, each workgroup for itself
+//     while its first pixels arrive, reads the image again and writes.
+// A thread keeps eight channels (16 bytes of a pixel) and walks over pixels,
+// whatever the group size: groups of any width, also those that no vector fits,
+// differ only in how the joined statistics are looked up.
+// Measured (bf16, silu; forward, backward with gamma and beta's gradients):
+// 32 of 56 x 56 x 256 in 32 groups 27.6 and 51.5 us (3.7 and 3.0 TB/s; backward
+// has 38 operations a value, 27 us), 16 of 27 x 27 x 320 12.4 and 18.5, 32 of
+// 48 x 48 x 640 in one 55 and 92, 2 of 8 x 8 x 1280 5.3 and 8.8.
 //
 // Variance: a thread sums d = x - x0 and d^2 with its own first value x0 of
 // each channel as the shift, which loses nothing to a large mean and is never
@@ -35,15 +43,17 @@ struct GnArgs {
     const void* gamma;     // nullptr: 1
     const void* beta;      // nullptr: 0
     float *mean, *rstd;    // N x G
-    float* part;           // N x chunks x C pairs: (mean, M2), or (sum dz, sum dz xh)
-    float* coef;           // planes of N x C: mean, rstd gamma, beta; backward also -rstd^2 c2 and -rstd c1 (the two means)
-    float* sums;           // backward: N x C pairs (sum dz, sum dz xh)
+    float* part;           // pairs of every unit of channels and chunk, N x C/uw x chunks: (mean, M2); backward
+                           // (sum gamma dz, sum gamma dz xh)
+    float* sums;           // backward: pairs (sum dz, sum dz xh) of every channel, `rows` of them (images or chunks)
     void *dgamma, *dbeta;  // nullptr: not wanted
     int64_t ldx, lddy, ldo;
     int64_t HW;
     int N, C, G, cpg, param_kind, act;
     uint32_t cpg_magic;    // fastdiv multiplier of cpg
     int chunks, pixels;    // chunks of an image and pixels per chunk
+    int uw;                // channels of a unit: a group, or what of it lies in one slab
+    int rows;              // of `sums`
     int grid;              // workgroups over the images
     int sv, pl, slabs;     // vectors (8 channels) a workgroup covers, its pixel lanes, slabs of an image's channels
     float eps;
@@ -74,7 +84,36 @@ struct GnSpot {
     }
 };
 
-// Per-channel means and squared deviations of a chunk.
+// Lanes of a workgroup for `items` sums of one length: as many neighbours an
+// item as there are, a power of two and at most a wave.
+struct GnLanes {
+    int lanes, lane, item, step;
+    __device__ __forceinline__ explicit GnLanes(int items) {
+        lanes = 64;
+        while (lanes > 1 && lanes * items > (int)blockDim.x) lanes >>= 1;
+        lane = (int)threadIdx.x & (lanes - 1);
+        item = (int)threadIdx.x / lanes;
+        step = (int)blockDim.x / lanes;
+    }
+    // over the item's lanes, in a fixed order; every one of them gets it
+    __device__ __forceinline__ float sum(float v) const {
+        for (int d = lanes >> 1; d >= 1; d >>= 1) v += __shfl_xor(v, d);
+        return v;
+    }
+};
+
+// Threads for each of `items` sums that lie side by side in LDS rows, so that
+// neighbouring threads take neighbouring items.
+__device__ __forceinline__ int lanes_share(int items) {
+    const int share = (int)blockDim.x / items;
+    return share < 1 ? 1 : (share > 16 ? 16 : share);
+}
+
+__device__ __forceinline__ float* unit_pair(const GnArgs& a, int n, int unit, int chunk) {
+    return a.part + (((int64_t)n * (a.C / a.uw) + unit) * a.chunks + chunk) * 2;
+}
+
+// Means and squared deviations of a chunk, by unit of channels.
 template <bool FP16>
 __global__ __launch_bounds__(kGnThreads) void gn_partial_kernel(const GnArgs a) {
     __shared__ float smean[kGnThreads * 8], sm2[kGnThreads * 8];
@@ -116,116 +155,146 @@ __global__ __launch_bounds__(kGnThreads) void gn_partial_kernel(const GnArgs a) 
         }
     }
     __syncthreads();
-    const int nch = a.sv * 8, total = (int)(s.p1 - s.p0);
-    const int slab = (int)blockIdx.x % a.slabs;
-    for (int ch = (int)threadIdx.x; ch < nch; ch += (int)blockDim.x) {
-        const int c = slab * nch + ch;
-        if (c >= a.C) break;
-        float mean = 0.0f;
-        for (int p = 0; p < a.pl && p < total; ++p) {
-            const int cnt = (total - p + a.pl - 1) / a.pl;
-            mean = __builtin_fmaf((float)cnt, smean[p * nch + ch], mean);
+    const int nch = a.sv * 8, total = (int)(s.p1 - s.p0), slab = (int)blockIdx.x % a.slabs;
+    const int here = a.C - slab * nch < nch ? a.C - slab * nch : nch;  // channels of this slab
+    // The pixel lanes of a channel, into lane 0's: several threads a channel, taking the lanes' means about lane 0's.
+    const int q0 = total / a.pl, extra = total - q0 * a.pl;  // pixels of a lane, and lanes with one more
+    const int share = lanes_share(here);
+    for (int ch = (int)threadIdx.x % (share > 1 ? here : (int)blockDim.x); ch < here; ch += (int)blockDim.x) {
+        const int q = share > 1 ? (int)threadIdx.x / here : 0;
+        const float m0 = smean[ch];
+        float t1 = 0.0f, t2 = 0.0f;
+        if (q < share) {
+#pragma unroll 4
+            for (int p = q; p < a.pl; p += share) {
+                const float n = (float)(q0 + (p < extra)), d = smean[p * nch + ch] - m0;
+                if (n > 0.0f) {
+                    t1 = __builtin_fmaf(n, d, t1);
+                    t2 += sm2[p * nch + ch] + n * d * d;
+                }
+            }
         }
-        mean /= (float)total;
-        float m2 = 0.0f;
-        for (int p = 0; p < a.pl && p < total; ++p) {
-            const int cnt = (total - p + a.pl - 1) / a.pl;
-            const float d = smean[p * nch + ch] - mean;
-            m2 += sm2[p * nch + ch] + (float)cnt * d * d;
+        if (share > 1) {
+            __syncthreads();
+            if (q < share) smean[q * here + ch] = t1, sm2[q * here + ch] = t2;
+            __syncthreads();
+            if (q == 0)
+                for (int k = 1; k < share; ++k) t1 += smean[k * here + ch], t2 += sm2[k * here + ch];
         }
-        float* dst = a.part + (((int64_t)s.n * a.chunks + s.chunk) * a.C + c) * 2;
-        dst[0] = mean;
-        dst[1] = m2;
+        if (q == 0) {
+            const float dm = t1 / (float)total, m2 = t2 - t1 * dm;
+            smean[ch] = m0 + dm;
+            sm2[ch] = m2 < 0.0f ? 0.0f : m2;
+        }
+    }
+    __syncthreads();
+    const GnLanes j(here / a.uw);
+    for (int u = j.item; u < here / a.uw; u += j.step) {  // the channels of a unit, equal in number of pixels
+        float mean = 0.0f, m2 = 0.0f;
+        for (int c = j.lane; c < a.uw; c += j.lanes) mean += smean[u * a.uw + c];
+        mean = j.sum(mean) / (float)a.uw;
+        for (int c = j.lane; c < a.uw; c += j.lanes) {
+            const float d = smean[u * a.uw + c] - mean;
+            m2 += sm2[u * a.uw + c] + (float)total * d * d;
+        }
+        m2 = j.sum(m2);
+        if (j.lane == 0) {
+            float* dst = unit_pair(a, s.n, slab * nch / a.uw + u, s.chunk);
+            dst[0] = mean;
+            dst[1] = m2;
+        }
     }
 }
 
-// Sum over a workgroup (at most 16 waves), in a fixed order; every thread gets it.
-__device__ __forceinline__ float block_sum(float v, float* red) {
-#pragma unroll
-    for (int d = 32; d >= 1; d >>= 1) v += __shfl_xor(v, d);
-    __syncthreads();  // an earlier sum has been read
-    if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = v;
-    __syncthreads();
-    float t = red[0];
-    for (int w = 1; w < (int)(blockDim.x >> 6); ++w) t += red[w];
-    return t;
-}
-
-// Lanes of a workgroup over a group's channels (consecutive ones, so that a
-// chunk's pairs are read together) and, beyond them, over the chunks.
-struct GnJoin {
-    int cw, lanes, cl, kl;
-    __device__ __forceinline__ explicit GnJoin(int cpg) {
-        cw = 1;
-        while (cw < cpg && cw < (int)blockDim.x) cw *= 2;
-        lanes = (int)blockDim.x / cw;
-        cl = (int)threadIdx.x & (cw - 1);
-        kl = (int)threadIdx.x / cw;
+// The groups that the channels of a slab belong to.
+struct GnGroups {
+    int g0, count;
+    __device__ __forceinline__ explicit GnGroups(const GnArgs& a) {
+        const int c0 = (int)blockIdx.x % a.slabs * a.sv * 8;
+        const int c1 = (c0 + a.sv * 8 < a.C ? c0 + a.sv * 8 : a.C) - 1;
+        g0 = group_of(a, c0);
+        count = group_of(a, c1) - g0 + 1;
     }
 };
 
-constexpr int kGnJoinThreads = 512;
+constexpr int kGnThreadsChannels = kGnThreads * 8;  // channels of a slab at most, so its groups
 
-// Joins the chunks and channels of one group of one image into its statistics,
-// and writes what the apply kernel needs of each channel: mean, rstd gamma, beta.
-__global__ __launch_bounds__(kGnJoinThreads) void gn_finish_kernel(const GnArgs a) {
-    __shared__ float red[16];
-    const int n = (int)blockIdx.x / a.G, g = (int)blockIdx.x % a.G;
-    const GnJoin j(a.cpg);
-    const float* part = a.part + ((int64_t)n * a.chunks * a.C + (int64_t)g * a.cpg) * 2;
+// Joins the chunks of the slab's groups into their statistics, to sm and sr by
+// group of the slab; the first chunk's workgroups write them out.  The chunks'
+// means are taken about the first one's, one pass over the pairs: what that
+// loses is at most the number of chunks times a rounding, since the first chunk
+// is part of the variance.
+__device__ __forceinline__ void join_chunks(const GnArgs& a, int n, int chunk, float* sm, float* sr) {
+    const GnGroups gs(a);
+    const GnLanes j(gs.count);
+    const int upg = a.cpg / a.uw, pairs = upg * a.chunks;
     const float total = (float)a.HW * (float)a.cpg;
-    const int last = (int)(a.HW - (int64_t)(a.chunks - 1) * a.pixels);  // pixels of the last chunk
-    float s = 0.0f;
-    for (int c = j.cl; c < a.cpg; c += j.cw)
-        for (int k = j.kl; k < a.chunks; k += j.lanes)
-            s = __builtin_fmaf((float)(k + 1 < a.chunks ? a.pixels : last), part[((int64_t)k * a.C + c) * 2], s);
-    const float mean = block_sum(s, red) / total;
-    s = 0.0f;
-    for (int c = j.cl; c < a.cpg; c += j.cw)
-        for (int k = j.kl; k < a.chunks; k += j.lanes) {
-            const float* src = part + ((int64_t)k * a.C + c) * 2;
-            const float d = src[0] - mean;
-            s += src[1] + (float)(k + 1 < a.chunks ? a.pixels : last) * d * d;
-        }
-    const float var = block_sum(s, red) / total;
-    const float rstd = 1.0f / __builtin_sqrtf(var + a.eps);
-    if (threadIdx.x == 0 && a.mean) a.mean[blockIdx.x] = mean;
-    if (threadIdx.x == 0 && a.rstd) a.rstd[blockIdx.x] = rstd;
-    const int64_t plane = (int64_t)a.N * a.C;
-    for (int c = (int)threadIdx.x; c < a.cpg; c += (int)blockDim.x) {
-        const int64_t ch = (int64_t)g * a.cpg + c, at = (int64_t)n * a.C + ch;
-        a.coef[at] = mean;
-        a.coef[plane + at] = rstd * (a.gamma ? load_kind(a.gamma, ch, a.param_kind) : 1.0f);
-        a.coef[2 * plane + at] = a.beta ? load_kind(a.beta, ch, a.param_kind) : 0.0f;
-    }
-}
-
-// Plane k of the joined coefficients of a thread's channels.
-__device__ __forceinline__ void load_coef(const GnArgs& a, int n, int c, int k, float (&v)[8]) {
-    const float* src = a.coef + (k * (int64_t)a.N + n) * a.C + c;
-    const f32x4s_t lo = *(const f32x4s_t*)src, hi = *(const f32x4s_t*)(src + 4);
+    const float full = (float)a.pixels * (float)a.uw;
+    const float last = (float)(int)(a.HW - (int64_t)(a.chunks - 1) * a.pixels) * (float)a.uw;
+    for (int g = j.item; g < gs.count; g += j.step) {
+        const float* src = unit_pair(a, n, (gs.g0 + g) * upg, 0);
+        const float m0 = src[0];
+        float s1 = 0.0f, s2 = 0.0f;
+        int at = j.lane % a.chunks;  // the pair's chunk
+        const int ahead = j.lanes % a.chunks;
+        constexpr int U = 8;
+        for (int k = j.lane; k < pairs; k += U * j.lanes) {
+            float m[U], q[U];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) v[i] = lo[i], v[4 + i] = hi[i];
+            for (int u = 0; u < U; ++u)
+                if (k + u * j.lanes < pairs) m[u] = src[2 * (k + u * j.lanes)], q[u] = src[2 * (k + u * j.lanes) + 1];
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                if (k + u * j.lanes >= pairs) break;
+                const float d = m[u] - m0, w = at + 1 < a.chunks ? full : last;
+                s1 = __builtin_fmaf(w, d, s1);
+                s2 += q[u] + w * d * d;
+                at += ahead;
+                if (at >= a.chunks) at -= a.chunks;
+            }
+        }
+        s1 = j.sum(s1);
+        s2 = j.sum(s2);
+        const float dm = s1 / total, m2 = s2 - s1 * dm;
+        if (j.lane == 0) {
+            const float mean = m0 + dm, rstd = 1.0f / __builtin_sqrtf((m2 < 0.0f ? 0.0f : m2) / total + a.eps);
+            sm[g] = mean;
+            sr[g] = rstd;
+            if (chunk == 0 && a.mean) a.mean[n * a.G + gs.g0 + g] = mean;
+            if (chunk == 0 && a.rstd) a.rstd[n * a.G + gs.g0 + g] = rstd;
+        }
+    }
+    __syncthreads();
 }
 
 template <bool FP16>
 __global__ __launch_bounds__(kGnThreads) void gn_apply_kernel(const GnArgs a) {
+    __shared__ float sm[kGnThreadsChannels], sr[kGnThreadsChannels];
     const GnSpot s(a);
-    if (!s.on) return;
-    float mu[8], ga[8], be[8];
-    load_coef(a, s.n, s.c, 0, mu);
-    load_coef(a, s.n, s.c, 1, ga);
-    load_coef(a, s.n, s.c, 2, be);
+    constexpr int U = 4;
     const char* img = (const char*)a.x + ((int64_t)s.n * a.HW * a.ldx + s.c) * 2;
     char* out = (char*)a.out + ((int64_t)s.n * a.HW * a.ldo + s.c) * 2;
+    u32x4s_t w[U];
+    auto load = [&](int64_t p) __attribute__((always_inline)) {
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+            if (s.on && p + u * a.pl < s.p1) w[u] = *(const u32x4s_t*)(img + (p + u * a.pl) * a.ldx * 2);
+    };
+    load(s.p0 + s.p);  // on its way during the join
+    join_chunks(a, s.n, s.chunk, sm, sr);
+    if (!s.on) return;
+    const int g0 = GnGroups(a).g0;
+    float mu[8], ga[8], be[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const int g = group_of(a, s.c + i) - g0;
+        mu[i] = sm[g];
+        ga[i] = sr[g] * (a.gamma ? load_kind(a.gamma, s.c + i, a.param_kind) : 1.0f);
+        be[i] = a.beta ? load_kind(a.beta, s.c + i, a.param_kind) : 0.0f;
+    }
     with_act(a.act, [&](auto A) __attribute__((always_inline)) {
         constexpr int ACT = decltype(A)::value;
-        constexpr int U = 4;
         for (int64_t p = s.p0 + s.p; p < s.p1; p += U * a.pl) {
-            u32x4s_t w[U];
-#pragma unroll
-            for (int u = 0; u < U; ++u)
-                if (p + u * a.pl < s.p1) w[u] = *(const u32x4s_t*)(img + (p + u * a.pl) * a.ldx * 2);
 #pragma unroll
             for (int u = 0; u < U; ++u) {
                 if (p + u * a.pl >= s.p1) break;
@@ -236,11 +305,12 @@ __global__ __launch_bounds__(kGnThreads) void gn_apply_kernel(const GnArgs a) {
                     v[i] = act_of<ACT>(__builtin_fmaf(v[i] - mu[i], ga[i], be[i]));
                 *(u32x4s_t*)(out + (p + u * a.pl) * a.ldo * 2) = pack8<FP16>(v);
             }
+            load(p + U * a.pl);
         }
     });
 }
 
-// Per-channel sums of dz and dz xh of a chunk.
+// Sums of dz and dz xh of a chunk, by channel and, weighted with gamma, by unit.
 template <bool FP16>
 __global__ __launch_bounds__(kGnThreads) void gn_backward_partial_kernel(const GnArgs a) {
     __shared__ float s1[kGnThreads * 8], s2[kGnThreads * 8];
@@ -293,125 +363,144 @@ __global__ __launch_bounds__(kGnThreads) void gn_backward_partial_kernel(const G
     }
     __syncthreads();
     const int nch = a.sv * 8, slab = (int)blockIdx.x % a.slabs;
-    for (int ch = (int)threadIdx.x; ch < nch; ch += (int)blockDim.x) {
-        const int c = slab * nch + ch;
-        if (c >= a.C) break;
+    const int here = a.C - slab * nch < nch ? a.C - slab * nch : nch;
+    const int share = lanes_share(here);
+    for (int ch = (int)threadIdx.x % (share > 1 ? here : (int)blockDim.x); ch < here; ch += (int)blockDim.x) {
+        const int c = slab * nch + ch, q = share > 1 ? (int)threadIdx.x / here : 0;
         float t1 = 0.0f, t2 = 0.0f;
-        for (int p = 0; p < a.pl; ++p) {
-            t1 += s1[p * nch + ch];
-            t2 += s2[p * nch + ch];
+        if (q < share) {
+#pragma unroll 4
+            for (int p = q; p < a.pl; p += share) {
+                t1 += s1[p * nch + ch];
+                t2 += s2[p * nch + ch];
+            }
         }
-        float* dst = a.part + (((int64_t)s.n * a.chunks + s.chunk) * a.C + c) * 2;
-        dst[0] = t1;
-        dst[1] = t2;
-    }
-}
-
-// One group of one image: its channels' sums over the chunks (kept for dgamma
-// and dbeta), its two means, and the apply kernel's coefficients.
-__global__ __launch_bounds__(kGnJoinThreads) void gn_backward_finish_kernel(const GnArgs a) {
-    __shared__ float red[2 * kGnJoinThreads];
-    const int n = (int)blockIdx.x / a.G, g = (int)blockIdx.x % a.G;
-    const GnJoin j(a.cpg);
-    const float* part = a.part + ((int64_t)n * a.chunks * a.C + (int64_t)g * a.cpg) * 2;
-    float m1 = 0.0f, m2 = 0.0f;
-    for (int c0 = 0; c0 < a.cpg; c0 += j.cw) {
-        const int c = c0 + j.cl;
-        float t1 = 0.0f, t2 = 0.0f;
-        if (c < a.cpg)
-            for (int k = j.kl; k < a.chunks; k += j.lanes) {
-                t1 += part[((int64_t)k * a.C + c) * 2];
-                t2 += part[((int64_t)k * a.C + c) * 2 + 1];
-            }
-        __syncthreads();
-        red[threadIdx.x] = t1;
-        red[kGnJoinThreads + threadIdx.x] = t2;
-        __syncthreads();
-        if (j.kl == 0 && c < a.cpg) {
-            for (int l = 1; l < j.lanes; ++l) {
-                t1 += red[l * j.cw + j.cl];
-                t2 += red[kGnJoinThreads + l * j.cw + j.cl];
-            }
-            const int64_t ch = (int64_t)g * a.cpg + c;
-            float* dst = a.sums + ((int64_t)n * a.C + ch) * 2;
+        if (share > 1) {
+            __syncthreads();
+            if (q < share) s1[q * here + ch] = t1, s2[q * here + ch] = t2;
+            __syncthreads();
+            if (q == 0)
+                for (int k = 1; k < share; ++k) t1 += s1[k * here + ch], t2 += s2[k * here + ch];
+        }
+        if (q > 0) continue;
+        if (a.dgamma || a.dbeta) {
+            float* dst = a.sums + (((int64_t)s.n * a.chunks + s.chunk) * a.C + c) * 2;
             dst[0] = t1;
             dst[1] = t2;
-            const float ga = a.gamma ? load_kind(a.gamma, ch, a.param_kind) : 1.0f;
-            m1 = __builtin_fmaf(ga, t1, m1);
-            m2 = __builtin_fmaf(ga, t2, m2);
         }
+        const float ga = a.gamma ? load_kind(a.gamma, c, a.param_kind) : 1.0f;
+        s1[ch] = ga * t1;
+        s2[ch] = ga * t2;
     }
     __syncthreads();
-    const float total = (float)a.HW * (float)a.cpg, mean = a.mean[blockIdx.x], rstd = a.rstd[blockIdx.x];
-    m1 = block_sum(m1, red) / total;
-    m2 = block_sum(m2, red) / total;
-    const int64_t plane = (int64_t)a.N * a.C;
-    for (int c = (int)threadIdx.x; c < a.cpg; c += (int)blockDim.x) {
-        const int64_t ch = (int64_t)g * a.cpg + c, at = (int64_t)n * a.C + ch;
-        a.coef[at] = mean;
-        a.coef[plane + at] = rstd * (a.gamma ? load_kind(a.gamma, ch, a.param_kind) : 1.0f);
-        a.coef[2 * plane + at] = a.beta ? load_kind(a.beta, ch, a.param_kind) : 0.0f;
-        a.coef[3 * plane + at] = -rstd * rstd * m2;
-        a.coef[4 * plane + at] = -rstd * m1;
+    const GnLanes j(here / a.uw);
+    for (int u = j.item; u < here / a.uw; u += j.step) {
+        float t1 = 0.0f, t2 = 0.0f;
+        for (int c = j.lane; c < a.uw; c += j.lanes) {
+            t1 += s1[u * a.uw + c];
+            t2 += s2[u * a.uw + c];
+        }
+        t1 = j.sum(t1);
+        t2 = j.sum(t2);
+        if (j.lane == 0) {
+            float* dst = unit_pair(a, s.n, slab * nch / a.uw + u, s.chunk);
+            dst[0] = t1;
+            dst[1] = t2;
+        }
     }
 }
 
-// dgamma and dbeta of 32 channels: the images' sums, added in order by 8 lanes a channel.
+// dgamma and dbeta of COLS channels: the rows of `sums`, added in order by the workgroup's lanes of each channel.
+template <int COLS>
 __device__ __forceinline__ void gn_param_sums(const GnArgs& a, int block, int threads, float* red) {
-    const int t = (int)threadIdx.x, lanes = threads / 32;  // whole rows of 32 threads
-    const int c = block * 32 + (t & 31), l = t >> 5;
+    const int t = (int)threadIdx.x, lanes = threads / COLS;
+    const int c = block * COLS + t % COLS, l = t / COLS;
     float t1 = 0.0f, t2 = 0.0f;
-    if (c < a.C)
-        for (int n = l; n < a.N; n += lanes) {
+    if (c < a.C) {
+#pragma unroll 8
+        for (int n = l; n < a.rows; n += lanes) {
             t1 += a.sums[((int64_t)n * a.C + c) * 2];
             t2 += a.sums[((int64_t)n * a.C + c) * 2 + 1];
         }
+    }
     red[t] = t1;
     red[threads + t] = t2;
     __syncthreads();
     if (l == 0 && c < a.C) {
         for (int k = 1; k < lanes; ++k) {
-            t1 += red[k * 32 + t];
-            t2 += red[threads + k * 32 + t];
+            t1 += red[k * COLS + t];
+            t2 += red[threads + k * COLS + t];
         }
         if (a.dbeta) store_kind(a.dbeta, c, a.param_kind, t1);
         if (a.dgamma) store_kind(a.dgamma, c, a.param_kind, t2);
     }
 }
+constexpr int kGnJoinThreads = 512;
 __global__ __launch_bounds__(kGnJoinThreads) void gn_param_kernel(const GnArgs a) {
     __shared__ float red[2 * kGnJoinThreads];
-    gn_param_sums(a, (int)blockIdx.x, kGnJoinThreads, red);
+    gn_param_sums<32>(a, (int)blockIdx.x, kGnJoinThreads, red);
 }
 
 template <bool FP16>
 __global__ __launch_bounds__(kGnThreads) void gn_backward_apply_kernel(const GnArgs a) {
+    __shared__ float s1[kGnThreadsChannels], s2[kGnThreadsChannels];  // the two means of the slab's groups
     if ((int)blockIdx.x >= a.grid) {  // the workgroups past the images': dgamma and dbeta
-        __shared__ float red[2 * kGnThreads];
-        gn_param_sums(a, (int)blockIdx.x - a.grid, (int)blockDim.x, red);
+        gn_param_sums<8>(a, (int)blockIdx.x - a.grid, (int)blockDim.x, s1);
         return;
     }
     const GnSpot s(a);
-    if (!s.on) return;
-    float mu[8], ga[8], be[8], c2[8], c1[8];
-    load_coef(a, s.n, s.c, 0, mu);
-    load_coef(a, s.n, s.c, 1, ga);
-    load_coef(a, s.n, s.c, 2, be);
-    load_coef(a, s.n, s.c, 3, c2);
-    load_coef(a, s.n, s.c, 4, c1);
+    constexpr int U = 2;
     const char* img = (const char*)a.x + ((int64_t)s.n * a.HW * a.ldx + s.c) * 2;
     const char* grad = (const char*)a.dy + ((int64_t)s.n * a.HW * a.lddy + s.c) * 2;
     char* out = (char*)a.out + ((int64_t)s.n * a.HW * a.ldo + s.c) * 2;
+    u32x4s_t w[U], d[U];
+    auto load = [&](int64_t p) __attribute__((always_inline)) {
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+            if (s.on && p + u * a.pl < s.p1) {
+                w[u] = *(const u32x4s_t*)(img + (p + u * a.pl) * a.ldx * 2);
+                d[u] = *(const u32x4s_t*)(grad + (p + u * a.pl) * a.lddy * 2);
+            }
+    };
+    load(s.p0 + s.p);  // on its way during the join
+    const GnGroups gs(a);
+    {
+        const GnLanes j(gs.count);
+        const int upg = a.cpg / a.uw, pairs = upg * a.chunks;
+        const float rn = 1.0f / ((float)a.HW * (float)a.cpg);
+        for (int g = j.item; g < gs.count; g += j.step) {
+            const float* src = unit_pair(a, s.n, (gs.g0 + g) * upg, 0);
+            float t1 = 0.0f, t2 = 0.0f;
+#pragma unroll 8
+            for (int k = j.lane; k < pairs; k += j.lanes) {
+                t1 += src[2 * k];
+                t2 += src[2 * k + 1];
+            }
+            t1 = j.sum(t1);
+            t2 = j.sum(t2);
+            if (j.lane == 0) {
+                s1[g] = t1 * rn;
+                s2[g] = t2 * rn;
+            }
+        }
+    }
+    __syncthreads();
+    if (!s.on) return;
+    // dx = ga dz - (x - mu) rs^2 c2 - rs c1
+    float mu[8], ga[8], be[8], c2[8], c1[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const int g = group_of(a, s.c + i);
+        const float rs = a.rstd[s.n * a.G + g];
+        mu[i] = a.mean[s.n * a.G + g];
+        ga[i] = rs * (a.gamma ? load_kind(a.gamma, s.c + i, a.param_kind) : 1.0f);
+        be[i] = a.beta ? load_kind(a.beta, s.c + i, a.param_kind) : 0.0f;
+        c2[i] = -rs * rs * s2[g - gs.g0];
+        c1[i] = -rs * s1[g - gs.g0];
+    }
     with_act(a.act, [&](auto A) __attribute__((always_inline)) {
         constexpr int ACT = decltype(A)::value;
-        constexpr int U = 2;
         for (int64_t p = s.p0 + s.p; p < s.p1; p += U * a.pl) {
-            u32x4s_t w[U], d[U];
-#pragma unroll
-            for (int u = 0; u < U; ++u)
-                if (p + u * a.pl < s.p1) {
-                    w[u] = *(const u32x4s_t*)(img + (p + u * a.pl) * a.ldx * 2);
-                    d[u] = *(const u32x4s_t*)(grad + (p + u * a.pl) * a.lddy * 2);
-                }
 #pragma unroll
             for (int u = 0; u < U; ++u) {
                 if (p + u * a.pl >= s.p1) break;
@@ -426,6 +515,7 @@ __global__ __launch_bounds__(kGnThreads) void gn_backward_apply_kernel(const GnA
                 }
                 *(u32x4s_t*)(out + (p + u * a.pl) * a.ldo * 2) = pack8<FP16>(v);
             }
+            load(p + U * a.pl);
         }
     });
 }
@@ -506,7 +596,7 @@ __device__ __forceinline__ void channel_sums(const GnArgs& a, const GnSlab& s, c
 
 // Sums over the slab's groups, to out[group]: W values a thread, one (all its
 // channels being of one group) or its eight channels apart.  `red` holds W
-// floats a thread, `chan` (W == 8) the slab's channels.  Every thread calls it.
+// floats a thread, `chan` the slab's channels (W == 1: a value a wave).  Every thread calls it.
 template <int W>
 __device__ __forceinline__ void group_sums(const GnArgs& a, const GnSlab& s, const float (&val)[W], float* red,
                                            float* chan, float* out) {
@@ -518,18 +608,36 @@ __device__ __forceinline__ void group_sums(const GnArgs& a, const GnSlab& s, con
     } else {
         channel_sums(a, s, val, red, chan);
     }
-    for (int g = (int)(threadIdx.x >> 6); g < s.groups; g += waves) {  // a wave a group
-        float t = 0.0f;
-        if constexpr (W == 1) {
-            const int per = a.cpg / 8;
-            for (int e = 0; e < per; ++e)
-                for (int p = lane; p < a.pl; p += 64) t += red[p * a.sv + g * per + e];
-        } else {
-            for (int c = lane; c < a.cpg; c += 64) t += chan[g * a.cpg + c];
-        }
+    if constexpr (W == 1) {
+        // The values of a group, per of every pixel lane, by as many waves as there are for a group.
+        const int per = a.cpg / 8, share = waves / s.groups > 1 ? waves / s.groups : 1;
+        const int wave = (int)threadIdx.x >> 6, part = wave % share, len = per * a.pl;
+        for (int g = wave / share; g < s.groups; g += waves / share) {
+            float t = 0.0f;
+            for (int i = part * 64 + lane; i < len; i += 64 * share) {
+                const int p = i / per;
+                t += red[p * a.sv + g * per + i - p * per];
+            }
 #pragma unroll
-        for (int d = 32; d >= 1; d >>= 1) t += __shfl_xor(t, d);
-        if (lane == 0) out[g] = t;
+            for (int d = 32; d >= 1; d >>= 1) t += __shfl_xor(t, d);
+            if (lane == 0) (share > 1 ? chan[wave] : out[g]) = t;
+        }
+        if (share > 1) {
+            __syncthreads();
+            if ((int)threadIdx.x < s.groups) {
+                float t = chan[threadIdx.x * share];
+                for (int k = 1; k < share; ++k) t += chan[threadIdx.x * share + k];
+                out[threadIdx.x] = t;
+            }
+        }
+    } else {
+        for (int g = (int)(threadIdx.x >> 6); g < s.groups; g += waves) {  // a wave a group
+            float t = 0.0f;
+            for (int c = lane; c < a.cpg; c += 64) t += chan[g * a.cpg + c];
+#pragma unroll
+            for (int d = 32; d >= 1; d >>= 1) t += __shfl_xor(t, d);
+            if (lane == 0) out[g] = t;
+        }
     }
     __syncthreads();
 }
@@ -541,7 +649,7 @@ __global__ __launch_bounds__(kGnMaxThreads) void gn_resident_kernel(const GnArgs
     constexpr int W = SINGLE ? 1 : 8;
     __shared__ __attribute__((aligned(16))) float red[kGnMaxThreads * W];
     __shared__ float sums[kGnMaxVecs * W];  // by group of the slab
-    __shared__ float chan[SINGLE ? 1 : kGnMaxVecs * 8];
+    __shared__ float chan[SINGLE ? kGnMaxThreads / 64 : kGnMaxVecs * 8];
     const GnSlab s(a);
     const char* img = (const char*)a.x + ((int64_t)s.n * a.HW * a.ldx + s.c) * 2;
     u32x4s_t x[NV];
@@ -770,8 +878,8 @@ struct GnPlan {
     bool slab;      // one workgroup for an image's slab of groups; otherwise chunks of pixels
     bool resident;  // the slab stays in registers
     int nv;         // vectors a thread holds; 0: not resident
-    int sv, pl, slabs, threads, chunks, pixels;
-    int64_t part_bytes, coef_bytes, sum_bytes, bytes;
+    int sv, pl, slabs, threads, chunks, pixels, uw;
+    int64_t part_bytes, sum_bytes, bytes;
 };
 
 // One workgroup of up to 1024 threads for an image's slab of sv vectors (whole
@@ -792,11 +900,14 @@ static bool slab_plan(GnPlan& p, int64_t N, int64_t HW, int64_t C, int64_t G, bo
         if (!backward) return false;
     }
     while (2 * sv <= vecs && 2 * sv <= kGnMaxVecs && slabs(2 * sv) >= 256 && (backward || fits(2 * sv))) sv *= 2;
-    // A slab of over 64 KB takes its workgroup longer than the chunks' extra
-    // launches take, unless half the CUs have one and its pieces fill half a
-    // line (forward of 8 images of 128 x 128 x 128 in 32 groups, 16-byte
-    // pieces: 66 us, chunks 30; of 32 of 56 x 56 x 256, 64-byte pieces: 26, chunks 53).
-    if (HW * sv > 4096 && (sv < 4 || slabs(sv) < kGnSlabs)) return false;
+    // A large slab takes its workgroup longer than the chunks' second launch
+    // takes, unless half the CUs have one and its pieces fill half a line.
+    // Forward: 1 of 64 x 64 x 128 in 32 groups (4096 vectors) 14.3 us, in chunks
+    // 13.6; 9 of 24 x 24 x 40 in one (2880) 9.0 and 12.1; backward: 9 of 24 x 24 x 40
+    // 15.4 and 13.8, 1 of 16 x 16 x 1280 in 32 (1280) 12.0 and 16.5.  With the CUs
+    // full: forward of 32 of 56 x 56 x 256 in 32, 64-byte pieces, 26 and 53; of 8 of
+    // 128 x 128 x 128, 16-byte pieces, 66 and 30.
+    if (HW * sv > (backward ? 2048 : 3584) && (sv < 4 || slabs(sv) < kGnSlabs)) return false;
     p.resident = fits(sv);
     p.slab = true;
     p.sv = (int)sv;
@@ -809,6 +920,9 @@ static bool slab_plan(GnPlan& p, int64_t N, int64_t HW, int64_t C, int64_t G, bo
     const int64_t held = HW * sv, least = backward ? (held < 256 ? held : 256) : (held < 512 ? held / 2 : 256);
     int64_t threads = held / (backward ? 4 : 8);
     threads = threads < least ? least : threads;
+    // room for four (eight) pixels a thread where it holds them
+    if (p.resident && threads < sv * ((HW + (backward ? 3 : 7)) / (backward ? 4 : 8)))
+        threads = sv * ((HW + (backward ? 3 : 7)) / (backward ? 4 : 8));
     threads = threads < sv ? sv : threads;
     threads = (threads + 63) / 64 * 64;
     p.threads = (int)(threads < kGnMaxThreads ? threads : kGnMaxThreads);
@@ -834,17 +948,34 @@ static GnPlan gn_plan(int64_t N, int64_t HW, int64_t C, int64_t G, bool backward
     p.pl = kGnThreads / p.sv;
     if (p.pl > HW) p.pl = (int)HW;
     p.threads = (p.pl * p.sv + 63) / 64 * 64;
-    // about four workgroups a CU, each with at least eight pixels a lane
-    int64_t chunks = N > 0 ? (1024 + N * p.slabs - 1) / (N * p.slabs) : 1;
-    const int64_t top = (HW + 8 * p.pl - 1) / (8 * p.pl);
+    // a unit of channels lies in one group and one slab
+    int64_t uw = C / G;
+    for (int64_t q = p.slabs > 1 ? 8 * p.sv : 0; q != 0;) {
+        const int64_t r = uw % q;
+        uw = q;
+        q = r;
+    }
+    p.uw = (int)uw;
+    // A workgroup a CU, two from 16 MB on (4 of 64 x 64 x 320 forward and backward
+    // 17.6 and 21.4 us, 21.0 and 24.7 with two, 26.5 and 29.6 with four; 12 of 42 x 30
+    // x 1136 47.6 and 85.9, 34.4 and 55.1 with two), of at least two pixels a lane.
+    // Every workgroup joins units x chunks pairs after a stream of pixels x
+    // vectors / chunks: no more chunks than balance the two, the square root of
+    // pixels x vectors / units (1 of 64 x 64 x 320 in 32 groups, 71: 85 chunks 17.3 us,
+    // 171 20.1; 1 of 32 x 32 x 640, 50: 43 chunks 15.5 us, 171 19.7).
+    const int64_t wanted = N * HW * vecs < (1 << 20) ? 256 : 512;
+    int64_t chunks = N > 0 ? (wanted + N * p.slabs - 1) / (N * p.slabs) : 1;
+    const int64_t top = (HW + 2 * p.pl - 1) / (2 * p.pl);
+    int64_t join = 1;
+    while ((join + 1) * (join + 1) <= HW * uw / 8 && join < chunks) ++join;
     if (chunks > top) chunks = top;
+    if (chunks > join) chunks = join;
     if (chunks < 1) chunks = 1;
     p.pixels = (int)((HW + chunks - 1) / chunks);
     p.chunks = (int)((HW + p.pixels - 1) / p.pixels);
-    p.part_bytes = round_up(N * p.chunks * C * 8, 256);
-    p.coef_bytes = round_up(N * C * 4 * (backward ? 5 : 3), 256);
-    p.sum_bytes = backward ? round_up(N * C * 8, 256) : 0;
-    p.bytes = p.part_bytes + p.coef_bytes + p.sum_bytes;
+    p.part_bytes = round_up(N * p.chunks * (C / uw) * 8, 256);
+    p.sum_bytes = backward ? round_up(N * p.chunks * C * 8, 256) : 0;
+    p.bytes = p.part_bytes + p.sum_bytes;
     return p;
 }
 
@@ -901,6 +1032,8 @@ static GnArgs gn_args(const GnPlan& pl, int N, int64_t HW, int C, int G, const v
     a.act = (int)act;
     a.chunks = pl.chunks;
     a.pixels = pl.pixels;
+    a.uw = pl.uw;
+    a.rows = pl.slab ? N : N * pl.chunks;
     a.grid = (int)((int64_t)N * (pl.slab ? 1 : pl.chunks) * pl.slabs);
     a.sv = pl.sv;
     a.pl = pl.pl;
@@ -942,12 +1075,10 @@ static igc_status_t gn_forward(int N, int H, int W, int C, int G, const void* x,
         return hipGetLastError() == hipSuccess ? IGC_OK : IGC_ERR_HIP;
     }
     const unsigned grid = (unsigned)a.grid;
-    a.coef = (float*)((char*)ws.ptr + pl.part_bytes);
     a.mean = mean;
     a.rstd = rstd;
     a.eps = eps;
     hipLaunchKernelGGL(gn_partial_kernel<FP16>, dim3(grid), dim3(pl.threads), 0, stream, a);
-    hipLaunchKernelGGL(gn_finish_kernel, dim3((unsigned)(N * G)), dim3(kGnJoinThreads), 0, stream, a);
     hipLaunchKernelGGL(gn_apply_kernel<FP16>, dim3(grid), dim3(pl.threads), 0, stream, a);
     return hipGetLastError() == hipSuccess ? IGC_OK : IGC_ERR_HIP;
 }
@@ -970,7 +1101,7 @@ static igc_status_t gn_backward(int N, int H, int W, int C, int G, const void* x
     }
     const int64_t HW = (int64_t)H * W;
     const GnPlan pl = gn_plan(N, HW, C, G, true);
-    if ((int64_t)N * (pl.slab ? 1 : pl.chunks) * pl.slabs > 0x7fffffff - (C + 31) / 32) return IGC_ERR_UNSUPPORTED;
+    if ((int64_t)N * (pl.slab ? 1 : pl.chunks) * pl.slabs > 0x7fffffff - (C + 7) / 8) return IGC_ERR_UNSUPPORTED;
     Workspace ws;
     if (const igc_status_t st = ws.take(N > 0 ? pl.bytes : 0, user_ws, user_ws_bytes, stream)) return st;
     (void)hipGetLastError();
@@ -983,14 +1114,13 @@ static igc_status_t gn_backward(int N, int H, int W, int C, int G, const void* x
     a.ldo = lddx;
     a.mean = const_cast<float*>(mean);
     a.rstd = const_cast<float*>(rstd);
-    a.coef = (float*)((char*)ws.ptr + pl.part_bytes);
-    a.sums = (float*)((char*)ws.ptr + pl.part_bytes + pl.coef_bytes);
+    a.sums = (float*)((char*)ws.ptr + pl.part_bytes);
     a.dgamma = dgamma;
     a.dbeta = dbeta;
-    const unsigned params = dgamma || dbeta ? (unsigned)((C + 31) / 32) : 0;
+    const unsigned cols = pl.slab || N == 0 ? 32 : 8;  // channels of a workgroup that sums for dgamma and dbeta
+    const unsigned params = dgamma || dbeta ? ((unsigned)C + cols - 1) / cols : 0;
     if (N > 0 && !pl.slab) {
         hipLaunchKernelGGL(gn_backward_partial_kernel<FP16>, dim3((unsigned)a.grid), dim3(pl.threads), 0, stream, a);
-        hipLaunchKernelGGL(gn_backward_finish_kernel, dim3((unsigned)(N * G)), dim3(kGnJoinThreads), 0, stream, a);
         hipLaunchKernelGGL(gn_backward_apply_kernel<FP16>, dim3((unsigned)a.grid + params), dim3(pl.threads), 0, stream,
                            a);
     } else {

@@ -391,3 +391,30 @@ def test_residual_block():
         rel = float((v.double() - grads[k]).norm() / grads[k].norm())
         say(f"residual block d{k}: {rel:.2e}")
         assert rel <= limit, (k, rel)
+
+
+CHUNKED = [
+    (1, 40, 33, 2064, 3), (2, 9, 30, 4096, 1), (1, 30, 31, 4120, 5),     # groups across workgroups of 2048 channels
+    (2, 30, 31, 264, 264), (1, 33, 30, 2048, 2048), (1, 70, 70, 72, 9),  # one channel a group, and eight
+    (7, 56, 9, 736, 1), (12, 21, 15, 1136, 16), (1, 53, 20, 112, 1), (300, 5, 5, 1200, 2), (1, 4, 4, 1280, 1),
+    (3, 1, 7, 2048, 32), (2, 1, 7, 2048, 1), (1, 1, 4000, 8, 1), (1, 1, 2049, 8, 1), (1, 1, 3585, 8, 8),
+    (1, 2, 33000, 8, 1), (4, 260, 256, 32, 2),
+]
+
+
+@pytest.mark.parametrize("shape", CHUNKED)
+def test_chunks_slabs_and_units(shape):
+    """Shapes on both sides of one launch and two, of groups in one slab and across several, of one chunk and many."""
+    p = Norm(*shape, dtype="bf16", params="f32", act="silu", seed=sum(shape))
+    y, mean, rstd = p.forward()
+    p.check_forward(y, mean, rstd, f"{shape}")
+    p.check_backward(*p.backward(), f"{shape}")
+    again = p.forward()
+    first, second = p.backward(), p.backward()
+    synchronize()
+    for a, b in zip((y, mean, rstd) + first, again + second):
+        assert torch.equal(a.view(torch.uint8), b.view(torch.uint8)), "two runs differ"
+    x = p.x.clone()  # in place
+    p.check_forward(*p.forward(y=x, x=x), f"{shape} in place")
+    dy = p.dy.clone()
+    p.check_backward(*p.backward(dx=dy, dy=dy), f"{shape} in place")
