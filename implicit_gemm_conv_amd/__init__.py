@@ -106,26 +106,29 @@ assert _EPILOGUE.size == ctypes.sizeof(CEpilogue)
 
 
 def _bias(x, code):
-    if hasattr(x, "data_ptr"):
-        if x.dim() and x.shape[-1] > 1 and x.stride(-1) != 1:
-            raise ValueError("values of a row must lie together")
-        return x.data_ptr(), out_code(x.dtype) if code is None else code
-    if code is None:
-        raise TypeError("a raw address needs its type")
-    return int(x), code
+    try:
+        ptr = x.data_ptr()
+    except AttributeError:
+        if code is None:
+            raise TypeError("a raw address needs its type") from None
+        return int(x), code
+    if not x.is_contiguous() and x.shape[-1] > 1 and x.stride(-1) != 1:
+        raise ValueError("values of a row must lie together")
+    return ptr, out_code(x.dtype) if code is None else code
 
 
 def _matrix(x, code, ld):
-    if hasattr(x, "data_ptr"):
-        strides = x.stride()
-        if strides and strides[-1] != 1 and x.shape[-1] > 1:
-            raise ValueError("values of a row must lie together")
-        if ld is None:
-            ld = strides[0] if len(strides) == 2 else 0
-        return x.data_ptr(), ld, out_code(x.dtype) if code is None else code
-    if code is None or ld is None:
-        raise TypeError("a raw address needs its type and leading dimension")
-    return int(x), ld, code
+    try:
+        ptr, strides = x.data_ptr(), x.stride()
+    except AttributeError:
+        if code is None or ld is None:
+            raise TypeError("a raw address needs its type and leading dimension") from None
+        return int(x), ld, code
+    if strides and strides[-1] != 1 and x.shape[-1] > 1:
+        raise ValueError("values of a row must lie together")
+    if ld is None:
+        ld = strides[0] if len(strides) == 2 else 0
+    return ptr, ld, out_code(x.dtype) if code is None else code
 
 
 class Epilogue:

@@ -316,10 +316,12 @@ typedef struct {
 
 /* GEMM with a fused epilogue: operands, layouts, sizes, alignment and errors
  * as gemm_bf16 / gemm_fp16, D in the place of C; epilogue must not be NULL.
- * K == 0 leaves z = bias.  With the built-in choice, at most 64 rows of a
- * row-major A run on a kernel that streams B once; tiles and schedules with an
- * explicit tune as gemm_bf16_ex, without stream-K (IGC_ERR_UNSUPPORTED), and
- * without a K split only for the configurations the built-in choice takes.
+ * K == 0 leaves z = bias.  The built-in choice has tiles down to 64 x 64 and
+ * never stream-K; a product of at most 32 rows of a row-major A runs on a kernel
+ * that streams B once where that is faster.  With an explicit tune, tiles and
+ * schedules as gemm_bf16_ex, except that stream-K, and without a K split a
+ * configuration without IGC_SCOPE_EPILOGUE, are IGC_ERR_UNSUPPORTED; so is a D,
+ * residual or pre of which the rows of one tile span 2^31 bytes or more.
  * Workspace: igc_epilogue_workspace_bytes. */
 igc_status_t gemm_bf16_epilogue(int64_t M, int64_t N, int64_t K, const void *A, int64_t lda, igc_layout_t la,
                                 const void *B, int64_t ldb, igc_layout_t lb, void *D, int64_t ldd, igc_out_t d_type,
@@ -361,8 +363,9 @@ igc_status_t conv2d_nhwc_implicit_gemm_epilogue_fp16_ex(int N, int H, int W, int
                                                         int64_t workspace_bytes, igc_stream_t stream);
 
 /* Workspace bytes of a call with an epilogue (op IGC_OP_GEMM or
- * IGC_OP_CONV_FPROP; GEMM view M x N x K; enough for every operand layout);
- * 0 when the schedule does not split K, -1 for bad arguments. */
+ * IGC_OP_CONV_FPROP; GEMM view M x N x K; enough for every operand layout): the
+ * fp32 parts of a K split, or the fp32 product of a convolution whose filter
+ * count is not a multiple of 8; otherwise 0; -1 for bad arguments. */
 int64_t igc_epilogue_workspace_bytes(igc_op_t op, int64_t M, int64_t N, int64_t K, const igc_tune_t *tune);
 
 /*
