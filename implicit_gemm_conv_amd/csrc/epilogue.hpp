@@ -101,6 +101,10 @@ struct EpiElement {
 // order, and with a known number of stores between, the wait for the next
 // turn's residual, requested before them, leaves them in flight.
 //
+// Measured, 4096 x 4096 x 1024 on 256 x 256 tiles: 31.0 us without an epilogue, 33.4
+// through this one with nothing to do, bias 34.1, gelu_tanh 36.5, gelu 42.0,
+// residual 37.0, pre kept 37.1, the backward form 41.8.
+//
 // Chunk c (16 bytes, four columns) of staged row r lies at c ^ (r & (CPR-1)):
 // the 16 rows of an accumulator block are written to distinct banks, and the
 // two chunks a lane reads back stay distinct over the lanes of a phase.
@@ -288,14 +292,21 @@ __global__ __launch_bounds__(C::NT) void gemm_epi_kernel(const Params p, const E
     const int id = xcd_order((int)blockIdx.x, p.tiles_m * p.tiles_n);
     int tm, tn;
     group_coords(id, p.tiles_m, p.tiles_n, p.group_m, tm, tn);
+    float bias[8];
+    const auto load_bias = [&](int64_t n0) __attribute__((always_inline)) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) bias[i] = e.bias && n0 + i < p.N ? load_kind(e.bias, n0 + i, e.bias_kind) : 0.0f;
+    };
+    // The bias of tiles of up to 128 x 128 waits for nothing if it is asked for before the K loop (1000 x 500 x 250
+    // 5.96 and 5.80 us, 1024 x 1024 x 1024 7.53 and 7.38); larger ones have no registers to keep it in.
+    constexpr bool EARLY = C::BM * C::BN <= 128 * 128;
+    if constexpr (EARLY)
+        load_bias((int64_t)tn * C::BN + (int)(threadIdx.x >> 6) % C::WN * C::WTN + ((int)threadIdx.x & 63) % (C::WTN / 8) * 8);
     run_tile<C, V>(p, tm, tn, 0, p.K, [&](auto& ml, auto& acc) __attribute__((always_inline)) {
         // opaque copy of the lane: nothing derived from it is computed before, and kept through, the K loop
         int lane = ml.lane;
         asm volatile("" : "+v"(lane));
-        float bias[8];
-        const int64_t n0 = ml.n0 + ml.wn * C::WTN + (lane % (C::WTN / 8)) * 8;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) bias[i] = e.bias && n0 + i < p.N ? load_kind(e.bias, n0 + i, e.bias_kind) : 0.0f;
+        if constexpr (!EARLY) load_bias(ml.n0 + ml.wn * C::WTN + (lane % (C::WTN / 8)) * 8);
         ring_barrier();  // every wave has finished reading the ring
         epi_passes<C, 0, BWD>(ml, acc, stage_piece<C, PIECE>(ml.wave), p, e, bias, lane);
     });
