@@ -109,6 +109,7 @@ struct EpiElement {
 // the 16 rows of an accumulator block are written to distinct banks, and the
 // two chunks a lane reads back stay distinct over the lanes of a phase.
 typedef __attribute__((ext_vector_type(4))) int i32x4e_t;
+typedef __attribute__((ext_vector_type(2))) unsigned u32x2e_t;
 
 // One of the matrices beside the product: a buffer at the wave's sub-tile and
 // the byte distance of its rows and of eight columns.
@@ -143,21 +144,37 @@ struct EpiMatrix {
             decode8(load(q, in, 0), kind, v);
         }
     }
-    __device__ __forceinline__ void store8(void* base, int64_t off, int q, bool in, int left, const float (&v)[8]) const {
-        const bool whole = in && left >= 8;
+    // The same, written.  tail: N % 8, what `left` is where it is less than eight: that piece goes out as its four,
+    // two and one values, behind a branch that only waves at the end of the rows take (with a loop over its values
+    // 1894 x 5071 x 88 took 27.9 us on 256 x 256 tiles, against 17.7 for 5072 columns; now 17.1).
+    __device__ __forceinline__ void store8(int q, bool in, int left, int tail, const float (&v)[8]) const {
+        const bool whole = in && left >= 8, part = in && left < 8;
         if (kind == KIND_F32) {
             store(q, whole, 0, __builtin_bit_cast(u32x4s_t, f32x4s_t{v[0], v[1], v[2], v[3]}));
             store(q, whole, 1, __builtin_bit_cast(u32x4s_t, f32x4s_t{v[4], v[5], v[6], v[7]}));
+            if (tail && __builtin_amdgcn_ballot_w64(part)) {
+                if (tail & 4) store(q, part, 0, __builtin_bit_cast(u32x4s_t, f32x4s_t{v[0], v[1], v[2], v[3]}));
+                const int at = part ? (int)(first + q * step) + 4 * (tail & 4) : (int)kOob;
+                const float a0 = tail & 4 ? v[4] : v[0], a1 = tail & 4 ? v[5] : v[1], a2 = tail & 4 ? v[6] : v[2];
+                if (tail & 2)
+                    __builtin_amdgcn_raw_buffer_store_b64(
+                        u32x2e_t{__builtin_bit_cast(unsigned, a0), __builtin_bit_cast(unsigned, a1)}, rs, at, 0, 0);
+                if (tail & 1)
+                    __builtin_amdgcn_raw_buffer_store_b32(__builtin_bit_cast(unsigned, tail & 2 ? a2 : a0), rs,
+                                                          part ? at + 4 * (tail & 2) : (int)kOob, 0, 0);
+            }
         } else {
-            store(q, whole, 0, kind == KIND_BF16 ? pack8<false>(v) : pack8<true>(v));
-        }
-        if (in && left < 8) {  // the piece that straddles the end of the row
-            float z[7] = {v[0], v[1], v[2], v[3], v[4], v[5], v[6]};
-#pragma unroll 1
-            for (int i = 0; i < left; ++i) {
-                store_kind(base, off + i, kind, z[0]);
-#pragma unroll
-                for (int k = 0; k < 6; ++k) z[k] = z[k + 1];
+            const u32x4s_t w = kind == KIND_BF16 ? pack8<false>(v) : pack8<true>(v);
+            store(q, whole, 0, w);
+            if (tail && __builtin_amdgcn_ballot_w64(part)) {
+                const int at = part ? (int)(first + q * step) : (int)kOob;
+                if (tail & 4) __builtin_amdgcn_raw_buffer_store_b64(u32x2e_t{w[0], w[1]}, rs, at, 0, 0);
+                if (tail & 2)
+                    __builtin_amdgcn_raw_buffer_store_b32(tail & 4 ? w[2] : w[0], rs, part ? at + 2 * (tail & 4) : at, 0, 0);
+                if (tail & 1)
+                    __builtin_amdgcn_raw_buffer_store_b16(
+                        (unsigned short)(tail & 4 ? (tail & 2 ? w[3] : w[2]) : (tail & 2 ? w[1] : w[0])), rs,
+                        part ? at + 2 * (tail & 6) : at, 0, 0);
             }
         }
     }
@@ -238,8 +255,7 @@ __device__ __forceinline__ void epi_rows(ML& ml, const typename C::Acc (&acc)[C:
             if (e.pre) {
 #pragma unroll
                 for (int u = 0; u < UQ; ++u)
-                    pre.store8(e.pre, (m0 + row0 + (q0 + u) * RPI) * e.ldp + n0 + col, q0 + u, (q0 + u) * RPI < rows, left,
-                               v[u]);
+                    pre.store8(q0 + u, (q0 + u) * RPI < rows, left, (int)(p.N & 7), v[u]);
             }
             with_act(e.act, [&](auto A) __attribute__((always_inline)) {
 #pragma unroll
@@ -263,7 +279,7 @@ __device__ __forceinline__ void epi_rows(ML& ml, const typename C::Acc (&acc)[C:
         if (q0 + UQ < NQ) fetch(q0 + UQ);
 #pragma unroll
         for (int u = 0; u < UQ; ++u)
-            out.store8(p.C, (m0 + row0 + (q0 + u) * RPI) * p.ldc + n0 + col, q0 + u, (q0 + u) * RPI < rows, left, v[u]);
+            out.store8(q0 + u, (q0 + u) * RPI < rows, left, (int)(p.N & 7), v[u]);
     }
     // reads done before the piece is written again
     wait_lgkmcnt0();
@@ -278,6 +294,46 @@ __device__ __forceinline__ void epi_passes(ML& ml, const typename C::Acc (&acc)[
         constexpr int NI = C::FM - I0 < 4 ? C::FM - I0 : 4;
         epi_rows<C, I0, NI, BWD>(ml, acc, reg, p, e, bias, lane);
         epi_passes<C, I0 + NI, BWD>(ml, acc, reg, p, e, bias, lane);
+    }
+}
+
+// The last K % 8 (p.k_ragged8) of K, past the p.K that the loop ran to: one more
+// MFMA a block, its operands straight from memory, zeros for the k that are not
+// there and in place of what lies past a row's end.  The loop stays the one for
+// whole chunks; the one that mends straddling chunks in LDS needs registers that
+// 256 x 256 tiles do not have (4096 x 4096 x 1001: 84 us with it, 41 with this).
+template <class C, class ML>
+__device__ __forceinline__ void add_k_tail(const Params& p, const ML& ml, typename C::Acc (&acc)[C::FM][C::FN], int lane) {
+    auto piece = [&](const void* base, int64_t ld, bool k_contiguous, int64_t row) __attribute__((always_inline)) {
+        u32x4s_t w{0, 0, 0, 0};
+        if (lane < 16) {  // the lanes of an operand's first eight k
+            if (k_contiguous) {
+                w = raw8(base, row * ld + p.K);
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    w[i] = p.k_ragged8 >= 2 * i + 2 ? w[i] : (p.k_ragged8 == 2 * i + 1 ? (w[i] & 0xffffu) : 0u);
+            } else {
+#pragma unroll
+                for (int k = 0; k < 7; ++k)
+                    if (k < p.k_ragged8)
+                        w[k / 2] |= (unsigned)((const unsigned short*)base)[(p.K + k) * ld + row] << (16 * (k & 1));
+            }
+        }
+        return __builtin_bit_cast(i16x8_t, w);
+    };
+    const int r = lane & 15;
+    i16x8_t fb[C::FN];
+#pragma unroll
+    for (int j = 0; j < C::FN; ++j) {
+        const int64_t n = ml.n0 + ml.wn * C::WTN + 16 * j + r;
+        fb[j] = piece(p.B, p.ldb, C::B_KC, n < p.N ? n : p.N - 1);
+    }
+#pragma unroll
+    for (int i = 0; i < C::FM; ++i) {
+        const int64_t m = ml.m0 + ml.wm * C::WTM + 16 * i + r;
+        const i16x8_t fa = piece(p.A, p.lda, C::A_KC, m < p.M ? m : p.M - 1);
+#pragma unroll
+        for (int j = 0; j < C::FN; ++j) acc[i][j] = mfma<C::FP16>(fb[j], fa, acc[i][j]);
     }
 }
 
@@ -307,6 +363,8 @@ __global__ __launch_bounds__(C::NT) void gemm_epi_kernel(const Params p, const E
         int lane = ml.lane;
         asm volatile("" : "+v"(lane));
         if constexpr (!EARLY) load_bias(ml.n0 + ml.wn * C::WTN + (lane % (C::WTN / 8)) * 8);
+        if constexpr (C::OPK == OP_GEMM)
+            if (p.k_ragged8) add_k_tail<C>(p, ml, acc, lane);
         ring_barrier();  // every wave has finished reading the ring
         epi_passes<C, 0, BWD>(ml, acc, stage_piece<C, PIECE>(ml.wave), p, e, bias, lane);
     });
@@ -335,6 +393,8 @@ __global__ __launch_bounds__(C::NT) void gemm_part_kernel(const Params p) {
         int lane = ml.lane;
         asm volatile("" : "+v"(lane));
         IGC_LDS char* reg = stage_piece<C, PIECE>(ml.wave);
+        if constexpr (C::OPK == OP_GEMM)
+            if (p.k_ragged8 && split == p.k_splits - 1) add_k_tail<C>(p, ml, acc, lane);
         ring_barrier();  // every wave has finished reading the ring
         static_for<0, (C::FM + 3) / 4>([&](auto PASS) __attribute__((always_inline)) {
             constexpr int I0 = 4 * PASS, NI = C::FM - I0 < 4 ? C::FM - I0 : 4;

@@ -14,7 +14,7 @@ using Here = Cfg<FP16, IGC_BM, IGC_BN, IGC_BK, IGC_D, IGC_W, IGC_MI, IGC_HALF, I
 
 template <class C, int V, bool BWD>
 constexpr const void* kernel_of() {
-    if constexpr (!variant_applies<C, V>() || (BWD && C::OPK != OP_GEMM))
+    if constexpr (!variant_applies<C, V>() || V == RAGGED || (BWD && C::OPK != OP_GEMM))
         return nullptr;
     else
         return reinterpret_cast<const void*>(&gemm_epi_kernel<C, V, BWD>);
@@ -24,7 +24,7 @@ constexpr const void* kernel_of() {
 // only by request, keep the plain kernel.
 template <class C, int V>
 constexpr const void* part_of() {
-    if constexpr (!variant_applies<C, V>() || C::BM * C::BN > 256 * 128)
+    if constexpr (!variant_applies<C, V>() || V == RAGGED || C::BM * C::BN > 256 * 128)
         return nullptr;
     else
         return reinterpret_cast<const void*>(&gemm_part_kernel<C, V>);

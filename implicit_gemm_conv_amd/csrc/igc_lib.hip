@@ -154,7 +154,7 @@ struct Plan {
 static Plan pick(const igc_tune_t* tune, bool fp16, bool a_kc, bool b_kc, int op, int64_t M, int64_t N, int64_t K,
                  bool epilogue = false) {
     Plan pl;
-    pl.tune = tune ? *tune : (epilogue ? epilogue_tune(M, N, K, op) : default_tune(M, N, K, op));
+    pl.tune = tune ? *tune : (epilogue ? epilogue_tune(M, N, K, op, a_kc) : default_tune(M, N, K, op));
     const igc_tune_t& t = pl.tune;
     pl.inst = find_instance(t, fp16, a_kc, b_kc, op);
     pl.valid = t.stream_k >= 0 && !(t.k_splits > 1 && t.stream_k > 0) && (t.sk_hybrid == 0 || t.sk_hybrid == 1) &&
@@ -251,10 +251,15 @@ static igc_status_t launch(const Plan& pl, Params p, const Epi* epi, void* user_
         if (span(p.ldc, p.out_kind) || (epi->res && span(epi->ldr, epi->res_kind)) ||
             (epi->pre && span(epi->ldp, epi->pre_kind)))
             return IGC_ERR_UNSUPPORTED;
-        fn = ei ? ei->fn[epi->backward ? 1 : 0][v] : nullptr;
+        fn = ei ? ei->fn[epi->backward ? 1 : 0][v == RAGGED ? PLAIN : v] : nullptr;
     }
+    bool tail = epi && L.S == 1 && !loose && v == RAGGED;  // a kernel that adds the last K % 8 by itself
     // parts of a K split through staged stores, where they are built and the sub-tile's offsets fit
-    if (ei && L.S > 1 && ei->part[v] && inst->bm * L.ldws * 4 < 0x7fff0000LL) fn = ei->part[v];
+    if (const void* part = ei && L.S > 1 ? ei->part[v == RAGGED ? PLAIN : v] : nullptr;
+        part && inst->bm * L.ldws * 4 < 0x7fff0000LL) {
+        fn = part;
+        tail = v == RAGGED;
+    }
     if (!fn) return IGC_ERR_UNSUPPORTED;
     if (user_ws && (user_ws_bytes < L.bytes || (reinterpret_cast<uintptr_t>(user_ws) & 255u)))
         return IGC_ERR_INVALID_VALUE;
@@ -302,6 +307,10 @@ static igc_status_t launch(const Plan& pl, Params p, const Epi* epi, void* user_
             arg.ldc = L.ldws;
             arg.out_kind = OUT_F32;
             arg.vec_ok = 1;
+        }
+        if (tail) {
+            arg.k_ragged8 = (int)(p.K % 8);
+            arg.K -= arg.k_ragged8;
         }
         Epi earg = epi ? *epi : Epi{};
         void* args[] = {&arg, &earg};  // (the plain kernels take the first alone)
@@ -775,11 +784,17 @@ igc_status_t conv2d_nhwc_implicit_gemm_epilogue_fp16_ex(int N, int H, int W, int
 
 int64_t igc_epilogue_workspace_bytes(igc_op_t op, int64_t M, int64_t N, int64_t K, const igc_tune_t* tune) {
     if (M < 0 || N < 0 || K < 0 || (op != IGC_OP_GEMM && op != IGC_OP_CONV_FPROP)) return -1;
-    const Plan pl = pick(tune, false, true, true, (int)op, M, N, K, true);
-    if (!pl.valid || !pl.inst) return -1;
-    if (M == 0 || N == 0) return 0;
-    int64_t bytes = layout_of(pl, M, N, K, op == IGC_OP_CONV_FPROP && N % 8 != 0).bytes;
-    if (op == IGC_OP_GEMM && !tune && M <= kFewRows)  // the operand layouts decide which kernel runs: room for either
+    int64_t bytes = 0;
+    for (const bool a_kc : {true, false}) {  // room for every operand layout
+        if (op != IGC_OP_GEMM && !a_kc) break;
+        Plan pl = pick(tune, false, a_kc, true, (int)op, M, N, K, true);
+        if (!pl.inst && !a_kc) continue;  // a configuration built for row-major A alone
+        if (!pl.valid || !pl.inst) return -1;
+        if (M == 0 || N == 0) return 0;
+        const int64_t q = layout_of(pl, M, N, K, op == IGC_OP_CONV_FPROP && N % 8 != 0).bytes;
+        bytes = q > bytes ? q : bytes;
+    }
+    if (op == IGC_OP_GEMM && !tune && M <= kFewRows)
         for (const bool b_kc : {false, true}) {
             const int64_t few = few_rows_bytes(few_rows_plan(M, N, K, b_kc), M, N);
             bytes = few > bytes ? few : bytes;

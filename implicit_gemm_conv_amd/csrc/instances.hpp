@@ -23,7 +23,8 @@ struct EpiInstance {
     int bm, bn, bk, d, waves, mfma, half, loaders, sync;
     int op;
     bool fp16, a_kc, b_kc;
-    const void* fn[2][4];  // forward and backward, by loop variant; nullptr where not built
+    // forward and backward, by loop variant; nullptr where not built (RAGGED: PLAIN, whose epilogue adds the K tail)
+    const void* fn[2][4];
     const void* part[4];   // one part of a K split, for the epilogue to follow
 };
 
@@ -36,7 +37,7 @@ void register_epilogues(const EpiInstance* table, int count);
 const EpiInstance* find_epilogue(const Instance& inst);
 igc_tune_t default_tune(int64_t M, int64_t N, int64_t K, int op);
 // The built-in choice for a call with an epilogue: no stream-K.
-igc_tune_t epilogue_tune(int64_t M, int64_t N, int64_t K, int op);
+igc_tune_t epilogue_tune(int64_t M, int64_t N, int64_t K, int op, bool a_kc);
 int num_tunes();
 igc_tune_t tune_at(int i);
 int tune_scope(int i);

@@ -166,15 +166,25 @@ igc_tune_t default_tune(int64_t M, int64_t N, int64_t K, int op) {
 // which give way to the same smaller tiles (7326 x 48 x 936, 58 tiles of 128 x
 // 64: 17.1 us, 115 of 64 x 64 9.4; 12032 x 72 x 192, 188 and 188 of 64 x 128: 7.7
 // and 6.5).
-igc_tune_t epilogue_tune(int64_t M, int64_t N, int64_t K, int op) {
+igc_tune_t epilogue_tune(int64_t M, int64_t N, int64_t K, int op, bool a_kc) {
     igc_tune_t t = default_tune(M, N, K, op);
     constexpr int64_t kCUs = 256;
+    if (op == IGC_OP_GEMM && (t.bm == 256 || (t.bm == 128 && t.bn == 128 && t.stream_k == 0 && t.k_splits <= 1))) {
+        // 256 x 256 tiles where they need a third of the rounds of 128 x 128, which their epilogue makes dearer than
+        // the plain calls' (3000 x 3000 x 1000 40.7 us in three rounds, 33.6 in one; 1800 x 5500 x 2048 50.9 and 47.0;
+        // 4000 x 3000 x 64 17.6 and 15.9).  Not with a column-major A, whose transposing LDS reads make their loading
+        // waves spill: 8192^3 2257 us, 256 x 128 tiles 847; 4096 x 4096 x 1024 83.7 and 45.5.
+        const auto rounds = [&](int64_t bm, int64_t bn) { return (((M + bm - 1) / bm) * ((N + bn - 1) / bn) + kCUs - 1) / kCUs; };
+        if (rounds(256, 256) * 100 <= rounds(128, 128) * 34)
+            return a_kc ? igc_tune_t{256, 256, 64, 2, 8, 16, 1, 4, 1, 0, 0, 0} : igc_tune_t{256, 128, 64, 3, 8, 16, 0, 4, 1, 0, 0, 0};
+    }
     const bool narrow = t.bn == 64 && ((M + 63) / 64) * ((N + 127) / 128) <= kCUs;
     if (!narrow && (t.bm != 128 || t.bn != 128)) return t;
     // Two rounds of 128 x 128 tiles against one of 256 x 128: 1024 x 8192 x 1024 27 and 22 us, 1536 x 4096 x 4096
-    // 63 and 50 (192 tiles); with 160 tiles they tie or lose (1000 x 5000 x 1024 23 and 25).
+    // 63 and 50 (192 tiles), 6000 x 800 x 800 22.3 and 18.7 (168); with 160 tiles they tie or lose (1000 x 5000 x 1024
+    // 23 and 25).
     const int64_t tall = ((M + 255) / 256) * ((N + 127) / 128), rounds_tall = (tall + kCUs - 1) / kCUs;
-    if (op == IGC_OP_GEMM && t.stream_k == 0 && t.k_splits <= 1 && tall * 10 >= rounds_tall * kCUs * 7 &&
+    if (op == IGC_OP_GEMM && t.stream_k == 0 && t.k_splits <= 1 && tall * 100 >= rounds_tall * kCUs * 65 &&
         (((M + 127) / 128) * ((N + 127) / 128) + kCUs - 1) / kCUs >= 2 * rounds_tall)
         return igc_tune_t{256, 128, 64, 3, 8, 16, 0, 4, 1, 0, 0, 0};
     // A convolution of shallow K in several rounds of 128 x 128 tiles is bound by its loads and stores, as with up to

@@ -558,6 +558,21 @@ def test_parts_of_every_tile(cfg):
             p.check(p.run(tune=igc.tune(cfg, k_splits=s)), f"{cfg} {M}x{N}x{K} in {s}")
 
 
+@pytest.mark.parametrize("cfg", GEMM_TILES, ids=str)
+def test_k_tails_of_every_tile(cfg):
+    """The last K % 8, with NaN behind every row: K below 8, around a K tile, and parts that are a tail alone."""
+    for K in (1, 5, 7, 9, 63, 65, 517, 1030):
+        for la, lb in itertools.product(("row", "col"), repeat=2):
+            say(f"tail {cfg} {K} {la} {lb}")
+            p = Problem(133, 75, K, "bf16" if K % 2 else "fp16", la=la, lb=lb, act="silu", pre="in", seed=K)
+            p.check(p.run(tune=igc.tune(cfg)), f"{cfg} {K} {la} {lb}")
+            if K > 500:
+                for s in (2, 3, 5):
+                    p.check(p.run(tune=igc.tune(cfg, k_splits=s)), f"{cfg} {K} {la} {lb} in {s}")
+        q = Problem(70, 130, K, "fp16", lb="row", act="gelu", backward=True, seed=K)
+        q.check(q.run(tune=igc.tune(cfg)), f"{cfg} {K} backward")
+
+
 @pytest.mark.parametrize("cfg", igc.tunes(igc.SCOPE_EPILOGUE), ids=str)
 def test_convolution_parts_of_every_tile(cfg):
     """The same of the convolution, with filter counts that no vector fits."""
