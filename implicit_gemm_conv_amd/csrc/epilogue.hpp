@@ -153,28 +153,44 @@ struct EpiMatrix {
             store(q, whole, 0, __builtin_bit_cast(u32x4s_t, f32x4s_t{v[0], v[1], v[2], v[3]}));
             store(q, whole, 1, __builtin_bit_cast(u32x4s_t, f32x4s_t{v[4], v[5], v[6], v[7]}));
             if (tail && __builtin_amdgcn_ballot_w64(part)) {
-                if (tail & 4) store(q, part, 0, __builtin_bit_cast(u32x4s_t, f32x4s_t{v[0], v[1], v[2], v[3]}));
-                const int at = part ? (int)(first + q * step) + 4 * (tail & 4) : (int)kOob;
-                const float a0 = tail & 4 ? v[4] : v[0], a1 = tail & 4 ? v[5] : v[1], a2 = tail & 4 ? v[6] : v[2];
-                if (tail & 2)
-                    __builtin_amdgcn_raw_buffer_store_b64(
-                        u32x2e_t{__builtin_bit_cast(unsigned, a0), __builtin_bit_cast(unsigned, a1)}, rs, at, 0, 0);
-                if (tail & 1)
-                    __builtin_amdgcn_raw_buffer_store_b32(__builtin_bit_cast(unsigned, tail & 2 ? a2 : a0), rs,
-                                                          part ? at + 4 * (tail & 2) : (int)kOob, 0, 0);
+                const int at = part ? (int)(first + q * step) : (int)kOob;
+                const auto rest = [&](float x, float y, float z, int o) __attribute__((always_inline)) {
+                    if (tail & 2) {
+                        __builtin_amdgcn_raw_buffer_store_b64(
+                            u32x2e_t{__builtin_bit_cast(unsigned, x), __builtin_bit_cast(unsigned, y)}, rs, o, 0, 0);
+                        if (tail & 1)
+                            __builtin_amdgcn_raw_buffer_store_b32(__builtin_bit_cast(unsigned, z), rs, part ? o + 8 : o, 0, 0);
+                    } else if (tail & 1) {
+                        __builtin_amdgcn_raw_buffer_store_b32(__builtin_bit_cast(unsigned, x), rs, o, 0, 0);
+                    }
+                };
+                if (tail & 4) {
+                    store(q, part, 0, __builtin_bit_cast(u32x4s_t, f32x4s_t{v[0], v[1], v[2], v[3]}));
+                    rest(v[4], v[5], v[6], part ? at + 16 : at);
+                } else {
+                    rest(v[0], v[1], v[2], at);
+                }
             }
         } else {
             const u32x4s_t w = kind == KIND_BF16 ? pack8<false>(v) : pack8<true>(v);
             store(q, whole, 0, w);
             if (tail && __builtin_amdgcn_ballot_w64(part)) {
                 const int at = part ? (int)(first + q * step) : (int)kOob;
-                if (tail & 4) __builtin_amdgcn_raw_buffer_store_b64(u32x2e_t{w[0], w[1]}, rs, at, 0, 0);
-                if (tail & 2)
-                    __builtin_amdgcn_raw_buffer_store_b32(tail & 4 ? w[2] : w[0], rs, part ? at + 2 * (tail & 4) : at, 0, 0);
-                if (tail & 1)
-                    __builtin_amdgcn_raw_buffer_store_b16(
-                        (unsigned short)(tail & 4 ? (tail & 2 ? w[3] : w[2]) : (tail & 2 ? w[1] : w[0])), rs,
-                        part ? at + 2 * (tail & 6) : at, 0, 0);
+                // (branches, not selects: those between two elements of a register array go through scratch)
+                const auto rest = [&](unsigned x, unsigned y, int o) __attribute__((always_inline)) {
+                    if (tail & 2) {
+                        __builtin_amdgcn_raw_buffer_store_b32(x, rs, o, 0, 0);
+                        if (tail & 1) __builtin_amdgcn_raw_buffer_store_b16((unsigned short)y, rs, part ? o + 4 : o, 0, 0);
+                    } else if (tail & 1) {
+                        __builtin_amdgcn_raw_buffer_store_b16((unsigned short)x, rs, o, 0, 0);
+                    }
+                };
+                if (tail & 4) {
+                    __builtin_amdgcn_raw_buffer_store_b64(u32x2e_t{w[0], w[1]}, rs, at, 0, 0);
+                    rest(w[2], w[3], part ? at + 8 : at);
+                } else {
+                    rest(w[0], w[1], at);
+                }
             }
         }
     }
