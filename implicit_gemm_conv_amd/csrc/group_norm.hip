@@ -188,7 +188,7 @@ __global__ __launch_bounds__(kGnThreads) void gn_partial_kernel(const GnArgs a) 
         }
     }
     __syncthreads();
-    const GnLanes j(here / a.uw);
+    const GnLanes j(nch / a.uw);  // (of a full slab: the order of a unit's sum is the same in every slab)
     for (int u = j.item; u < here / a.uw; u += j.step) {  // the channels of a unit, equal in number of pixels
         float mean = 0.0f, m2 = 0.0f;
         for (int c = j.lane; c < a.uw; c += j.lanes) mean += smean[u * a.uw + c];
@@ -206,27 +206,32 @@ __global__ __launch_bounds__(kGnThreads) void gn_partial_kernel(const GnArgs a) 
     }
 }
 
-// The groups that the channels of a slab belong to.
+// The groups that the channels of a slab belong to.  A group may lie across
+// slabs, whose workgroups each join it for themselves: `shared` groups are what
+// the join's lanes are dealt for, the same number in every slab, so that all of
+// them add in one order and get the same bits.
 struct GnGroups {
-    int g0, count;
+    int c0, g0, count, shared;
     __device__ __forceinline__ explicit GnGroups(const GnArgs& a) {
-        const int c0 = (int)blockIdx.x % a.slabs * a.sv * 8;
+        c0 = (int)blockIdx.x % a.slabs * a.sv * 8;
         const int c1 = (c0 + a.sv * 8 < a.C ? c0 + a.sv * 8 : a.C) - 1;
         g0 = group_of(a, c0);
         count = group_of(a, c1) - g0 + 1;
+        shared = a.slabs > 1 ? group_of(a, a.sv * 8) + 1 : a.G;
     }
 };
 
 constexpr int kGnThreadsChannels = kGnThreads * 8;  // channels of a slab at most, so its groups
 
 // Joins the chunks of the slab's groups into their statistics, to sm and sr by
-// group of the slab; the first chunk's workgroups write them out.  The chunks'
+// group of the slab; of the first chunk's workgroups the one whose slab holds a
+// group's first channel writes them out.  The chunks'
 // means are taken about the first one's, one pass over the pairs: what that
 // loses is at most the number of chunks times a rounding, since the first chunk
 // is part of the variance.
 __device__ __forceinline__ void join_chunks(const GnArgs& a, int n, int chunk, float* sm, float* sr) {
     const GnGroups gs(a);
-    const GnLanes j(gs.count);
+    const GnLanes j(gs.shared);
     const int upg = a.cpg / a.uw, pairs = upg * a.chunks;
     const float total = (float)a.HW * (float)a.cpg;
     const float full = (float)a.pixels * (float)a.uw;
@@ -260,8 +265,9 @@ __device__ __forceinline__ void join_chunks(const GnArgs& a, int n, int chunk, f
             const float mean = m0 + dm, rstd = 1.0f / __builtin_sqrtf((m2 < 0.0f ? 0.0f : m2) / total + a.eps);
             sm[g] = mean;
             sr[g] = rstd;
-            if (chunk == 0 && a.mean) a.mean[n * a.G + gs.g0 + g] = mean;
-            if (chunk == 0 && a.rstd) a.rstd[n * a.G + gs.g0 + g] = rstd;
+            const bool first = chunk == 0 && (gs.g0 + g) * a.cpg >= gs.c0;
+            if (first && a.mean) a.mean[n * a.G + gs.g0 + g] = mean;
+            if (first && a.rstd) a.rstd[n * a.G + gs.g0 + g] = rstd;
         }
     }
     __syncthreads();
@@ -393,7 +399,7 @@ __global__ __launch_bounds__(kGnThreads) void gn_backward_partial_kernel(const G
         s2[ch] = ga * t2;
     }
     __syncthreads();
-    const GnLanes j(here / a.uw);
+    const GnLanes j(nch / a.uw);
     for (int u = j.item; u < here / a.uw; u += j.step) {
         float t1 = 0.0f, t2 = 0.0f;
         for (int c = j.lane; c < a.uw; c += j.lanes) {
@@ -465,7 +471,7 @@ __global__ __launch_bounds__(kGnThreads) void gn_backward_apply_kernel(const GnA
     load(s.p0 + s.p);  // on its way during the join
     const GnGroups gs(a);
     {
-        const GnLanes j(gs.count);
+        const GnLanes j(gs.shared);
         const int upg = a.cpg / a.uw, pairs = upg * a.chunks;
         const float rn = 1.0f / ((float)a.HW * (float)a.cpg);
         for (int g = j.item; g < gs.count; g += j.step) {

@@ -418,3 +418,30 @@ def test_chunks_slabs_and_units(shape):
     p.check_forward(*p.forward(y=x, x=x), f"{shape} in place")
     dy = p.dy.clone()
     p.check_backward(*p.backward(dx=dy, dy=dy), f"{shape} in place")
+
+
+@pytest.mark.parametrize("shape", [(2, 32, 32, 2560, 32), (1, 32, 32, 4128, 86), (2, 20, 30, 2072, 7)])
+def test_a_group_has_one_result_whichever_slab_it_lies_in(shape):
+    """Every group holds the same values, and some lie across two workgroups' channels: the statistics, outputs and
+    gradients of all of them are the same to the last bit, on every call."""
+    N, H, W, C, G = shape
+    g = generator(sum(shape))
+    for dtype in ("bf16", "fp16"):
+        say(f"slabs {shape} {dtype}")
+        one = normal(g, N, H, W, 1, C // G) * 1.5 + normal(g, C // G)
+        p = Norm(*shape, dtype=dtype, act="silu", affine=False, x=one.expand(N, H, W, G, C // G).reshape(N, H, W, C))
+        p.dy = p.wide(normal(g, N, H, W, 1, C // G, dtype=p.t).expand(N, H, W, G, C // G).reshape(N, H, W, C))
+        y, mean, rstd = p.forward()
+        p.check_forward(y, mean, rstd, f"{shape}")
+        dx, dg, db = p.backward(mean=mean, rstd=rstd)
+        p.check_backward(dx, dg, db, f"{shape}")
+        for what, v in (("mean", mean), ("rstd", rstd), ("y", p.inside(y, "y").transpose(1, 2).reshape(N, G, -1)),
+                        ("dx", p.inside(dx, "dx").transpose(1, 2).reshape(N, G, -1)), ("dgamma", dg.reshape(1, G, -1)),
+                        ("dbeta", db.reshape(1, G, -1))):
+            assert torch.equal(v, v[:, :1].expand_as(v).contiguous()), f"{what}: groups of equal values differ"
+        for _ in range(5):
+            again = p.forward()
+            grads = p.backward(mean=mean, rstd=rstd)
+            synchronize()
+            for a, b in zip((y, mean, rstd, dx, dg, db), again + grads):
+                assert torch.equal(a.view(torch.uint8), b.view(torch.uint8)), "two runs differ"
