@@ -2,8 +2,10 @@
 
 Every function here forwards to the C entry point of the same name in
 implicit_gemm_conv_amd/libigc.so and returns its igc_status_t as an int.
-Tensor arguments may be torch tensors (their data_ptr() is passed) or plain
-integer device addresses.  `stream` defaults to torch's current HIP stream.
+Tensor arguments may be torch tensors (their data_ptr() is passed) on the GPU
+or in pinned memory -- others raise ValueError, since the GPU would fault on a
+host address -- or plain integer device addresses.  `stream` defaults to
+torch's current HIP stream.
 All computation happens in the HIP kernels; there is no fallback: if the
 library is not built, every call raises.
 
@@ -105,6 +107,15 @@ _EPILOGUE = struct.Struct("@iiPiPqiPqi0q")  # igc_epilogue_t, the layout of CEpi
 assert _EPILOGUE.size == ctypes.sizeof(CEpilogue)
 
 
+def _on_host(x):
+    """Whether a tensor that is not a GPU's lies where the GPU cannot reach it.  (Plain addresses cannot be told apart.)"""
+    return x.data_ptr() != 0 and x.nbytes != 0 and not x.is_pinned()
+
+
+def _refuse_host(what):
+    raise ValueError(f"{what} is in host memory, where the GPU cannot reach it")
+
+
 def _bias(x, code):
     try:
         ptr = x.data_ptr()
@@ -135,12 +146,17 @@ class Epilogue:
     """A fused epilogue (igc_epilogue_t) from tensors: types come from their dtypes, the leading dimensions of a
     `residual` and `pre` of two dimensions from their first stride unless given (a convolution's are not looked at),
     and the tensors are kept alive with it.  A raw device address needs its type (bias_type, residual_type, pre_type:
-    an OUT_ code) and leading dimension.  `raw` holds the packed C structure: calls take it as it is."""
-    __slots__ = ("raw", "_keep")
+    an OUT_ code) and leading dimension.  `raw` holds the packed C structure: calls take it as it is, and refuse one
+    whose tensors are in host memory."""
+    __slots__ = ("raw", "_keep", "_host")
 
     def __init__(self, act="none", bias=None, residual=None, pre=None, backward=False, ldr=None, ldp=None,
                  bias_type=None, residual_type=None, pre_type=None):
         self._keep = (bias, residual, pre)
+        self._host = None
+        for name, x in (("bias", bias), ("residual", residual), ("pre", pre)):
+            if x is not None and not getattr(x, "is_cuda", True) and _on_host(x):
+                self._host = name
         self.raw = _EPILOGUE.pack(act_code(act), backward, *((0, 0) if bias is None else _bias(bias, bias_type)),
                                   *((0, 0, 0) if residual is None else _matrix(residual, residual_type, ldr)),
                                   *((0, 0, 0) if pre is None else _matrix(pre, pre_type, ldp)))
@@ -239,10 +255,15 @@ def lib():
 
 def _ptr(x):
     """A tensor's device address, or an address as it is."""
+    if x is None or type(x) is int:
+        return x
     try:
-        return x.data_ptr()
+        ptr = x.data_ptr()
     except AttributeError:
-        return None if x is None else int(x)
+        return int(x)
+    if not getattr(x, "is_cuda", True) and _on_host(x):
+        _refuse_host("a tensor")
+    return ptr
 
 
 def _nbytes(x):
@@ -343,7 +364,11 @@ conv2d_nhwc_wgrad_implicit_gemm_fp16_ex = _conv_ex("conv2d_nhwc_wgrad_implicit_g
 
 
 def _epi(e):
-    return e.raw if isinstance(e, Epilogue) else None if e is None else bytes(e)
+    if isinstance(e, Epilogue):
+        if e._host:
+            _refuse_host("the epilogue's " + e._host)
+        return e.raw
+    return None if e is None else bytes(e)
 
 
 def _entry(name):

@@ -643,3 +643,20 @@ def test_activation_over_the_whole_range(act):
     fin = torch.isfinite(zd)
     assert ((got - want).abs()[fin] <= GRAD_ABS).all()
     assert act == "none" or torch.isnan(got[-2])
+
+
+def test_pinned_tensors_are_read_and_written():
+    """Pinned memory is the GPU's to reach: operands, bias, residual and output there give the same bits."""
+    for M in (3, 100):
+        p = Problem(M, 72, 64, "bf16", act="silu", seed=M)
+        want = p.run()
+        synchronize()
+        pinned = {n: torch.empty(v.shape, dtype=v.dtype, pin_memory=True).copy_(v)
+                  for n, v in (("Abuf", p.Abuf), ("Bbuf", p.Bbuf), ("bias", p.bias), ("D", want))}
+        res = torch.zeros(M, p.ldd, dtype=p.res.dtype, pin_memory=True)
+        res[:, :72].copy_(p.res)
+        p.Abuf, p.Bbuf, p.bias, D = (pinned[n] for n in ("Abuf", "Bbuf", "bias", "D"))
+        D.fill_(float("nan"))
+        p.run(D=D, epilogue=p.epilogue(residual=res))
+        synchronize()
+        assert torch.equal(D[:M, :72], want[:M, :72].cpu()) and torch.isnan(D[M:].float()).all()

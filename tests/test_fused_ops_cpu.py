@@ -158,3 +158,34 @@ def test_binding():
     assert igc.Epilogue(residual=P, ldr=8, residual_type=1).c.ldr == 8
     assert ctypes.sizeof(igc.CEpilogue) == 72 and len(e.raw) == 72
     assert bytes(e.c) == e.raw
+
+
+def test_host_tensors_are_refused():
+    """Every call refuses a tensor in host memory, in each of its places, and an epilogue that holds one, before the
+    library is entered; what holds no values and plain addresses pass."""
+    t, v = torch.zeros(64, 64, dtype=torch.bfloat16), torch.zeros(64)
+    gemm, conv = dict(GEMM_CALL, N=16, ldd=16), CONV_CALL
+    calls = [(igc.gemm_bf16, gemm, "ABD", ()), (igc.gemm_bf16_ex, gemm, "ABD", (None,)), (igc.gemm_bf16_noalloc, gemm, "ABD", ()),
+             (igc.conv2d_nhwc_implicit_gemm, conv, "xwy", ()), (igc.conv2d_nhwc_wgrad_implicit_gemm_ex, conv, "xwy", (None,)),
+             (igc.gemm_bf16_epilogue, gemm, "ABD", (epi(),)), (igc.gemm_fp16_epilogue_ex, gemm, "ABD", (epi(), None)),
+             (igc.conv2d_nhwc_implicit_gemm_epilogue, conv, "xwy", (epi(),)),
+             (igc.epilogue_backward_bf16, BACK_CALL, ("dD", "pre", "dz", "dbias"), ()),
+             (igc.epilogue_backward_fp16_ex, BACK_CALL, ("dD", "pre", "dz", "dbias"), ()),
+             (igc.group_norm_nhwc_bf16, NORM_CALL, ("x", "gamma", "beta", "y", "mean", "rstd"), ()),
+             (igc.group_norm_nhwc_fp16_ex, NORM_CALL, ("x", "gamma", "beta", "y", "mean", "rstd"), ()),
+             (igc.group_norm_nhwc_backward_bf16, NORM_BACK, ("x", "gamma", "beta", "mean", "rstd", "dy", "dx", "dgamma", "dbeta"), ())]
+    for f, args, names, more in calls:
+        for name in names:
+            with pytest.raises(ValueError, match="host memory"):
+                f(*{**args, name: t}.values(), *more, stream=0)
+    with pytest.raises(ValueError, match="host memory"):
+        igc.gemm_bf16_ex(*gemm.values(), None, torch.zeros(256, dtype=torch.uint8), stream=0)
+    for parts in (dict(bias=v), dict(residual=t), dict(pre=t)):
+        e = igc.Epilogue(**parts)  # the structure itself is made
+        with pytest.raises(ValueError, match="host memory"):
+            igc.gemm_bf16_epilogue(*gemm.values(), e, stream=0)
+        with pytest.raises(ValueError, match="host memory"):
+            igc.conv2d_nhwc_implicit_gemm_epilogue_ex(*conv.values(), e, stream=0)
+    none = torch.empty(0)
+    assert igc.gemm_bf16_epilogue(*{**gemm, "M": 0, "A": none, "D": none}.values(), epi(), stream=0) == igc.IGC_OK
+    assert igc.gemm_bf16_epilogue(*{**gemm, "M": 0}.values(), igc.Epilogue(residual=P, ldr=64, residual_type=1), stream=0) == igc.IGC_OK
