@@ -129,6 +129,9 @@ __global__ __launch_bounds__(32 * kSumLanes) void column_sum_kernel(const float*
 // 7.5.  Without: 1024 x 4096 5.1 against 7.9.
 constexpr int64_t kBackTallRows = 384, kBackTallSums = 1024;
 
+// Sizes beyond these are refused (back_plan's numbers of blocks are ints).
+static bool too_large(int64_t M, int64_t N) { return N >= (1ll << 31) || M >= (1ll << 40); }
+
 struct BackPlan {
     bool tall;  // one workgroup of 1024 threads for 64 columns and all rows
     int cl_shift, col_blocks, chunks;
@@ -177,7 +180,7 @@ static igc_status_t backward_any(bool fp16, int64_t M, int64_t N, igc_act_t act,
             return IGC_ERR_MISALIGNED;
     }
     if (dbias && reinterpret_cast<uintptr_t>(dbias) % out_size(bias_type)) return IGC_ERR_MISALIGNED;
-    if (N >= (1ll << 31) || M >= (1ll << 40)) return IGC_ERR_UNSUPPORTED;
+    if (too_large(M, N)) return IGC_ERR_UNSUPPORTED;
     const BackPlan pl = back_plan(M, N, dz != nullptr, dbias != nullptr);
     if ((int64_t)pl.col_blocks * pl.chunks > 0x7fffffff) return IGC_ERR_UNSUPPORTED;
     Workspace ws;
@@ -255,7 +258,7 @@ igc_status_t epilogue_backward_fp16_ex(int64_t M, int64_t N, igc_act_t act, cons
 }
 
 int64_t igc_epilogue_backward_workspace_bytes(int64_t M, int64_t N) {
-    if (M < 0 || N < 0) return -1;
+    if (M < 0 || N < 0 || too_large(M, N)) return -1;
     return N == 0 ? 0 : back_bytes(back_plan(M, N, true, true), N);
 }
 

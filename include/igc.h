@@ -377,7 +377,8 @@ int64_t igc_epilogue_workspace_bytes(igc_op_t op, int64_t M, int64_t N, int64_t 
  * dbias_type, aligned to its size); dbias NULL: only dz; both NULL is
  * IGC_ERR_INVALID_VALUE.  pre is read only when act is not IGC_ACT_NONE.  dz
  * may be dD or pre (same leading dimension).  M == 0 writes dbias = 0.
- * Workspace when dbias is given: igc_epilogue_backward_workspace_bytes.
+ * N >= 2^31 or M >= 2^40 is IGC_ERR_UNSUPPORTED.  Workspace when dbias is
+ * given: igc_epilogue_backward_workspace_bytes (-1 for sizes that the call refuses).
  */
 igc_status_t epilogue_backward_bf16(int64_t M, int64_t N, igc_act_t act, const void *dD, int64_t ldd, const void *pre,
                                     int64_t ldp, void *dz, int64_t ldz, void *dbias, igc_out_t dbias_type,

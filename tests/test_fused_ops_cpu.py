@@ -2,6 +2,8 @@
 workspaces, and the binding marshals what it is given.  No GPU is used."""
 import ctypes
 import os
+import subprocess
+import sys
 
 import pytest
 import torch
@@ -189,3 +191,27 @@ def test_host_tensors_are_refused():
     none = torch.empty(0)
     assert igc.gemm_bf16_epilogue(*{**gemm, "M": 0, "A": none, "D": none}.values(), epi(), stream=0) == igc.IGC_OK
     assert igc.gemm_bf16_epilogue(*{**gemm, "M": 0}.values(), igc.Epilogue(residual=P, ldr=64, residual_type=1), stream=0) == igc.IGC_OK
+
+
+def test_workspace_queries_of_impossible_sizes():
+    """The queries answer for any sizes, those that no call takes included (in a process of its own: a division by a
+    block count cut to 32 bits ended it)."""
+    code = """if True:
+        import implicit_gemm_conv_amd as igc
+        for k in (31, 32, 39, 40, 41, 47, 62):
+            for d in (-257, -1, 0, 1):
+                big = (1 << k) + d
+                assert igc.igc_epilogue_backward_workspace_bytes(1000, big) == (-1 if big >= 1 << 31 else 0), big
+                assert (igc.igc_epilogue_backward_workspace_bytes(big, 8) == -1) == (big >= 1 << 40), big
+                for op in (igc.OP_GEMM, igc.OP_CONV_FPROP):
+                    for sizes in ((big, 8, 8), (8, big, 8), (8, 8, big), (1, big, 4096), (big, 8, 4096)):
+                        igc.igc_epilogue_workspace_bytes(op, *sizes)
+        for sizes in ((2**31 - 1, 1, 1, 8, 1), (1, 2**31 - 1, 2**31 - 1, 8, 1), (1, 1, 1, 2**31 - 8, 1), (1, 46340, 46341, 8, 8)):
+            assert igc.igc_group_norm_workspace_bytes(*sizes) >= -1
+    """
+    r = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True,
+                       cwd=os.path.dirname(os.path.dirname(os.path.abspath(__file__))))
+    assert r.returncode == 0, (r.returncode, r.stderr[-500:])
+    for f in (igc.epilogue_backward_bf16, igc.epilogue_backward_fp16):
+        assert f(*{**BACK_CALL, "N": 1 << 31, "ldd": 1 << 31, "ldp": 1 << 31, "ldz": 1 << 31}.values(), stream=0) == UNSUPPORTED
+        assert f(*{**BACK_CALL, "M": 1 << 40}.values(), stream=0) == UNSUPPORTED
