@@ -140,7 +140,7 @@ struct BackPlan {
 
 static BackPlan back_plan(int64_t M, int64_t N, bool dz, bool dbias) {
     BackPlan pl{};
-    if (dbias && M <= (dz ? kBackTallRows : kBackTallSums)) {
+    if (dbias && M <= (dz ? kBackTallRows : kBackTallSums) && launchable((N + 63) / 64, kBackTall)) {
         pl.tall = true;
         pl.cl_shift = 3;
         pl.col_blocks = (int)((N + 63) / 64);

@@ -1061,7 +1061,7 @@ static igc_status_t gn_forward(int N, int H, int W, int C, int G, const void* x,
         return IGC_ERR_MISALIGNED;
     const int64_t HW = (int64_t)H * W;
     const GnPlan pl = gn_plan(N, HW, C, G, false);
-    if ((int64_t)N * (pl.slab ? 1 : pl.chunks) * pl.slabs > 0x7fffffff) return IGC_ERR_UNSUPPORTED;
+    if (!launchable((int64_t)N * (pl.slab ? 1 : pl.chunks) * pl.slabs, pl.threads)) return IGC_ERR_UNSUPPORTED;
     Workspace ws;
     if (const igc_status_t st = ws.take(pl.slab ? 0 : pl.bytes, user_ws, user_ws_bytes, stream)) return st;
     (void)hipGetLastError();
@@ -1107,7 +1107,12 @@ static igc_status_t gn_backward(int N, int H, int W, int C, int G, const void* x
     }
     const int64_t HW = (int64_t)H * W;
     const GnPlan pl = gn_plan(N, HW, C, G, true);
-    if ((int64_t)N * (pl.slab ? 1 : pl.chunks) * pl.slabs > 0x7fffffff - (C + 7) / 8) return IGC_ERR_UNSUPPORTED;
+    const unsigned cols = pl.slab || N == 0 ? 32 : 8;  // channels of a workgroup that sums for dgamma and dbeta
+    const unsigned params = dgamma || dbeta ? ((unsigned)C + cols - 1) / cols : 0;
+    const int64_t images = (int64_t)N * (pl.slab ? 1 : pl.chunks) * pl.slabs;  // workgroups over them
+    if (cols == 8 ? !launchable(images + params, pl.threads)
+                  : !launchable(images, pl.threads) || !launchable(params, kGnJoinThreads))
+        return IGC_ERR_UNSUPPORTED;
     Workspace ws;
     if (const igc_status_t st = ws.take(N > 0 ? pl.bytes : 0, user_ws, user_ws_bytes, stream)) return st;
     (void)hipGetLastError();
@@ -1123,8 +1128,6 @@ static igc_status_t gn_backward(int N, int H, int W, int C, int G, const void* x
     a.sums = (float*)((char*)ws.ptr + pl.part_bytes);
     a.dgamma = dgamma;
     a.dbeta = dbeta;
-    const unsigned cols = pl.slab || N == 0 ? 32 : 8;  // channels of a workgroup that sums for dgamma and dbeta
-    const unsigned params = dgamma || dbeta ? ((unsigned)C + cols - 1) / cols : 0;
     if (N > 0 && !pl.slab) {
         hipLaunchKernelGGL(gn_backward_partial_kernel<FP16>, dim3((unsigned)a.grid), dim3(pl.threads), 0, stream, a);
         hipLaunchKernelGGL(gn_backward_apply_kernel<FP16>, dim3((unsigned)a.grid + params), dim3(pl.threads), 0, stream,

@@ -12,6 +12,8 @@ inline bool aligned16(const void* ptr) { return (reinterpret_cast<uintptr_t>(ptr
 inline bool valid_type(igc_out_t t) { return t == IGC_OUT_F32 || t == IGC_OUT_BF16 || t == IGC_OUT_F16; }
 inline int out_size(igc_out_t t) { return t == IGC_OUT_F32 ? 4 : 2; }
 inline int64_t round_up(int64_t v, int64_t m) { return (v + m - 1) / m * m; }
+// A launch has fewer than 2^32 threads.
+inline bool launchable(int64_t blocks, int64_t threads) { return blocks <= 0x7fffffff && blocks * threads < (1ll << 32); }
 
 // igc_lib.hip: the library's pool, and whether a stream is being captured into a graph.
 void* workspace_alloc(size_t bytes, hipStream_t stream);

@@ -410,7 +410,9 @@ int64_t igc_epilogue_backward_workspace_bytes(int64_t M, int64_t N);
  * Requirements: H, W, C, G >= 1, N >= 0 (N == 0 is a no-op), C % G == 0, ldx,
  * ldy >= C, eps >= 0, else IGC_ERR_INVALID_VALUE; C % 8 == 0 and the alignment
  * rule, else IGC_ERR_MISALIGNED; H*W < 2^31 and N*C < 2^30, else
- * IGC_ERR_UNSUPPORTED.  Workspace: igc_group_norm_workspace_bytes.
+ * IGC_ERR_UNSUPPORTED, which is also what a call whose launch would need 2^32
+ * threads returns: none with N < 2^25, N*H*W*C < 2^35 and, with dgamma or dbeta,
+ * C <= 2^28 - 32.  Workspace: igc_group_norm_workspace_bytes.
  */
 igc_status_t group_norm_nhwc_bf16(int N, int H, int W, int C, int G, const void *x, int64_t ldx, const void *gamma,
                                   const void *beta, igc_out_t param_type, float eps, igc_act_t act, void *y,

@@ -660,3 +660,17 @@ def test_pinned_tensors_are_read_and_written():
         p.run(D=D, epilogue=p.epilogue(residual=res))
         synchronize()
         assert torch.equal(D[:M, :72], want[:M, :72].cpu()) and torch.isnan(D[M:].float()).all()
+
+
+def test_epilogue_backward_of_one_very_long_row():
+    """A row so long that a workgroup of 64 columns and 1024 threads for every piece of it would pass 2^32 threads."""
+    N = (1 << 28) + 24
+    d = torch.empty(1, N, dtype=torch.bfloat16, device="cuda").normal_(generator=torch.Generator(device="cuda").manual_seed(1))
+    db = torch.full((N,), float("nan"), device="cuda")
+    say("one long row")
+    igc.check(igc.epilogue_backward_bf16(1, N, "silu", d, N, d, N, None, 0, db, igc.OUT_F32))
+    synchronize()
+    for n0 in range(0, N, 1 << 25):
+        v = d[0, n0:n0 + (1 << 25)].double()
+        want = v * act_grad64(v, "silu")
+        assert_within(db[n0:n0 + (1 << 25)], want, v.abs() * GRAD_ABS + U32 * want.abs(), f"columns from {n0}")

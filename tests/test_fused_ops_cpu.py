@@ -215,3 +215,15 @@ def test_workspace_queries_of_impossible_sizes():
     for f in (igc.epilogue_backward_bf16, igc.epilogue_backward_fp16):
         assert f(*{**BACK_CALL, "N": 1 << 31, "ldd": 1 << 31, "ldp": 1 << 31, "ldz": 1 << 31}.values(), stream=0) == UNSUPPORTED
         assert f(*{**BACK_CALL, "M": 1 << 40}.values(), stream=0) == UNSUPPORTED
+
+
+def test_launches_of_too_many_threads_are_refused():
+    """Nothing is enqueued where one of a call's launches would have 2^32 threads: the sums of dgamma and dbeta would
+    otherwise run after a launch that failed."""
+    many, wide = dict(N=1 << 26, H=1, W=1, C=8, G=1, ldx=8), dict(N=1, H=1, W=1, C=1 << 28, G=1 << 25, ldx=1 << 28)
+    for name in ("group_norm_nhwc_bf16", "group_norm_nhwc_fp16"):
+        assert getattr(igc, name)(*{**NORM_CALL, **many, "ldy": 8}.values(), stream=0) == UNSUPPORTED
+    for name in ("group_norm_nhwc_backward_bf16", "group_norm_nhwc_backward_fp16"):
+        assert getattr(igc, name)(*{**NORM_BACK, **many, "lddy": 8, "lddx": 8}.values(), stream=0) == UNSUPPORTED
+        for N in (0, 1):
+            assert getattr(igc, name)(*{**NORM_BACK, **wide, "N": N, "lddy": 1 << 28, "lddx": 1 << 28}.values(), stream=0) == UNSUPPORTED
