@@ -255,15 +255,16 @@ def lib():
 
 def _ptr(x):
     """A tensor's device address, or an address as it is."""
-    if x is None or type(x) is int:
-        return x
+    if x is None:
+        return None
     try:
-        ptr = x.data_ptr()
+        if x.is_cuda:  # (one attribute, 0.07 us, before the common return)
+            return x.data_ptr()
     except AttributeError:
-        return int(x)
-    if not getattr(x, "is_cuda", True) and _on_host(x):
+        return x.data_ptr() if hasattr(x, "data_ptr") else int(x)
+    if _on_host(x):
         _refuse_host("a tensor")
-    return ptr
+    return x.data_ptr()
 
 
 def _nbytes(x):
