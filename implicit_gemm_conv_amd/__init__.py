@@ -138,14 +138,16 @@ def _matrix(x, code, ld):
     if strides and strides[-1] != 1 and x.shape[-1] > 1:
         raise ValueError("values of a row must lie together")
     if ld is None:
+        if len(strides) > 2 and not x.is_contiguous():
+            raise ValueError("an epilogue's tensor of more than two dimensions is taken as dense, and this one is not")
         ld = strides[0] if len(strides) == 2 else 0
     return ptr, ld, out_code(x.dtype) if code is None else code
 
 
 class Epilogue:
     """A fused epilogue (igc_epilogue_t) from tensors: types come from their dtypes, the leading dimensions of a
-    `residual` and `pre` of two dimensions from their first stride unless given (a convolution's are not looked at),
-    and the tensors are kept alive with it.  A raw device address needs its type (bias_type, residual_type, pre_type:
+    `residual` and `pre` of two dimensions from their first stride unless given, and the tensors are kept alive with it.
+    Those of more dimensions and no given leading dimension, and all of a convolution's, have to be dense (ValueError).  A raw device address needs its type (bias_type, residual_type, pre_type:
     an OUT_ code) and leading dimension.  `raw` holds the packed C structure: calls take it as it is, and refuse one
     whose tensors are in host memory."""
     __slots__ = ("raw", "_keep", "_host")
@@ -372,6 +374,15 @@ def _epi(e):
     return None if e is None else bytes(e)
 
 
+def _conv_epi(e):
+    """The same for a convolution, whose residual and pre are dense NPQK whatever their leading dimensions say."""
+    if isinstance(e, Epilogue):
+        for x in e._keep[1:]:
+            if hasattr(x, "is_contiguous") and not x.is_contiguous():
+                raise ValueError("a convolution's residual and pre have to be dense, and one of them is not")
+    return _epi(e)
+
+
 def _entry(name):
     """The C function, looked up once, at the first call."""
     found = []
@@ -407,13 +418,13 @@ def _conv_epilogue(name):
     def call(N, H, W, C, K, R, S, stride_h, stride_w, pad_h, pad_w, dil_h, dil_w, x, w, y, y_type, epilogue,
              stream=None):
         return plain()(N, H, W, C, K, R, S, stride_h, stride_w, pad_h, pad_w, dil_h, dil_w, _ptr(x), _ptr(w),
-                       _ptr(y), y_type, _epi(epilogue), _stream(stream))
+                       _ptr(y), y_type, _conv_epi(epilogue), _stream(stream))
 
     def call_ex(N, H, W, C, K, R, S, stride_h, stride_w, pad_h, pad_w, dil_h, dil_w, x, w, y, y_type, epilogue,
                 tune=None, workspace=None, workspace_bytes=None, stream=None):
         wsb = workspace_bytes if workspace_bytes is not None else _nbytes(workspace)
         return ex()(N, H, W, C, K, R, S, stride_h, stride_w, pad_h, pad_w, dil_h, dil_w, _ptr(x), _ptr(w),
-                    _ptr(y), y_type, _epi(epilogue), _tune(tune), _ptr(workspace), wsb, _stream(stream))
+                    _ptr(y), y_type, _conv_epi(epilogue), _tune(tune), _ptr(workspace), wsb, _stream(stream))
     call.__name__, call_ex.__name__ = name, name + "_ex"
     return call, call_ex
 

@@ -227,3 +227,23 @@ def test_launches_of_too_many_threads_are_refused():
         assert getattr(igc, name)(*{**NORM_BACK, **many, "lddy": 8, "lddx": 8}.values(), stream=0) == UNSUPPORTED
         for N in (0, 1):
             assert getattr(igc, name)(*{**NORM_BACK, **wide, "N": N, "lddy": 1 << 28, "lddx": 1 << 28}.values(), stream=0) == UNSUPPORTED
+
+
+def test_a_convolution_takes_no_tensor_with_gaps():
+    """A convolution reads and writes its residual and pre as dense NPQK: a slice of a wider tensor is refused, where its
+    strides would be passed over.  A product takes such rows with their leading dimension."""
+    wide = torch.zeros(1, 8, 8, 24, dtype=torch.bfloat16)
+    rows = wide.reshape(64, 24)
+    for name in ("residual", "pre"):
+        for gaps in (wide[..., :16], wide[:, :, ::2], wide[:, 1:7, 1:]):
+            with pytest.raises(ValueError, match="dense"):
+                igc.Epilogue(**{name: gaps})
+        for e in (igc.Epilogue(**{name: rows[:, :16]}), igc.Epilogue(**{name: wide[..., :16]}, ldr=24, ldp=24)):
+            assert (e.c.ldr if name == "residual" else e.c.ldp) == 24
+            for call, more in ((igc.conv2d_nhwc_implicit_gemm_epilogue, ()), (igc.conv2d_nhwc_implicit_gemm_epilogue_fp16_ex, (None,))):
+                with pytest.raises(ValueError, match="dense"):
+                    call(*CONV_CALL.values(), e, *more, stream=0)
+        for dense in (wide, rows, wide[:, :, :, 8:9].contiguous(), wide[:, 2:6]):
+            e = igc.Epilogue(**{name: dense})
+            with pytest.raises(ValueError, match="host memory"):  # past the check above
+                igc.conv2d_nhwc_implicit_gemm_epilogue(*CONV_CALL.values(), e, stream=0)
