@@ -531,7 +531,11 @@ __global__ __launch_bounds__(kGnThreads) void gn_backward_apply_kernel(const GnA
 // whole groups, one kernel reads x once, reduces, and writes y: 4 bytes a value
 // and one launch.  A thread keeps NV vectors; sums of a group go through LDS in
 // a fixed order.  The mean comes first and then the squared deviations from it,
-// from the registers, so the variance needs no shift.
+// from the registers, so the variance needs no shift.  The sum times
+// the rounded reciprocal of the count is corrected by its remainder, so that the
+// mean of a constant group is the constant wherever the sum is exact: with eps =
+// 1e-5 a mean of 1000 that is off by one step moves xh by 0.02.  (A division in
+// each thread instead: 16 of 27 x 27 x 320 13.4 us, 12.8 without.)
 __device__ __forceinline__ void one_at_a_time() { __builtin_amdgcn_sched_barrier(0); }  // one vector unpacked at once
 
 // The packed values are what stays in registers from one phase to the next:
@@ -674,7 +678,7 @@ __global__ __launch_bounds__(kGnMaxThreads) void gn_resident_kernel(const GnArgs
     }
 #pragma unroll
     for (int i = 0; i < W; ++i) gi[i] = s.on ? group_of(a, s.c + i) - s.g0 : 0;
-    const float rn = 1.0f / ((float)a.HW * (float)a.cpg);
+    const float count = (float)a.HW * (float)a.cpg, rn = 1.0f / count;
     float acc[W], mu[W], rs[W];
 #pragma unroll
     for (int i = 0; i < W; ++i) acc[i] = 0.0f;
@@ -690,7 +694,8 @@ __global__ __launch_bounds__(kGnMaxThreads) void gn_resident_kernel(const GnArgs
     keep_packed(x);
 #pragma unroll
     for (int i = 0; i < W; ++i) {
-        mu[i] = sums[gi[i]] * rn;
+        const float sum = sums[gi[i]], m = sum * rn, rest = __builtin_fmaf(-m, count, sum);
+        mu[i] = rest == rest ? __builtin_fmaf(rest, rn, m) : m;  // (an infinite sum has none)
         acc[i] = 0.0f;
     }
 #pragma unroll

@@ -445,3 +445,25 @@ def test_a_group_has_one_result_whichever_slab_it_lies_in(shape):
             synchronize()
             for a, b in zip((y, mean, rstd, dx, dg, db), again + grads):
                 assert torch.equal(a.view(torch.uint8), b.view(torch.uint8)), "two runs differ"
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+def test_a_constant_group_is_its_beta(dtype):
+    """Groups of one value each, in counts that are no powers of two: every sum below is exact in fp32, so the mean is
+    the value, the variance 0 and y the rounded beta, to the last bit, in one launch and in chunks."""
+    for shape in ((2, 7, 9, 40, 1), (1, 13, 1, 8, 1), (3, 7, 7, 24, 8), (2, 14, 14, 320, 32), (16, 27, 27, 320, 32),
+                  (2, 47, 53, 320, 32), (1, 40, 33, 2064, 3)):
+        N, H, W, C, G = shape
+        for value in (1000.0, 3.0, -7.25):
+            say(f"constant {value} {shape} {dtype}")
+            p = Norm(*shape, dtype=dtype, act="none", x=torch.full((N, H, W, C), value))
+            y, mean, rstd = p.forward()
+            p.check_forward(y, mean, rstd, f"constant {value} {shape}")
+            assert (mean == value).all()
+            assert torch.equal(y[..., :C], p.beta.to(p.t).expand(N, H, W, C))
+    p = Norm(2, 14, 14, 320, 32, dtype=dtype)
+    x = p.x.clone()
+    x[0, 3, 4, 5] = float("inf")
+    _, mean, rstd = p.forward(x=x)
+    synchronize()
+    assert mean[0, 0] == float("inf") and torch.isfinite(mean).sum() == mean.numel() - 1
