@@ -38,7 +38,7 @@ EXPORTS = (
     "gemm_bf16_epilogue", "gemm_fp16_epilogue", "gemm_bf16_epilogue_ex", "gemm_fp16_epilogue_ex",
     "conv2d_nhwc_implicit_gemm_epilogue", "conv2d_nhwc_implicit_gemm_epilogue_fp16",
     "conv2d_nhwc_implicit_gemm_epilogue_ex", "conv2d_nhwc_implicit_gemm_epilogue_fp16_ex",
-    "igc_epilogue_workspace_bytes",
+    "igc_epilogue_workspace_bytes", "igc_epilogue_default_tune",
     "epilogue_backward_bf16", "epilogue_backward_fp16", "epilogue_backward_bf16_ex", "epilogue_backward_fp16_ex",
     "igc_epilogue_backward_workspace_bytes",
     "group_norm_nhwc_bf16", "group_norm_nhwc_fp16", "group_norm_nhwc_bf16_ex", "group_norm_nhwc_fp16_ex",
@@ -215,6 +215,7 @@ def lib():
             protos["group_norm_nhwc_backward_" + t] = grad + [p]
             protos["group_norm_nhwc_backward_" + t + "_ex"] = grad + [p, i64, p]
         for name, args, res in (("igc_epilogue_workspace_bytes", [i32, i64, i64, i64, tp], i64),
+                                ("igc_epilogue_default_tune", [i32, i64, i64, i64, i32, i32, tp], i32),
                                 ("igc_epilogue_backward_workspace_bytes", [i64, i64], i64),
                                 ("igc_group_norm_workspace_bytes", [i32] * 5, i64)):
             getattr(L, name).argtypes = args
@@ -496,6 +497,14 @@ group_norm_nhwc_backward_fp16, group_norm_nhwc_backward_fp16_ex = _group_norm_ba
 
 def igc_epilogue_workspace_bytes(op, M, N, K, tune=None):
     return lib().igc_epilogue_workspace_bytes(op, M, N, K, _tune(tune))
+
+
+def igc_epilogue_default_tune(M, N, K, op=OP_GEMM, la=ROW_MAJOR, lb=COL_MAJOR):
+    """The Tune that a call with an epilogue takes; bm = 0 where a product runs on the kernel of few rows."""
+    t = Tune()
+    if not lib().igc_epilogue_default_tune(op, M, N, K, la, lb, ctypes.byref(t)):
+        raise ValueError("bad arguments, or a schedule that is not compiled")
+    return t
 
 
 def igc_epilogue_backward_workspace_bytes(M, N):

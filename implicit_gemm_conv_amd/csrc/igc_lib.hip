@@ -373,6 +373,23 @@ static int64_t few_rows_bytes(const FewRowsPlan& pl, int64_t M, int64_t N) {
     return pl.splits > 1 ? round_up(pl.splits * M * round_up(N, 4) * 4, 256) : 0;
 }
 
+// Whether every kernel that a call with an epilogue may launch on a schedule is compiled, for both input types.
+static bool epilogue_built(const igc_tune_t& t, int op, bool a_kc, bool b_kc) {
+    if (t.stream_k > 0) return false;
+    for (const bool fp16 : {false, true}) {
+        const Instance* inst = find_instance(t, fp16, a_kc, b_kc, op);
+        const EpiInstance* ei = inst ? find_epilogue(*inst) : nullptr;
+        if (!ei) return false;
+        for (const int v : {(int)PLAIN, (int)UNIFORM_TAP, (int)CONV_GENERIC}) {
+            if (op == OP_GEMM && v != PLAIN) continue;
+            const bool plain = inst->fn[v] && (op != OP_GEMM || inst->fn[RAGGED]);
+            const bool whole = ei->fn[0][v] && (op == OP_GEMM ? ei->fn[1][v] != nullptr : plain);  // (plain: loose rows)
+            if (t.k_splits > 1 ? !ei->part[v] && !plain : !whole) return false;
+        }
+    }
+    return true;
+}
+
 static igc_status_t few_rows(bool fp16, int64_t M, int64_t N, int64_t K, const void* A, int64_t lda, const void* B,
                              int64_t ldb, bool b_kc, void* C, int64_t ldc, igc_out_t ct, const Epi& e, void* user_ws,
                              int64_t user_ws_bytes, hipStream_t stream) {
@@ -800,6 +817,23 @@ int64_t igc_epilogue_workspace_bytes(igc_op_t op, int64_t M, int64_t N, int64_t 
             bytes = few > bytes ? few : bytes;
         }
     return bytes;
+}
+
+int igc_epilogue_default_tune(igc_op_t op, int64_t M, int64_t N, int64_t K, igc_layout_t la, igc_layout_t lb,
+                              igc_tune_t* out) {
+    if (!out || M < 0 || N < 0 || K < 0 || (op != IGC_OP_GEMM && op != IGC_OP_CONV_FPROP)) return 0;
+    if (op == IGC_OP_GEMM && ((la != IGC_ROW_MAJOR && la != IGC_COL_MAJOR) || (lb != IGC_ROW_MAJOR && lb != IGC_COL_MAJOR)))
+        return 0;
+    const bool conv = op == IGC_OP_CONV_FPROP, a_kc = conv || la == IGC_ROW_MAJOR, b_kc = conv || lb == IGC_COL_MAJOR;
+    if (!conv && takes_few_rows(M, N, K, round_up(K, 8), a_kc, round_up(b_kc ? K : N, 8), b_kc)) {
+        const FewRowsPlan pl = few_rows_plan(M, N, K, b_kc);
+        *out = igc_tune_t{};
+        out->bn = 16 * pl.nb;
+        out->k_splits = pl.splits;
+        return 1;
+    }
+    *out = epilogue_tune(M, N, K, (int)op, a_kc);
+    return epilogue_built(*out, (int)op, a_kc, b_kc);
 }
 
 int64_t igc_workspace_bytes(igc_op_t op, int64_t M, int64_t N, int64_t K, const igc_tune_t* tune) {

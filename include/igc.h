@@ -368,6 +368,15 @@ igc_status_t conv2d_nhwc_implicit_gemm_epilogue_fp16_ex(int N, int H, int W, int
  * count is not a multiple of 8; otherwise 0; -1 for bad arguments. */
 int64_t igc_epilogue_workspace_bytes(igc_op_t op, int64_t M, int64_t N, int64_t K, const igc_tune_t *tune);
 
+/* The built-in choice of a call with an epilogue (op IGC_OP_GEMM with operand
+ * layouts la and lb, or IGC_OP_CONV_FPROP, which does not look at them) into
+ * *out; returns 1, or 0 for bad arguments or a choice that is not compiled for
+ * both input types.  Where a product of dense operands runs on the kernel of few
+ * rows, which has no tile: bm = 0, bn the columns of a workgroup, k_splits the
+ * parts along K, and 0 elsewhere. */
+int igc_epilogue_default_tune(igc_op_t op, int64_t M, int64_t N, int64_t K, igc_layout_t la, igc_layout_t lb,
+                              igc_tune_t *out);
+
 /*
  * Gradient of the epilogue in one pass, for a dD and a pre of the input type
  * (bf16 or fp16), M x N row-major (a convolution's dense y: M = N*P*Q, N = K):

@@ -247,3 +247,36 @@ def test_a_convolution_takes_no_tensor_with_gaps():
             e = igc.Epilogue(**{name: dense})
             with pytest.raises(ValueError, match="host memory"):  # past the check above
                 igc.conv2d_nhwc_implicit_gemm_epilogue(*CONV_CALL.values(), e, stream=0)
+
+
+def test_the_fused_calls_choice_is_compiled():
+    """The choice of calls with an epilogue, in every operand layout: its kernels are compiled for both types, it never is
+    stream-K, the workspace query has room for its parts, and the sizes below reach every tile that it can name."""
+    seen = set()
+    full = igc.tunes(igc.SCOPE_EPILOGUE | igc.SCOPE_ALL)
+    layouts = [(a, b) for a in (igc.ROW_MAJOR, igc.COL_MAJOR) for b in (igc.ROW_MAJOR, igc.COL_MAJOR)]
+    sizes = [(M, N, K) for M in (1, 8, 9, 20, 21, 33, 65, 100, 200, 256, 1000, 2100, 4096, 100352)
+             for N in (1, 64, 72, 256, 304, 1000, 2100, 8192, 16400, 33000) for K in (0, 8, 72, 520, 1000, 2085, 4096, 8192, 65536)]
+    sizes += [(3000, 3000, 1000), (1536, 4096, 4096), (6000, 800, 800), (100352, 256, 2304), (22176, 304, 160), (12032, 72, 192)]
+    for op in (igc.OP_GEMM, igc.OP_CONV_FPROP):
+        for M, N, K in sizes:
+            for la, lb in layouts if op == igc.OP_GEMM else layouts[:1]:
+                t = igc.igc_epilogue_default_tune(M, N, K, op, la, lb)  # raises where it is not compiled
+                need = igc.igc_epilogue_workspace_bytes(op, M, N, K)
+                if t.k_splits > 1:  # (a ring period is at most 512 of K: fewer parts may be enough)
+                    assert t.k_splits <= 256 and need >= 2 * M * N * 4, (op, M, N, K, la, lb)
+                if t.bm == 0:
+                    assert op == igc.OP_GEMM and la == igc.ROW_MAJOR and M <= 32 and t.bn in (16, 32, 64, 128)
+                else:
+                    assert t.stream_k == 0 and t.astuple() in (full if op == igc.OP_GEMM else igc.tunes(igc.SCOPE_EPILOGUE))
+                seen.add((op, t.bm, t.bn, t.k_splits > 1))
+    G, F = igc.OP_GEMM, igc.OP_CONV_FPROP
+    assert seen >= {(G, 0, 16, False), (G, 0, 16, True), (G, 0, 32, False), (G, 0, 64, False), (G, 0, 128, False),
+                    (G, 64, 64, False), (G, 64, 64, True), (G, 64, 128, False), (G, 64, 128, True), (G, 128, 128, False),
+                    (G, 256, 128, False), (G, 256, 128, True), (G, 256, 256, False), (F, 64, 64, False), (F, 64, 128, False),
+                    (F, 128, 64, False), (F, 256, 64, False), (F, 224, 256, False), (F, 256, 256, False)}, sorted(seen)
+    for bad in ((igc.OP_CONV_WGRAD, 0, 0), (igc.OP_GEMM, 2, 0), (igc.OP_GEMM, 0, -1)):
+        with pytest.raises(ValueError):
+            igc.igc_epilogue_default_tune(64, 64, 64, *bad)
+    with pytest.raises(ValueError):
+        igc.igc_epilogue_default_tune(-1, 64, 64)
