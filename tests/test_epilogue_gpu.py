@@ -674,3 +674,43 @@ def test_epilogue_backward_of_one_very_long_row():
         v = d[0, n0:n0 + (1 << 25)].double()
         want = v * act_grad64(v, "silu")
         assert_within(db[n0:n0 + (1 << 25)], want, v.abs() * GRAD_ABS + U32 * want.abs(), f"columns from {n0}")
+
+
+FEW = [  # M, N, K, layout of B, columns of a workgroup: several turns of K a wave and a partial last one
+    (1, 16411, 1100, "row", 64), (8, 16400, 2085, "row", 64), (8, 32650, 1100, "row", 128), (3, 33003, 2085, "row", 128),
+    (1, 500, 2047, "row", 32), (20, 300, 2045, "row", 32), (7, 700, 1100, "col", 16), (32, 203, 2041, "col", 16),
+    (8, 5000, 4099, "col", 16),
+]
+
+
+@pytest.mark.parametrize("M,N,K,lb,cols", FEW)
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+def test_every_kernel_of_few_rows(M, N, K, lb, cols, dtype):
+    """Each operand width of the kernel of few rows, which the query says it runs on, over a K of several turns."""
+    t = igc.igc_epilogue_default_tune(M, N, K, lb=igc.COL_MAJOR if lb == "col" else igc.ROW_MAJOR)
+    assert (t.bm, t.bn, t.k_splits) == (0, cols, 1)
+    for backward in (False, True):
+        say(f"few rows {M}x{N}x{K} {lb} {dtype} backward {backward}")
+        p = Problem(M, N, K, dtype, lb=lb, act="silu" if backward else "gelu", bias="f32", residual="in", pre="in",
+                    backward=backward, seed=M + K)
+        p.check(p.run(), f"{M}x{N}x{K} {lb} {backward}")
+
+
+@pytest.mark.parametrize("M,N,K", [(1, 40, 9000), (5, 300, 12345), (8, 1000, 6200), (3, 24, 65531)])
+def test_few_rows_in_parts(M, N, K):
+    """Parts along K of the kernel of few rows: column-major weights, at most eight rows and a K of 6144 or more."""
+    assert igc.igc_epilogue_default_tune(M, N, K).bm == 0 and igc.igc_epilogue_default_tune(M, N, K).k_splits > 1
+    for dtype, backward in (("bf16", False), ("fp16", True), ("fp16", False)):
+        say(f"few rows in parts {M}x{N}x{K} {dtype} backward {backward}")
+        p = Problem(M, N, K, dtype, act="gelu_tanh", pre="in", backward=backward, seed=K)
+        ws = torch.empty(igc.igc_epilogue_workspace_bytes(igc.OP_GEMM, M, N, K), dtype=torch.uint8, device="cuda")
+        before = igc.igc_pool_allocations()
+        D = p.run(workspace=ws)
+        p.check(D, f"{M}x{N}x{K} {dtype}")
+        assert igc.igc_pool_allocations() == before
+        own = p.run()
+        synchronize()
+        assert torch.equal(own[:M, :N], D[:M, :N]) and igc.igc_pool_allocations() == before + 1
+        E = torch.full_like(D, float("nan"))
+        E[:M, :N] = p.res
+        p.check(p.run(D=E, workspace=ws, epilogue=p.epilogue(residual=E)), "residual in place")
