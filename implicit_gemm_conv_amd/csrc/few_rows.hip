@@ -15,11 +15,14 @@
 // byte permute per register (two k of one column from two rows), so the MFMA's
 // column index is every NB-th column.
 //
-// Measured (weights from memory, not the caches): 1 x 4096 x 4096 column-major
-// 9.2 us (33.6 MB, 3.6 TB/s), 1 x 16384 x 4096 32.2 and row-major 28.2 (4.8
-// TB/s), 1 x 1024 x 1024 3.7 and 5.5.  What is left at 4096 is a launch, a first
-// load and the join: 2 us beyond the bytes.  A through LDS instead of straight
-// from the caches measured no faster.
+// Measured, calls of one graph one after the other, weights from memory (in
+// brackets: the same weights again, from the last-level cache): 1 x 4096 x 4096
+// column-major 8.8 us (7.2; 33.6 MB, 3.8 TB/s), 1 x 16384 x 4096 32.2 (23.2) and
+// row-major 28.2 (23.0; 4.8 TB/s), 17 x 8192 x 2048 row-major 13.6 (9.3; 2.5 TB/s:
+// two row blocks have operand blocks of 32 columns, 64-byte pieces of a row),
+// 1 x 1024 x 1024 column-major 4.0 (3.0).  What is left at 4096 is a launch, a
+// first load and the join: 2 us beyond the bytes.  A through LDS instead of
+// straight from the caches measured no faster.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
@@ -138,7 +141,7 @@ __global__ __launch_bounds__(64 * WAVES) void few_rows_kernel(const FewRowsArgs 
 #pragma unroll
     for (int i = 0; i < MT; ++i) aoff[i] = (uint32_t)((16 * i + r < a.M ? 16 * i + r : a.M - 1) * a.lda + 8 * g) * 2;
 
-    // element x = thread + 512 t of the workgroup is (x / COLS, x % COLS): what its epilogue reads comes first
+    // element x = thread + 64 WAVES t of the workgroup is (x / COLS, x % COLS): what its epilogue reads comes first
     EpiElement el[EPT];
     if (a.splits == 1) {
 #pragma unroll
@@ -262,7 +265,7 @@ FewRowsPlan few_rows_plan(int64_t M, int64_t N, int64_t K, bool b_kc) {
 template <bool FP16, bool B_KC, int MT, int NB>
 static hipError_t go(const FewRowsArgs& a, const Epi& e, hipStream_t stream) {
     // Eight waves; sixteen for B row-major where 128 registers hold their operands, whose smaller turns spread
-    // better (17 x 8192 x 2048 12.3 -> 11.1 us).  A turn holds 16 to 32 KB of B a workgroup.
+    // better (17 x 8192 x 2048 12.3 -> 11.1 us).  A turn holds 32 KB of B a workgroup (column-major) or 64 KB.
     constexpr int W = !B_KC && NB <= 4 ? 16 : 8;
     constexpr int U = B_KC ? 4 : (W == 16 ? 4 / NB : 8 / NB);
     hipLaunchKernelGGL((few_rows_kernel<FP16, B_KC, MT, NB, W, U>), dim3((unsigned)(a.cols * a.splits)), dim3(64 * W), 0,

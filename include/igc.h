@@ -322,6 +322,11 @@ typedef struct {
  * schedules as gemm_bf16_ex, except that stream-K, and without a K split a
  * configuration without IGC_SCOPE_EPILOGUE, are IGC_ERR_UNSUPPORTED; so is a D,
  * residual or pre of which the rows of one tile span 2^31 bytes or more.
+ * An epilogue of nothing (IGC_ACT_NONE, every pointer NULL) gives the plain product
+ * on these schedules, which is the faster call where gemm_bf16 / gemm_fp16 take
+ * 128 x 128 tiles for a small output (1024 x 1024 x 1024 6.1 us against 9.5) or
+ * 256 x 256 tiles with a column-major A, such as a wide layer's weight gradient
+ * (4096 x 4096 x 8192 219 us against 548).
  * Workspace: igc_epilogue_workspace_bytes. */
 igc_status_t gemm_bf16_epilogue(int64_t M, int64_t N, int64_t K, const void *A, int64_t lda, igc_layout_t la,
                                 const void *B, int64_t ldb, igc_layout_t lb, void *D, int64_t ldd, igc_out_t d_type,
