@@ -44,6 +44,10 @@ EXPORTS = (
     "group_norm_nhwc_bf16", "group_norm_nhwc_fp16", "group_norm_nhwc_bf16_ex", "group_norm_nhwc_fp16_ex",
     "group_norm_nhwc_backward_bf16", "group_norm_nhwc_backward_fp16", "group_norm_nhwc_backward_bf16_ex",
     "group_norm_nhwc_backward_fp16_ex", "igc_group_norm_workspace_bytes",
+    "gemm_int8", "gemm_int8_ex", "igc_gemm_int8_workspace_bytes", "igc_gemm_int8_default_tune",
+    "rms_norm_bf16", "rms_norm_fp16", "rms_norm_int8_bf16", "rms_norm_int8_fp16",
+    "rms_norm_backward_bf16", "rms_norm_backward_fp16", "rms_norm_backward_bf16_ex", "rms_norm_backward_fp16_ex",
+    "igc_rms_norm_backward_workspace_bytes", "quantize_rows_int8_bf16", "quantize_rows_int8_fp16",
     "igc_workspace_bytes", "igc_tune_supported", "igc_default_tune", "igc_tune_count", "igc_tune_get",
     "igc_tune_scope", "igc_tune_lds_bytes", "igc_status_string", "igc_take_device_error", "igc_debug_stream_k",
     "igc_pool_allocations", "igc_ring_schedule", "igc_lds_chunk", "igc_stage_slot",
@@ -214,7 +218,20 @@ def lib():
             grad = [i32] * 5 + [p, i64, p, p, i32, p, p, i32, p, i64, p, i64, p, p]
             protos["group_norm_nhwc_backward_" + t] = grad + [p]
             protos["group_norm_nhwc_backward_" + t + "_ex"] = grad + [p, i64, p]
-        for name, args, res in (("igc_epilogue_workspace_bytes", [i32, i64, i64, i64, tp], i64),
+            rows = [i64, i64, p, i64, p, i64, p, i64, p, i32, f32, p, i64, p, p]
+            protos["rms_norm_" + t] = rows
+            protos["rms_norm_int8_" + t] = rows
+            grad = [i64, i64, p, i64, p, i32, p, p, i64, p, i64, p, i64, p]
+            protos["rms_norm_backward_" + t] = grad + [p]
+            protos["rms_norm_backward_" + t + "_ex"] = grad + [p, i64, p]
+            protos["quantize_rows_int8_" + t] = [i64, i64, i32, p, i64, p, i64, p, i64, p, p]
+        int8 = [i64, i64, i64, p, i64, p, p, i64, p, p, i64, i32, ep]
+        protos["gemm_int8"] = int8 + [p]
+        protos["gemm_int8_ex"] = int8 + [tp, p, i64, p]
+        for name, args, res in (("igc_gemm_int8_workspace_bytes", [i64, i64, i64, tp], i64),
+                                ("igc_gemm_int8_default_tune", [i64, i64, i64, tp], i32),
+                                ("igc_rms_norm_backward_workspace_bytes", [i64, i64], i64),
+                                ("igc_epilogue_workspace_bytes", [i32, i64, i64, i64, tp], i64),
                                 ("igc_epilogue_default_tune", [i32, i64, i64, i64, i32, i32, tp], i32),
                                 ("igc_epilogue_backward_workspace_bytes", [i64, i64], i64),
                                 ("igc_group_norm_workspace_bytes", [i32] * 5, i64)):
@@ -481,6 +498,66 @@ def _group_norm_backward(name):
     return call, call_ex
 
 
+def _rms_norm(name):
+    entry = _entry(name)
+
+    def call(M, C, x, ldx, residual, ldr, h, ldh, gamma, param_type, eps, y, ldy, rstd=None, stream=None):
+        return entry()(M, C, _ptr(x), ldx, _ptr(residual), ldr, _ptr(h), ldh, _ptr(gamma), param_type, eps, _ptr(y), ldy,
+                       _ptr(rstd), _stream(stream))
+    call.__name__ = name
+    return call
+
+
+def _rms_norm_int8(name):
+    entry = _entry(name)
+
+    def call(M, C, x, ldx, residual, ldr, h, ldh, gamma, param_type, eps, q, ldq, scale, stream=None):
+        return entry()(M, C, _ptr(x), ldx, _ptr(residual), ldr, _ptr(h), ldh, _ptr(gamma), param_type, eps, _ptr(q), ldq,
+                       _ptr(scale), _stream(stream))
+    call.__name__ = name
+    return call
+
+
+def _rms_norm_backward(name):
+    plain, ex = _entry(name), _entry(name + "_ex")
+
+    def call(M, C, h, ldh, gamma, param_type, rstd, dy, lddy, dh, lddh, dx, lddx, dgamma=None, stream=None):
+        return plain()(M, C, _ptr(h), ldh, _ptr(gamma), param_type, _ptr(rstd), _ptr(dy), lddy, _ptr(dh), lddh, _ptr(dx),
+                       lddx, _ptr(dgamma), _stream(stream))
+
+    def call_ex(M, C, h, ldh, gamma, param_type, rstd, dy, lddy, dh, lddh, dx, lddx, dgamma=None, workspace=None,
+                workspace_bytes=None, stream=None):
+        wsb = workspace_bytes if workspace_bytes is not None else _nbytes(workspace)
+        return ex()(M, C, _ptr(h), ldh, _ptr(gamma), param_type, _ptr(rstd), _ptr(dy), lddy, _ptr(dh), lddh, _ptr(dx),
+                    lddx, _ptr(dgamma), _ptr(workspace), wsb, _stream(stream))
+    call.__name__, call_ex.__name__ = name, name + "_ex"
+    return call, call_ex
+
+
+def _quantize_rows(name):
+    entry = _entry(name)
+
+    def call(M, C, act, x, ldx, gate, ldg, q, ldq, scale, stream=None):
+        return entry()(M, C, act_code(act), _ptr(x), ldx, _ptr(gate), ldg, _ptr(q), ldq, _ptr(scale), _stream(stream))
+    call.__name__ = name
+    return call
+
+
+_gemm_int8, _gemm_int8_ex = _entry("gemm_int8"), _entry("gemm_int8_ex")
+
+
+def gemm_int8(M, N, K, A, lda, scale_a, B, ldb, scale_b, D, ldd, d_type, epilogue=None, stream=None):
+    return _gemm_int8()(M, N, K, _ptr(A), lda, _ptr(scale_a), _ptr(B), ldb, _ptr(scale_b), _ptr(D), ldd, d_type,
+                        _epi(epilogue), _stream(stream))
+
+
+def gemm_int8_ex(M, N, K, A, lda, scale_a, B, ldb, scale_b, D, ldd, d_type, epilogue=None, tune=None, workspace=None,
+                 workspace_bytes=None, stream=None):
+    wsb = workspace_bytes if workspace_bytes is not None else _nbytes(workspace)
+    return _gemm_int8_ex()(M, N, K, _ptr(A), lda, _ptr(scale_a), _ptr(B), ldb, _ptr(scale_b), _ptr(D), ldd, d_type,
+                           _epi(epilogue), _tune(tune), _ptr(workspace), wsb, _stream(stream))
+
+
 gemm_bf16_epilogue, gemm_bf16_epilogue_ex = _gemm_epilogue("gemm_bf16_epilogue")
 gemm_fp16_epilogue, gemm_fp16_epilogue_ex = _gemm_epilogue("gemm_fp16_epilogue")
 conv2d_nhwc_implicit_gemm_epilogue, conv2d_nhwc_implicit_gemm_epilogue_ex = \
@@ -493,6 +570,29 @@ group_norm_nhwc_bf16, group_norm_nhwc_bf16_ex = _group_norm("group_norm_nhwc_bf1
 group_norm_nhwc_fp16, group_norm_nhwc_fp16_ex = _group_norm("group_norm_nhwc_fp16")
 group_norm_nhwc_backward_bf16, group_norm_nhwc_backward_bf16_ex = _group_norm_backward("group_norm_nhwc_backward_bf16")
 group_norm_nhwc_backward_fp16, group_norm_nhwc_backward_fp16_ex = _group_norm_backward("group_norm_nhwc_backward_fp16")
+
+rms_norm_bf16, rms_norm_fp16 = _rms_norm("rms_norm_bf16"), _rms_norm("rms_norm_fp16")
+rms_norm_int8_bf16, rms_norm_int8_fp16 = _rms_norm_int8("rms_norm_int8_bf16"), _rms_norm_int8("rms_norm_int8_fp16")
+rms_norm_backward_bf16, rms_norm_backward_bf16_ex = _rms_norm_backward("rms_norm_backward_bf16")
+rms_norm_backward_fp16, rms_norm_backward_fp16_ex = _rms_norm_backward("rms_norm_backward_fp16")
+quantize_rows_int8_bf16 = _quantize_rows("quantize_rows_int8_bf16")
+quantize_rows_int8_fp16 = _quantize_rows("quantize_rows_int8_fp16")
+
+
+def igc_gemm_int8_workspace_bytes(M, N, K, tune=None):
+    return lib().igc_gemm_int8_workspace_bytes(M, N, K, _tune(tune))
+
+
+def igc_gemm_int8_default_tune(M, N, K):
+    """The Tune that gemm_int8 takes; bm = 0 where it runs on the kernel of few rows."""
+    t = Tune()
+    if not lib().igc_gemm_int8_default_tune(M, N, K, ctypes.byref(t)):
+        raise ValueError("bad arguments, or a schedule that is not compiled")
+    return t
+
+
+def igc_rms_norm_backward_workspace_bytes(M, C):
+    return lib().igc_rms_norm_backward_workspace_bytes(M, C)
 
 
 def igc_epilogue_workspace_bytes(op, M, N, K, tune=None):

@@ -11,7 +11,9 @@ forward-convolution configurations the study GEMMs and the complete forward
 convolution), and from csrc/epilogue_instances.hip as one object per family for the
 configurations that also have a fused epilogue, all in parallel, then linked with the host-side C ABI
 (csrc/igc_lib.hip, csrc/registry.hip), the split-K reduction (csrc/split_reduce.hip), the product of a few rows
-(csrc/few_rows.hip), the epilogue's gradient (csrc/epilogue_backward.hip) and group norm (csrc/group_norm.hip).
+(csrc/few_rows.hip), the epilogue's gradient (csrc/epilogue_backward.hip), group norm (csrc/group_norm.hip), the
+8-bit integer product (csrc/int8_gemm.hip, and csrc/int8_instances.hip for each configuration with a fused epilogue)
+and the row norms and 8-bit rows (csrc/rms_norm.hip).
 """
 import concurrent.futures
 import os
@@ -84,6 +86,11 @@ def instance_units(configs=None):
                               f"-DIGC_W={w}", f"-DIGC_MI={mi}", f"-DIGC_HALF={h}", f"-DIGC_LW={lw}",
                               f"-DIGC_SYNC={sy}", f"-DIGC_FAMILY={fam}", "-c",
                               os.path.join(CSRC, "epilogue_instances.hip"), "-o", obj])
+            if full:  # and the product of 8-bit integers
+                obj = os.path.join(OBJ_DIR, f"int8_{bm}x{bn}x{bk}x{d}x{w}x{mi}x{h}x{lw}x{sy}.o")
+                units.append([HIPCC, *FLAGS, f"-DIGC_BM={bm}", f"-DIGC_BN={bn}", f"-DIGC_BK={bk}", f"-DIGC_D={d}",
+                              f"-DIGC_W={w}", f"-DIGC_MI={mi}", f"-DIGC_HALF={h}", f"-DIGC_LW={lw}",
+                              f"-DIGC_SYNC={sy}", "-c", os.path.join(CSRC, "int8_instances.hip"), "-o", obj])
     # the epilogue units with every operand layout take longest: first, so that none is left at the end
     units.sort(key=lambda u: "epi_256x256" not in u[-1])
     return units
@@ -95,8 +102,8 @@ def host_unit(name):
 
 def build(jobs=None, verbose=False):
     os.makedirs(OBJ_DIR, exist_ok=True)
-    units = instance_units() + [host_unit(n) for n in ("group_norm", "few_rows", "epilogue_backward", "igc_lib",
-                                                 "registry", "split_reduce", "probes")]
+    units = instance_units() + [host_unit(n) for n in ("group_norm", "few_rows", "epilogue_backward", "rms_norm",
+                                                       "igc_lib", "int8_gemm", "registry", "split_reduce", "probes")]
     # longest first: the instance objects dominate
     jobs = jobs or min(len(units), max(1, (os.cpu_count() or 4)))
     with concurrent.futures.ThreadPoolExecutor(jobs) as ex:

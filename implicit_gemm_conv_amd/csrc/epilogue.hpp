@@ -20,6 +20,17 @@ struct Epi {
     int backward;
 };
 
+// The epilogue after a product of 8-bit integers, whose exact 32-bit sum s gives
+// z = s * sa[m] * sb[n] + bias[n] (the sum's rounding to fp32, at most 2^-24 of
+// it, one for each scale, the last with the bias in a fused multiply-add).
+struct EpiInt8 : Epi {
+    const float* sa;  // M scales, or nullptr (1)
+    const float* sb;  // N scales, or nullptr (1)
+};
+// Whether a configuration's accumulators are integers.
+template <class C>
+constexpr bool kInt8 = std::is_same<typename C::Acc, i32x4_t>::value;
+
 // Eight consecutive values of row storage, element `off` first.  vec: whole
 // 16-byte pieces may be read as long as they hold one value below `left` (how
 // many of the eight lie inside the row); rows are then 16-byte multiples, so
@@ -65,6 +76,16 @@ __device__ __forceinline__ void store8(void* base, int64_t off, int kind, int le
 // Epilogue of one element: what it reads, then the rest.
 struct EpiElement {
     float bias = 0.0f, res = 0.0f, pre = 0.0f;
+    float sa = 1.0f, sb = 1.0f;
+    __device__ __forceinline__ void fetch(const EpiInt8& e, int64_t m, int64_t n) {
+        if (e.sa) sa = e.sa[m];
+        if (e.sb) sb = e.sb[n];
+        fetch(static_cast<const Epi&>(e), m, n);
+    }
+    __device__ __forceinline__ void finish(const EpiInt8& e, void* out, int64_t ldc, int out_kind, int64_t m, int64_t n,
+                                           int sum) const {
+        finish_z(e, out, ldc, out_kind, m, n, __builtin_fmaf((float)sum * sa, sb, bias));
+    }
     __device__ __forceinline__ void fetch(const Epi& e, int64_t m, int64_t n) {
         if (e.bias) bias = load_kind(e.bias, n, e.bias_kind);
         if (e.res) res = load_kind(e.res, m * e.ldr + n, e.res_kind);
@@ -72,7 +93,10 @@ struct EpiElement {
     }
     __device__ __forceinline__ void finish(const Epi& e, void* out, int64_t ldc, int out_kind, int64_t m, int64_t n,
                                            float acc) const {
-        const float z = acc + bias;
+        finish_z(e, out, ldc, out_kind, m, n, acc + bias);
+    }
+    __device__ __forceinline__ void finish_z(const Epi& e, void* out, int64_t ldc, int out_kind, int64_t m, int64_t n,
+                                             float z) const {
         float y = z;
         if (e.backward) {
             if (e.pre)
@@ -196,9 +220,25 @@ struct EpiMatrix {
     }
 };
 
-template <class C, int I0, int NI, bool BWD, class ML>
+// What a lane's eight columns bring: bias and, after a product of integers, scales.
+template <bool INT8>
+struct EpiColumns {
+    float bias[8];
+    float sb[INT8 ? 8 : 1];
+    template <class E>
+    __device__ __forceinline__ void load(const E& e, int64_t N, int64_t n0) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) bias[i] = e.bias && n0 + i < N ? load_kind(e.bias, n0 + i, e.bias_kind) : 0.0f;
+        if constexpr (INT8) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) sb[i] = e.sb && n0 + i < N ? e.sb[n0 + i] : 1.0f;
+        }
+    }
+};
+
+template <class C, int I0, int NI, bool BWD, class ML, class E>
 __device__ __forceinline__ void epi_rows(ML& ml, const typename C::Acc (&acc)[C::FM][C::FN], IGC_LDS char* reg,
-                                         const Params& p, const Epi& e, const float (&bias)[8], int lane) {
+                                         const Params& p, const E& e, const EpiColumns<kInt8<C>>& cv, int lane) {
     constexpr int RB = C::WTN * 4, CPR = RB / 16;
     constexpr int LPR = C::WTN / 8;  // lanes per row
     constexpr int RPI = 64 / LPR;    // rows per group
@@ -210,7 +250,7 @@ __device__ __forceinline__ void epi_rows(ML& ml, const typename C::Acc (&acc)[C:
 #pragma unroll
         for (int j = 0; j < C::FN; ++j) {
             const int row = 16 * i + (lane & 15), c = 4 * j + (lane >> 4);
-            *(IGC_LDS f32x4_t*)(reg + row * RB + ((c ^ (row & (CPR - 1))) << 4)) = acc[I0 + i][j];
+            *(IGC_LDS typename C::Acc*)(reg + row * RB + ((c ^ (row & (CPR - 1))) << 4)) = acc[I0 + i][j];
         }
     const int row0 = lane / LPR, col = (lane % LPR) * 8;
     const int64_t m0 = ml.m0 + ml.wm * C::WTM + 16 * I0, n0 = ml.n0 + ml.wn * C::WTN;
@@ -223,7 +263,17 @@ __device__ __forceinline__ void epi_rows(ML& ml, const typename C::Acc (&acc)[C:
     const bool res_raw = e.res && e.res_kind != KIND_F32;
     const bool pre_raw = BWD && e.pre && e.pre_kind != KIND_F32;
     u32x4s_t rv[UQ], gv[UQ];
+    [[maybe_unused]] float av[UQ];  // the rows' scales
+    [[maybe_unused]] __amdgpu_buffer_rsrc_t sa;
+    if constexpr (kInt8<C>) sa = make_rsrc_u(e.sa ? (const char*)(e.sa + m0) : (const char*)p.C);
     auto fetch = [&](int q) __attribute__((always_inline)) {
+        if constexpr (kInt8<C>) {
+#pragma unroll
+            for (int u = 0; u < UQ; ++u)
+                av[u] = e.sa ? __builtin_bit_cast(float, __builtin_amdgcn_raw_buffer_load_b32(
+                                                             sa, (q + u) * RPI < rows ? (row0 + (q + u) * RPI) * 4 : kOob, 0, 0))
+                             : 1.0f;
+        }
         if (res_raw) {
 #pragma unroll
             for (int u = 0; u < UQ; ++u) rv[u] = res.load(q + u, (q + u) * RPI < rows, 0);
@@ -245,10 +295,18 @@ __device__ __forceinline__ void epi_rows(ML& ml, const typename C::Acc (&acc)[C:
 #pragma unroll
         for (int u = 0; u < UQ; ++u) {
             const int row = (q0 + u) * RPI + row0, c = col / 4, x = row & (CPR - 1);
-            const f32x4_t lo = *(const IGC_LDS f32x4_t*)(reg + row * RB + ((c ^ x) << 4));
-            const f32x4_t hi = *(const IGC_LDS f32x4_t*)(reg + row * RB + (((c + 1) ^ x) << 4));
+            const typename C::Acc lo = *(const IGC_LDS typename C::Acc*)(reg + row * RB + ((c ^ x) << 4));
+            const typename C::Acc hi = *(const IGC_LDS typename C::Acc*)(reg + row * RB + (((c + 1) ^ x) << 4));
+            if constexpr (kInt8<C>) {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) v[u][i] = lo[i] + bias[i], v[u][4 + i] = hi[i] + bias[4 + i];
+                for (int i = 0; i < 4; ++i) {
+                    v[u][i] = __builtin_fmaf((float)lo[i] * av[u], cv.sb[i], cv.bias[i]);
+                    v[u][4 + i] = __builtin_fmaf((float)hi[i] * av[u], cv.sb[4 + i], cv.bias[4 + i]);
+                }
+            } else {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) v[u][i] = lo[i] + cv.bias[i], v[u][4 + i] = hi[i] + cv.bias[4 + i];
+            }
         }
         if constexpr (BWD) {
             if (e.pre) {
@@ -303,13 +361,13 @@ __device__ __forceinline__ void epi_rows(ML& ml, const typename C::Acc (&acc)[C:
 }
 
 // Every pass of a wave's sub-tile, at most four block rows each.
-template <class C, int I0, bool BWD, class ML>
+template <class C, int I0, bool BWD, class ML, class E>
 __device__ __forceinline__ void epi_passes(ML& ml, const typename C::Acc (&acc)[C::FM][C::FN], IGC_LDS char* reg,
-                                           const Params& p, const Epi& e, const float (&bias)[8], int lane) {
+                                           const Params& p, const E& e, const EpiColumns<kInt8<C>>& cv, int lane) {
     if constexpr (I0 < C::FM) {
         constexpr int NI = C::FM - I0 < 4 ? C::FM - I0 : 4;
-        epi_rows<C, I0, NI, BWD>(ml, acc, reg, p, e, bias, lane);
-        epi_passes<C, I0 + NI, BWD>(ml, acc, reg, p, e, bias, lane);
+        epi_rows<C, I0, NI, BWD>(ml, acc, reg, p, e, cv, lane);
+        epi_passes<C, I0 + NI, BWD>(ml, acc, reg, p, e, cv, lane);
     }
 }
 
@@ -318,12 +376,20 @@ __device__ __forceinline__ void epi_passes(ML& ml, const typename C::Acc (&acc)[
 // there and in place of what lies past a row's end.  The loop stays the one for
 // whole chunks; the one that mends straddling chunks in LDS needs registers that
 // 256 x 256 tiles do not have (4096 x 4096 x 1001: 84 us with it, 41 with this).
+// For 8-bit integers p.K counts pairs and the tail is K % 16 bytes of a row.
+__device__ __forceinline__ unsigned low_bytes(int n) {  // mask of a word's first n bytes (none below 1, all from 4)
+    return n >= 4 ? 0xffffffffu : (n <= 0 ? 0u : (1u << (8 * n)) - 1u);
+}
 template <class C, class ML>
 __device__ __forceinline__ void add_k_tail(const Params& p, const ML& ml, typename C::Acc (&acc)[C::FM][C::FN], int lane) {
     auto piece = [&](const void* base, int64_t ld, bool k_contiguous, int64_t row) __attribute__((always_inline)) {
         u32x4s_t w{0, 0, 0, 0};
         if (lane < 16) {  // the lanes of an operand's first eight k
-            if (k_contiguous) {
+            if constexpr (kInt8<C>) {
+                w = raw8(base, row * ld + p.K);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) w[i] &= low_bytes(p.k_ragged8 - 4 * i);
+            } else if (k_contiguous) {
                 w = raw8(base, row * ld + p.K);
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
@@ -355,8 +421,8 @@ __device__ __forceinline__ void add_k_tail(const Params& p, const ML& ml, typena
 
 // The data-parallel kernel of mainloop.hpp with the epilogue above.  (A K
 // split writes fp32 partials and applies the epilogue to their sum.)
-template <class C, int V, bool BWD>
-__global__ __launch_bounds__(C::NT) void gemm_epi_kernel(const Params p, const Epi e) {
+template <class C, int V, bool BWD, class E>
+__device__ __forceinline__ void epi_tile(const Params& p, const E& e) {
     static_assert(variant_applies<C, V>(), "loop variant of another operation");
     static_assert(C::MI == 16 && C::SYNC == 0, "epilogue of the 16x16x32 barrier rings");
     constexpr int PIECE = 4 * 16 * C::WTN * 4;  // a wave's staging area
@@ -364,26 +430,28 @@ __global__ __launch_bounds__(C::NT) void gemm_epi_kernel(const Params p, const E
     const int id = xcd_order((int)blockIdx.x, p.tiles_m * p.tiles_n);
     int tm, tn;
     group_coords(id, p.tiles_m, p.tiles_n, p.group_m, tm, tn);
-    float bias[8];
-    const auto load_bias = [&](int64_t n0) __attribute__((always_inline)) {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) bias[i] = e.bias && n0 + i < p.N ? load_kind(e.bias, n0 + i, e.bias_kind) : 0.0f;
-    };
+    EpiColumns<kInt8<C>> cv;
     // The bias of tiles of up to 128 x 128 waits for nothing if it is asked for before the K loop (1000 x 500 x 250
     // 5.96 and 5.80 us, 1024 x 1024 x 1024 7.53 and 7.38); larger ones have no registers to keep it in.
     constexpr bool EARLY = C::BM * C::BN <= 128 * 128;
     if constexpr (EARLY)
-        load_bias((int64_t)tn * C::BN + (int)(threadIdx.x >> 6) % C::WN * C::WTN + ((int)threadIdx.x & 63) % (C::WTN / 8) * 8);
+        cv.load(e, p.N,
+                (int64_t)tn * C::BN + (int)(threadIdx.x >> 6) % C::WN * C::WTN + ((int)threadIdx.x & 63) % (C::WTN / 8) * 8);
     run_tile<C, V>(p, tm, tn, 0, p.K, [&](auto& ml, auto& acc) __attribute__((always_inline)) {
         // opaque copy of the lane: nothing derived from it is computed before, and kept through, the K loop
         int lane = ml.lane;
         asm volatile("" : "+v"(lane));
-        if constexpr (!EARLY) load_bias(ml.n0 + ml.wn * C::WTN + (lane % (C::WTN / 8)) * 8);
+        if constexpr (!EARLY) cv.load(e, p.N, ml.n0 + ml.wn * C::WTN + (lane % (C::WTN / 8)) * 8);
         if constexpr (C::OPK == OP_GEMM)
             if (p.k_ragged8) add_k_tail<C>(p, ml, acc, lane);
         ring_barrier();  // every wave has finished reading the ring
-        epi_passes<C, 0, BWD>(ml, acc, stage_piece<C, PIECE>(ml.wave), p, e, bias, lane);
+        epi_passes<C, 0, BWD>(ml, acc, stage_piece<C, PIECE>(ml.wave), p, e, cv, lane);
     });
+}
+
+template <class C, int V, bool BWD>
+__global__ __launch_bounds__(C::NT) void gemm_epi_kernel(const Params p, const Epi e) {
+    epi_tile<C, V, BWD>(p, e);
 }
 
 // One split of a K split: the fp32 partial tile to the workspace, staged like
@@ -419,7 +487,7 @@ __global__ __launch_bounds__(C::NT) void gemm_part_kernel(const Params p) {
 #pragma unroll
                 for (int j = 0; j < C::FN; ++j) {
                     const int row = 16 * i + (lane & 15), c = 4 * j + (lane >> 4);
-                    *(IGC_LDS f32x4_t*)(reg + row * RB + ((c ^ (row & (CPR - 1))) << 4)) = acc[I0 + i][j];
+                    *(IGC_LDS typename C::Acc*)(reg + row * RB + ((c ^ (row & (CPR - 1))) << 4)) = acc[I0 + i][j];
                 }
             const int row0 = lane / CPR, c = lane % CPR;
             const int64_t m0 = ml.m0 + ml.wm * C::WTM + 16 * I0, n0 = ml.n0 + ml.wn * C::WTN;

@@ -10,6 +10,7 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include "column_sum.hpp"
 #include "epilogue.hpp"
 #include "host.hpp"
 
@@ -123,6 +124,11 @@ __global__ __launch_bounds__(32 * kSumLanes) void column_sum_kernel(const float*
         store_kind(out, n, kind, s);
     }
 }
+hipError_t launch_column_sum(const float* part, int64_t N, int chunks, void* out, int kind, hipStream_t stream) {
+    hipLaunchKernelGGL(column_sum_kernel, dim3((unsigned)((N + 31) / 32)), dim3(32 * kSumLanes), 0, stream, part, N, chunks,
+                       out, kind);
+    return hipGetLastError();
+}
 
 // Up to this many rows one launch does it all (no partial sums, no workspace).
 // Measured with dz: 777 x 1336 8.8 us, in chunks 7.5; 256 x 1336 5.2 against
@@ -213,11 +219,8 @@ static igc_status_t backward_any(bool fp16, int64_t M, int64_t N, igc_act_t act,
     else
         hipLaunchKernelGGL((epilogue_backward_kernel<false, kBackThreads>), grid, dim3(kBackThreads), 0, stream, a);
     hipError_t e = hipGetLastError();
-    if (e == hipSuccess && dbias && pl.chunks > 1) {
-        hipLaunchKernelGGL(column_sum_kernel, dim3((unsigned)((N + 31) / 32)), dim3(32 * kSumLanes), 0, stream, a.part, N,
-                           pl.chunks, dbias, (int)bias_type);
-        e = hipGetLastError();
-    }
+    if (e == hipSuccess && dbias && pl.chunks > 1)
+        e = launch_column_sum(a.part, N, pl.chunks, dbias, (int)bias_type, stream);
     return e == hipSuccess ? IGC_OK : IGC_ERR_HIP;
 }
 

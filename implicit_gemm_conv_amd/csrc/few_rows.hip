@@ -33,34 +33,44 @@ namespace igc {
 
 typedef __attribute__((ext_vector_type(2))) unsigned u32x2f_t;
 
+// The operands' types.  Those of 8 bits are column-major B alone.
+enum FewRowsIn : int { FEW_BF16 = 0, FEW_FP16 = 1, FEW_INT8 = 2 };
+
 // Of a 16-byte piece of a row starting at element k: the elements below `end`, zeros past it.
+template <int IN>
 __device__ __forceinline__ u32x4s_t keep_below(u32x4s_t w, int64_t k, int64_t end) {
-    const int n = end - k >= 8 ? 8 : (int)(end - k);
+    if constexpr (IN == FEW_INT8) {
+        const int n = end - k >= 16 ? 16 : (int)(end - k);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) w[i] = n >= 2 * i + 2 ? w[i] : (n == 2 * i + 1 ? (w[i] & 0xffffu) : 0u);
+        for (int i = 0; i < 4; ++i) w[i] &= low_bytes(n - 4 * i);
+    } else {
+        const int n = end - k >= 8 ? 8 : (int)(end - k);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) w[i] = n >= 2 * i + 2 ? w[i] : (n == 2 * i + 1 ? (w[i] & 0xffffu) : 0u);
+    }
     return w;
 }
 
-// Eight k of a row, the first of them k: `base` is the row's address of the
+// 16 bytes of a row, the first k of them k: `base` is the row's address of the
 // turn's first k (uniform) and `off` the lane's offset from it, so a load needs
 // one 32-bit register a lane.  MASKED: zeros at and past `end`, where nothing is read.
-template <bool MASKED>
-__device__ __forceinline__ u32x4s_t load_k8(const char* base, uint32_t off, int64_t k, int64_t end) {
+template <int IN, bool MASKED>
+__device__ __forceinline__ u32x4s_t load_k16(const char* base, uint32_t off, int64_t k, int64_t end) {
     if constexpr (MASKED) {
         if (k >= end) return u32x4s_t{0, 0, 0, 0};
-        return keep_below(*(const u32x4s_t*)(base + off), k, end);
+        return keep_below<IN>(*(const u32x4s_t*)(base + off), k, end);
     } else {
         return *(const u32x4s_t*)(base + off);
     }
 }
 
-// One 32-deep step of B for a wave: NB operands of 8 k per lane.  B_KC: NB
-// blocks of 16 columns; else the NB neighbouring columns of one load.
-template <bool B_KC, int NB>
+// One step of B for a wave, the depth of one MFMA: NB operands of 16 bytes per
+// lane.  B_KC: NB blocks of 16 columns; else the NB neighbouring columns of one load.
+template <int IN, bool B_KC, int NB>
 struct BStep {
     unsigned w[4 * NB];
 
-    // `base`: the step's first k in column n0; off[j]: the lane's eight k and its column of block j (B_KC), off[0]:
+    // `base`: the step's first k in column n0; off[j]: the lane's 16 bytes of its column of block j (B_KC), off[0]:
     // its eight k and first column.  k: the lane's first k
     template <bool MASKED>
     __device__ __forceinline__ void load(const char* base, const uint32_t (&off)[B_KC ? NB : 1], int64_t ldb, int64_t k,
@@ -68,7 +78,7 @@ struct BStep {
         if constexpr (B_KC) {
 #pragma unroll
             for (int j = 0; j < NB; ++j) {
-                const u32x4s_t v = load_k8<MASKED>(base, off[j], k, end);
+                const u32x4s_t v = load_k16<IN, MASKED>(base, off[j], k, end);
 #pragma unroll
                 for (int i = 0; i < 4; ++i) w[4 * j + i] = v[i];
             }
@@ -92,7 +102,7 @@ struct BStep {
             }
         }
     }
-    // operand j: the eight k of the lane's column j
+    // operand j: the k of the lane's column j
     __device__ __forceinline__ i16x8_t operand(int j) const {
         u32x4s_t v;
         if constexpr (B_KC) {
@@ -107,15 +117,23 @@ struct BStep {
     }
 };
 
-// MT: 16-row blocks of A; WAVES; U: 32-deep steps a turn.
-template <bool FP16, bool B_KC, int MT, int NB, int WAVES, int U>
-__global__ __launch_bounds__(64 * WAVES) void few_rows_kernel(const FewRowsArgs a, const Epi e) {
-    using Step = BStep<B_KC, NB>;
+template <bool INT8>
+using FewRowsEpi = typename std::conditional<INT8, EpiInt8, Epi>::type;
+
+// MT: 16-row blocks of A; WAVES; U: steps a turn (32 deep, or 64 of 8 bits).
+template <int IN, bool B_KC, int MT, int NB, int WAVES, int U>
+__global__ __launch_bounds__(64 * WAVES) void few_rows_kernel(const FewRowsArgs a, const FewRowsEpi<IN == FEW_INT8> e) {
+    static_assert(B_KC || IN != FEW_INT8, "8-bit operands are column-major");
+    using Step = BStep<IN, B_KC, NB>;
+    using Sum = typename std::conditional<IN == FEW_INT8, int, float>::type;
+    using Acc = typename std::conditional<IN == FEW_INT8, i32x4_t, f32x4_t>::type;
+    constexpr int ESZ = IN == FEW_INT8 ? 1 : 2, EPC = 16 / ESZ;  // bytes of an element, elements of a lane's piece
+    constexpr int SK = 4 * EPC;              // depth of a step
     constexpr int COLS = 16 * NB;            // columns of the workgroup
-    constexpr int UK = 32 * U;
+    constexpr int UK = SK * U;
     constexpr int E = MT * 16 * COLS;        // elements of the workgroup
     constexpr int EPT = (E + 64 * WAVES - 1) / (64 * WAVES);
-    __shared__ __attribute__((aligned(16))) float red[WAVES * E];  // [wave][operand block][lane][4]
+    __shared__ __attribute__((aligned(16))) Sum red[WAVES * E];  // [wave][operand block][lane][4]
 
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int r = lane & 15, g = lane >> 4;
@@ -126,20 +144,20 @@ __global__ __launch_bounds__(64 * WAVES) void few_rows_kernel(const FewRowsArgs 
     const int64_t kend = kbase + a.per < a.K ? kbase + a.per : a.K;
 
     // columns past N and rows past M repeat the last one: their sums are never stored
-    const char* bbase = (const char*)a.B + (B_KC ? n0 * a.ldb : n0) * 2;
-    const int64_t bstep = B_KC ? 2 : a.ldb * 2;  // bytes from one k to the next
+    const char* bbase = (const char*)a.B + (B_KC ? n0 * a.ldb : n0) * ESZ;
+    const int64_t bstep = B_KC ? ESZ : a.ldb * ESZ;  // bytes from one k to the next
     const int left = a.N - n0 < COLS ? (int)(a.N - n0) : COLS;
     uint32_t boff[B_KC ? NB : 1];
     if constexpr (B_KC) {
 #pragma unroll
         for (int j = 0; j < NB; ++j)
-            boff[j] = (uint32_t)((16 * j + r < left ? 16 * j + r : left - 1) * a.ldb + 8 * g) * 2;
+            boff[j] = (uint32_t)((16 * j + r < left ? 16 * j + r : left - 1) * a.ldb + EPC * g) * ESZ;
     } else {
         boff[0] = (uint32_t)(8 * g * a.ldb + (NB * r < left ? NB * r : (left - 1) / NB * NB)) * 2;
     }
     uint32_t aoff[MT];
 #pragma unroll
-    for (int i = 0; i < MT; ++i) aoff[i] = (uint32_t)((16 * i + r < a.M ? 16 * i + r : a.M - 1) * a.lda + 8 * g) * 2;
+    for (int i = 0; i < MT; ++i) aoff[i] = (uint32_t)((16 * i + r < a.M ? 16 * i + r : a.M - 1) * a.lda + EPC * g) * ESZ;
 
     // element x = thread + 64 WAVES t of the workgroup is (x / COLS, x % COLS): what its epilogue reads comes first
     EpiElement el[EPT];
@@ -151,11 +169,11 @@ __global__ __launch_bounds__(64 * WAVES) void few_rows_kernel(const FewRowsArgs 
         }
     }
 
-    f32x4_t acc[MT][NB];
+    Acc acc[MT][NB];
 #pragma unroll
     for (int i = 0; i < MT; ++i)
 #pragma unroll
-        for (int j = 0; j < NB; ++j) acc[i][j] = f32x4_t{0, 0, 0, 0};
+        for (int j = 0; j < NB; ++j) acc[i][j] = Acc{0, 0, 0, 0};
 
     // B of two turns in flight
     Step cur[U], nxt[U];
@@ -164,28 +182,29 @@ __global__ __launch_bounds__(64 * WAVES) void few_rows_kernel(const FewRowsArgs 
         if (k + UK <= kend) {
 #pragma unroll
             for (int u = 0; u < U; ++u)
-                s[u].template load<false>(base + 32 * u * bstep, boff, a.ldb, k + 32 * u + 8 * g, kend);
+                s[u].template load<false>(base + SK * u * bstep, boff, a.ldb, k + SK * u + EPC * g, kend);
         } else if (k < kend) {
 #pragma unroll
             for (int u = 0; u < U; ++u)
-                s[u].template load<true>(base + 32 * u * bstep, boff, a.ldb, k + 32 * u + 8 * g, kend);
+                s[u].template load<true>(base + SK * u * bstep, boff, a.ldb, k + SK * u + EPC * g, kend);
         }
     };
     int64_t k = kbase + (int64_t)wave * UK;
     load_b(cur, k);
     for (; k < kend; k += WAVES * UK) {
         u32x4s_t fa[U][MT];
-        const char* base = (const char*)a.A + k * 2;
+        const char* base = (const char*)a.A + k * ESZ;
         if (k + UK <= kend) {
 #pragma unroll
             for (int u = 0; u < U; ++u)
 #pragma unroll
-                for (int i = 0; i < MT; ++i) fa[u][i] = load_k8<false>(base + 64 * u, aoff[i], 0, 0);
+                for (int i = 0; i < MT; ++i) fa[u][i] = load_k16<IN, false>(base + 64 * u, aoff[i], 0, 0);
         } else {
 #pragma unroll
             for (int u = 0; u < U; ++u)
 #pragma unroll
-                for (int i = 0; i < MT; ++i) fa[u][i] = load_k8<true>(base + 64 * u, aoff[i], k + 32 * u + 8 * g, kend);
+                for (int i = 0; i < MT; ++i)
+                    fa[u][i] = load_k16<IN, true>(base + 64 * u, aoff[i], k + SK * u + EPC * g, kend);
         }
         load_b(nxt, k + WAVES * UK);
 #pragma unroll
@@ -195,7 +214,7 @@ __global__ __launch_bounds__(64 * WAVES) void few_rows_kernel(const FewRowsArgs 
                 const i16x8_t fb = cur[u].operand(j);
 #pragma unroll
                 for (int i = 0; i < MT; ++i)
-                    acc[i][j] = mfma<FP16>(fb, __builtin_bit_cast(i16x8_t, fa[u][i]), acc[i][j]);
+                    acc[i][j] = mfma<IN == FEW_FP16>(fb, __builtin_bit_cast(i16x8_t, fa[u][i]), acc[i][j]);
             }
 #pragma unroll
         for (int u = 0; u < U; ++u) cur[u] = nxt[u];
@@ -204,7 +223,7 @@ __global__ __launch_bounds__(64 * WAVES) void few_rows_kernel(const FewRowsArgs 
 #pragma unroll
     for (int i = 0; i < MT; ++i)
 #pragma unroll
-        for (int j = 0; j < NB; ++j) *(f32x4_t*)&red[((wave * MT + i) * NB + j) * 256 + lane * 4] = acc[i][j];
+        for (int j = 0; j < NB; ++j) *(Acc*)&red[((wave * MT + i) * NB + j) * 256 + lane * 4] = acc[i][j];
     __syncthreads();
     // element (m, c) of the workgroup: block (m/16, j), lane 16*(q/4) + m%16, word q%4, where column c is number q of
     // operand j: c = 16*j + q (B_KC) or NB*q + j
@@ -214,12 +233,12 @@ __global__ __launch_bounds__(64 * WAVES) void few_rows_kernel(const FewRowsArgs 
         const int m = x / COLS, c = x % COLS;
         if (m >= a.M || c >= left || x >= E) continue;
         const int j = B_KC ? c / 16 : c % NB, q = B_KC ? c % 16 : c / NB;
-        const float* src = &red[((m >> 4) * NB + j) * 256 + ((q >> 2) * 16 + (m & 15)) * 4 + (q & 3)];
-        float s = src[0];
+        const Sum* src = &red[((m >> 4) * NB + j) * 256 + ((q >> 2) * 16 + (m & 15)) * 4 + (q & 3)];
+        Sum s = src[0];
 #pragma unroll
         for (int w = 1; w < WAVES; ++w) s += src[w * E];
         if (a.splits > 1)
-            a.ws[((int64_t)split * a.M + m) * a.ldws + n0 + c] = s;
+            ((Sum*)a.ws)[((int64_t)split * a.M + m) * a.ldws + n0 + c] = s;
         else
             el[t].finish(e, a.C, a.ldc, a.out_kind, m, n0 + c, s);
     }
@@ -262,31 +281,43 @@ FewRowsPlan few_rows_plan(int64_t M, int64_t N, int64_t K, bool b_kc) {
     return pl;
 }
 
-template <bool FP16, bool B_KC, int MT, int NB>
-static hipError_t go(const FewRowsArgs& a, const Epi& e, hipStream_t stream) {
+// 8-bit operands: the bytes of a bf16 product of half the K.
+bool few_rows_int8_faster(int64_t M, int64_t N, int64_t K) { return few_rows_faster(M, N, (K + 1) / 2, true); }
+FewRowsPlan few_rows_int8_plan(int64_t M, int64_t N, int64_t K) {
+    FewRowsPlan pl = few_rows_plan(M, N, (K + 1) / 2, true);
+    pl.per *= 2;  // (splits of K stay: per was rounded up to 128 of 16 bits)
+    return pl;
+}
+
+template <int IN, bool B_KC, int MT, int NB>
+static hipError_t go(const FewRowsArgs& a, const FewRowsEpi<IN == FEW_INT8>& e, hipStream_t stream) {
     // Eight waves; sixteen for B row-major where 128 registers hold their operands, whose smaller turns spread
     // better (17 x 8192 x 2048 12.3 -> 11.1 us).  A turn holds 32 KB of B a workgroup (column-major) or 64 KB.
     constexpr int W = !B_KC && NB <= 4 ? 16 : 8;
     constexpr int U = B_KC ? 4 : (W == 16 ? 4 / NB : 8 / NB);
-    hipLaunchKernelGGL((few_rows_kernel<FP16, B_KC, MT, NB, W, U>), dim3((unsigned)(a.cols * a.splits)), dim3(64 * W), 0,
+    hipLaunchKernelGGL((few_rows_kernel<IN, B_KC, MT, NB, W, U>), dim3((unsigned)(a.cols * a.splits)), dim3(64 * W), 0,
                        stream, a, e);
     return hipGetLastError();
 }
 
-template <bool FP16, bool B_KC>
-static hipError_t pick_few(const FewRowsArgs& a, const Epi& e, int nb, hipStream_t st) {
+template <int IN, bool B_KC>
+static hipError_t pick_few(const FewRowsArgs& a, const FewRowsEpi<IN == FEW_INT8>& e, int nb, hipStream_t st) {
     if constexpr (B_KC) {
-        return a.M <= 16 ? go<FP16, true, 1, 1>(a, e, st) : go<FP16, true, 2, 1>(a, e, st);
+        return a.M <= 16 ? go<IN, true, 1, 1>(a, e, st) : go<IN, true, 2, 1>(a, e, st);
     } else {
-        if (a.M > 16) return go<FP16, false, 2, 2>(a, e, st);
-        if (nb == 8) return go<FP16, false, 1, 8>(a, e, st);
-        return nb == 4 ? go<FP16, false, 1, 4>(a, e, st) : go<FP16, false, 1, 2>(a, e, st);
+        if (a.M > 16) return go<IN, false, 2, 2>(a, e, st);
+        if (nb == 8) return go<IN, false, 1, 8>(a, e, st);
+        return nb == 4 ? go<IN, false, 1, 4>(a, e, st) : go<IN, false, 1, 2>(a, e, st);
     }
 }
 
 hipError_t launch_few_rows(const FewRowsArgs& a, const Epi& e, bool fp16, bool b_kc, int nb, hipStream_t stream) {
-    if (fp16) return b_kc ? pick_few<true, true>(a, e, nb, stream) : pick_few<true, false>(a, e, nb, stream);
-    return b_kc ? pick_few<false, true>(a, e, nb, stream) : pick_few<false, false>(a, e, nb, stream);
+    if (fp16) return b_kc ? pick_few<FEW_FP16, true>(a, e, nb, stream) : pick_few<FEW_FP16, false>(a, e, nb, stream);
+    return b_kc ? pick_few<FEW_BF16, true>(a, e, nb, stream) : pick_few<FEW_BF16, false>(a, e, nb, stream);
+}
+
+hipError_t launch_few_rows_int8(const FewRowsArgs& a, const EpiInt8& e, hipStream_t stream) {
+    return pick_few<FEW_INT8, true>(a, e, 1, stream);
 }
 
 }  // namespace igc

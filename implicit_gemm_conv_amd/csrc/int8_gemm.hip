@@ -1,0 +1,248 @@
+// int8_gemm.hip -- C ABI of the 8-bit integer product: argument checks, choice
+// of kernel and launch.  The kernels are in int8_instances.hip (tiles) and
+// few_rows.hip (up to 32 rows).
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "epilogue.hpp"
+#include "few_rows.hpp"
+#include "host.hpp"
+#include "igc.h"
+#include "int8_gemm.hpp"
+#include "ring.hpp"
+#include "split_reduce.hpp"
+
+namespace igc {
+
+constexpr int kMaxInt8 = 16;
+static Int8Instance g_int8[kMaxInt8];
+static int g_nint8 = 0;
+
+void register_int8(const Int8Instance& instance) {
+    if (g_nint8 < kMaxInt8) g_int8[g_nint8++] = instance;
+}
+
+static const Int8Instance* find_int8(const igc_tune_t& q) {
+    const int loaders = q.loader_waves == 0 ? q.waves : q.loader_waves;
+    for (int i = 0; i < g_nint8; ++i) {
+        const Instance& e = g_int8[i].tile;
+        if (e.bm == q.bm && e.bn == q.bn && e.bk == q.bk && e.d == q.pipe_depth && e.waves == q.waves &&
+            e.mfma == (q.mfma == 0 ? 32 : q.mfma) && e.half == q.half_stage && e.loaders == loaders &&
+            e.sync == q.ring_sync)
+            return &g_int8[i];
+    }
+    return nullptr;
+}
+
+// |A[m][k] B[n][k]| <= 2^14: a sum of fewer than 2^17 of them stays inside 32 bits.
+constexpr int64_t kMaxK = (1ll << 17) - 1;
+
+struct Int8Plan {
+    igc_tune_t tune = {};
+    const Int8Instance* inst = nullptr;
+    bool valid = true, few = false;
+    FewRowsPlan rows = {};
+    int S = 1;                // K parts
+    int64_t per = 0;          // pairs of K a part
+    int64_t ldws = 0, bytes = 0;
+};
+
+static Int8Plan plan_of(const igc_tune_t* tune, int64_t M, int64_t N, int64_t K) {
+    Int8Plan pl;
+    const int64_t pairs = K / 16 * 8;  // what the K loop runs to; the last K % 16 are added after it
+    if (!tune && M >= 1 && M <= kFewRows && few_rows_int8_faster(M, N, K)) {
+        pl.few = true;
+        pl.rows = few_rows_int8_plan(M, N, K);
+        pl.ldws = round_up(N, 4);
+        pl.bytes = pl.rows.splits > 1 ? round_up(pl.rows.splits * M * pl.ldws * 4, 256) : 0;
+        return pl;
+    }
+    pl.tune = tune ? *tune : epilogue_tune(M, N, (K + 1) / 2, IGC_OP_GEMM, true);
+    pl.inst = find_int8(pl.tune);
+    pl.valid = pl.tune.stream_k >= 0 && pl.tune.sk_hybrid == 0 && !(pl.tune.k_splits > 1 && pl.tune.stream_k > 0);
+    if (!pl.inst || pl.tune.k_splits <= 1 || pairs == 0) return pl;
+    // each part a whole number of ring periods
+    const Instance& t = pl.inst->tile;
+    const int64_t unit = (int64_t)t.bk * Ring::period(Ring::units(t.d, t.half));
+    pl.per = round_up((pairs + pl.tune.k_splits - 1) / pl.tune.k_splits, unit);
+    pl.S = (int)((pairs + pl.per - 1) / pl.per);
+    if (pl.S > 1) {
+        pl.ldws = round_up(N, 4);
+        pl.bytes = round_up((int64_t)pl.S * M * pl.ldws * 4, 256);
+    }
+    return pl;
+}
+
+static igc_status_t check_epilogue(const igc_epilogue_t* q, int64_t N, EpiInt8& e) {
+    e = EpiInt8{};
+    if (!q) return IGC_OK;
+    if ((int)q->act < IGC_ACT_NONE || (int)q->act > IGC_ACT_SILU || (q->backward != 0 && q->backward != 1))
+        return IGC_ERR_INVALID_VALUE;
+    if (q->backward) return IGC_ERR_UNSUPPORTED;
+    e.act = (int)q->act;
+    if (q->bias) {
+        if (!valid_type(q->bias_type)) return IGC_ERR_INVALID_VALUE;
+        if (reinterpret_cast<uintptr_t>(q->bias) % out_size(q->bias_type)) return IGC_ERR_MISALIGNED;
+        e.bias = q->bias;
+        e.bias_kind = (int)q->bias_type;
+    }
+    const auto matrix = [&](const void* ptr, int64_t ld, igc_out_t type) {
+        if (!valid_type(type) || ld < N) return IGC_ERR_INVALID_VALUE;
+        return !aligned16(ptr) || ld * out_size(type) % 16 != 0 ? IGC_ERR_MISALIGNED : IGC_OK;
+    };
+    if (q->residual) {
+        if (const igc_status_t st = matrix(q->residual, q->ldr, q->residual_type)) return st;
+        e.res = q->residual;
+        e.ldr = q->ldr;
+        e.res_kind = (int)q->residual_type;
+    }
+    if (q->pre) {
+        if (const igc_status_t st = matrix(q->pre, q->ldp, q->pre_type)) return st;
+        e.pre = q->pre;
+        e.ldp = q->ldp;
+        e.pre_kind = (int)q->pre_type;
+    }
+    return IGC_OK;
+}
+
+static igc_status_t int8_any(int64_t M, int64_t N, int64_t K, const int8_t* A, int64_t lda, const float* sa,
+                             const int8_t* B, int64_t ldb, const float* sb, void* D, int64_t ldd, igc_out_t dt,
+                             const igc_epilogue_t* epi, const igc_tune_t* tune, void* user_ws, int64_t user_ws_bytes,
+                             hipStream_t stream) {
+    if (M < 0 || N < 0 || K < 0 || !valid_type(dt)) return IGC_ERR_INVALID_VALUE;
+    EpiInt8 e;
+    if (const igc_status_t st = check_epilogue(epi, N, e)) return st;
+    e.sa = sa;
+    e.sb = sb;
+    if (K > kMaxK || M >= (1ll << 40) || N >= (1ll << 40)) return IGC_ERR_UNSUPPORTED;
+    const Int8Plan pl = plan_of(tune, M, N, K);
+    if (!pl.valid) return IGC_ERR_INVALID_VALUE;
+    if (!pl.few && (!pl.inst || pl.tune.stream_k > 0)) return IGC_ERR_UNSUPPORTED;
+    if (M == 0 || N == 0) return IGC_OK;
+    if (!D || ldd < N) return IGC_ERR_INVALID_VALUE;
+    if (K > 0) {
+        if (!A || !B || lda < K || ldb < K) return IGC_ERR_INVALID_VALUE;
+        if (!aligned16(A) || !aligned16(B) || lda % 16 != 0 || ldb % 16 != 0) return IGC_ERR_MISALIGNED;
+    }
+    if (!aligned16(D) || ldd * out_size(dt) % 16 != 0 || (reinterpret_cast<uintptr_t>(sa) & 3u) ||
+        (reinterpret_cast<uintptr_t>(sb) & 3u))
+        return IGC_ERR_MISALIGNED;
+
+    // per-tile buffer offsets are 32-bit: one tile's rows span less than 2^31 bytes
+    constexpr int64_t kSpan = 0x7fff0000ll;
+    if (lda > kSpan || ldb > kSpan || ldd > kSpan || e.ldr > kSpan || e.ldp > kSpan) return IGC_ERR_UNSUPPORTED;
+    if (pl.few) {
+        if (M * lda >= kSpan || 64 * ldb + 256 >= kSpan || N >= (1ll << 30) ||
+            !launchable(pl.rows.cols * pl.rows.splits, 512))
+            return IGC_ERR_UNSUPPORTED;
+        Workspace ws;
+        if (const igc_status_t st = ws.take(pl.bytes, user_ws, user_ws_bytes, stream)) return st;
+        (void)hipGetLastError();
+        FewRowsArgs a{};
+        a.A = A;
+        a.B = B;
+        a.C = D;
+        a.ws = (float*)ws.ptr;
+        a.N = N;
+        a.K = K;
+        a.lda = lda;
+        a.ldb = ldb;
+        a.ldc = ldd;
+        a.ldws = pl.ldws;
+        a.per = pl.rows.per;
+        a.M = (int)M;
+        a.cols = (int)pl.rows.cols;
+        a.splits = pl.rows.splits;
+        a.out_kind = (int)dt;
+        hipError_t err = launch_few_rows_int8(a, e, stream);
+        if (err == hipSuccess && pl.rows.splits > 1)
+            err = launch_split_epilogue((const int*)a.ws, pl.rows.splits, M * a.ldws, M, N, a.ldws, D, ldd, (int)dt, e,
+                                        stream);
+        return err == hipSuccess ? IGC_OK : IGC_ERR_HIP;
+    }
+
+    const Instance& t = pl.inst->tile;
+    const int64_t tiles_m = (M + t.bm - 1) / t.bm, tiles_n = (N + t.bn - 1) / t.bn;
+    const auto span = [&](int64_t ld, int kind) { return t.bm * ld * (kind == OUT_F32 ? 4 : 2) >= kSpan; };
+    const bool split = pl.S > 1;
+    if (t.bm * lda + 2 * t.bk >= kSpan || t.bn * ldb + 2 * t.bk >= kSpan || tiles_m * tiles_n > 0x7fffffff ||
+        !launchable(tiles_m * tiles_n * pl.S, 64 * t.waves) || (split && t.bm * pl.ldws * 4 >= kSpan) ||
+        (split && !launchable((M * ((N + 7) / 8) + 255) / 256, 256)) ||
+        (!split && (span(ldd, (int)dt) || (e.res && span(e.ldr, e.res_kind)) || (e.pre && span(e.ldp, e.pre_kind)))))
+        return IGC_ERR_UNSUPPORTED;
+    const void* fn = split ? pl.inst->part : pl.inst->fn;
+    if (!fn) return IGC_ERR_UNSUPPORTED;
+    Workspace ws;
+    if (const igc_status_t st = ws.take(pl.bytes, user_ws, user_ws_bytes, stream)) return st;
+    (void)hipGetLastError();  // launch errors below are ours alone
+    Params p = {};
+    p.A = A;
+    p.B = B;
+    p.C = D;
+    p.M = M;
+    p.N = N;
+    p.K = K / 16 * 8;
+    p.lda = lda / 2;
+    p.ldb = ldb / 2;
+    p.ldc = ldd;
+    p.tiles_m = (int)tiles_m;
+    p.tiles_n = (int)tiles_n;
+    p.out_kind = (int)dt;
+    p.group_m = 8;
+    p.k_ragged8 = (int)(K % 16);
+    p.vec_ok = 1;
+    p.k_splits = pl.S;
+    p.k_per_split = split ? pl.per : (p.K > 0 ? p.K : 1);
+    p.ws = (float*)ws.ptr;
+    p.ldws = pl.ldws;
+    p.ws_stride = M * pl.ldws;
+    void* args[] = {&p, &e};  // (the kernel of a part takes the first alone)
+    hipError_t err = hipLaunchKernel(fn, dim3((unsigned)(tiles_m * tiles_n * pl.S)), dim3(64 * t.waves), args, 0, stream);
+    if (err == hipSuccess && split)
+        err = launch_split_epilogue((const int*)p.ws, pl.S, p.ws_stride, M, N, p.ldws, D, ldd, (int)dt, e, stream);
+    if (err != hipSuccess) return IGC_ERR_HIP;
+    return hipGetLastError() == hipSuccess ? IGC_OK : IGC_ERR_HIP;
+}
+
+}  // namespace igc
+
+using namespace igc;
+
+extern "C" {
+
+igc_status_t gemm_int8(int64_t M, int64_t N, int64_t K, const int8_t* A, int64_t lda, const float* scale_a,
+                       const int8_t* B, int64_t ldb, const float* scale_b, void* D, int64_t ldd, igc_out_t d_type,
+                       const igc_epilogue_t* epilogue, igc_stream_t stream) {
+    return int8_any(M, N, K, A, lda, scale_a, B, ldb, scale_b, D, ldd, d_type, epilogue, nullptr, nullptr, 0,
+                    (hipStream_t)stream);
+}
+
+igc_status_t gemm_int8_ex(int64_t M, int64_t N, int64_t K, const int8_t* A, int64_t lda, const float* scale_a,
+                          const int8_t* B, int64_t ldb, const float* scale_b, void* D, int64_t ldd, igc_out_t d_type,
+                          const igc_epilogue_t* epilogue, const igc_tune_t* tune, void* workspace,
+                          int64_t workspace_bytes, igc_stream_t stream) {
+    return int8_any(M, N, K, A, lda, scale_a, B, ldb, scale_b, D, ldd, d_type, epilogue, tune, workspace,
+                    workspace_bytes, (hipStream_t)stream);
+}
+
+int64_t igc_gemm_int8_workspace_bytes(int64_t M, int64_t N, int64_t K, const igc_tune_t* tune) {
+    if (M < 0 || N < 0 || K < 0 || K > kMaxK || M >= (1ll << 40) || N >= (1ll << 40)) return -1;
+    const Int8Plan pl = plan_of(tune, M, N, K);
+    if (!pl.valid || (!pl.few && (!pl.inst || pl.tune.stream_k > 0))) return -1;
+    return M == 0 || N == 0 ? 0 : pl.bytes;
+}
+
+int igc_gemm_int8_default_tune(int64_t M, int64_t N, int64_t K, igc_tune_t* out) {
+    if (!out || M < 0 || N < 0 || K < 0 || K > kMaxK || M >= (1ll << 40) || N >= (1ll << 40)) return 0;
+    const Int8Plan pl = plan_of(nullptr, M, N, K);
+    if (pl.few) {
+        *out = igc_tune_t{};
+        out->bn = 16 * pl.rows.nb;
+        out->k_splits = pl.rows.splits;
+        return 1;
+    }
+    *out = pl.tune;
+    return pl.inst && pl.tune.stream_k == 0 && (pl.S > 1 ? pl.inst->part : pl.inst->fn) ? 1 : 0;
+}
+
+}  // extern "C"

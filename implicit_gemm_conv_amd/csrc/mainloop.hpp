@@ -53,6 +53,7 @@ typedef __attribute__((ext_vector_type(8))) __bf16 bf16x8_t;
 typedef __attribute__((ext_vector_type(8))) _Float16 f16x8_t;
 typedef __attribute__((ext_vector_type(16))) float f32x16_t;
 typedef __attribute__((ext_vector_type(4))) float f32x4_t;
+typedef __attribute__((ext_vector_type(4))) int i32x4_t;
 typedef __attribute__((ext_vector_type(4))) short i16x4_t;
 typedef __attribute__((ext_vector_type(8))) short i16x8_t;
 typedef __attribute__((ext_vector_type(2))) unsigned u32x2_t;
@@ -243,6 +244,15 @@ __device__ __forceinline__ f32x4_t mfma(i16x8_t a, i16x8_t b, f32x4_t c) {
         return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, a),
                                                        __builtin_bit_cast(bf16x8_t, b), c, 0, 0, 0);
     }
+}
+// MFMA 16x16x64 on 8-bit integers, 32-bit integer accumulate.  Its operands lie
+// in the registers as the 16x16x32's do, 16 bytes of a row a lane, so an 8-bit
+// operand whose K lies together moves through the mainloop as a 16-bit one of
+// half its K (pairs of values).
+template <bool>
+__device__ __forceinline__ i32x4_t mfma(i16x8_t a, i16x8_t b, i32x4_t c) {
+    return __builtin_amdgcn_mfma_i32_16x16x64_i8(__builtin_bit_cast(i32x4_t, a), __builtin_bit_cast(i32x4_t, b), c, 0, 0,
+                                                 0);
 }
 
 // ---------------------------------------------------------------------------
@@ -834,7 +844,6 @@ struct Mainloop {
     // and (once every wave is there) raises the flag to 1.  `raise` false is
     // the test hook that leaves one flag down.
     __device__ __forceinline__ void sk_publish(const Acc (&acc)[FM][FN], float* part, int* flag, bool raise) {
-        typedef __attribute__((ext_vector_type(4))) int i32x4_t;
         const __amdgpu_buffer_rsrc_t rs = make_rsrc(part);
 #pragma unroll
         for (int i = 0; i < FM; ++i)

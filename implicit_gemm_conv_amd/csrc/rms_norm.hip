@@ -1,0 +1,769 @@
+// rms_norm.hip -- rows: the root-mean-square norm with the residual's addition,
+// to 16 bits or to 8 bits with a scale a row, its gradient, and the rounding of
+// an activation's rows to 8 bits.
+//
+//   norm      h = x + residual (rounded to its type, as it is kept)
+//             rstd = 1 / sqrt(mean(h^2) + eps),  y = h rstd gamma
+//   8 bits    scale = max |v| / 127,  q = nearest(v / scale), v a row's values.
+//             In the norm rstd is common to a row and cancels in q, so one
+//             reduction, of sum h^2 and max |h gamma|, does for both.
+//   gradient  g = dy gamma, xh = h rstd:  dx = rstd (g - xh mean(g xh)) + dh,
+//             dgamma = sum over the rows of dy xh
+//   rows      v = act(x) gate, to 8 bits
+//
+// Memory bounds all of them: every value is read once and written once.  T
+// threads hold a row in registers, V vectors of eight values (16 bytes) each,
+// between the reduction and the output; a workgroup holds several rows where
+// they are short.  Rows of more than 8 * 1024 * 4 values are read twice.  All
+// sums are fp32 and taken in a fixed order.
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include <initializer_list>
+
+#include "column_sum.hpp"
+#include "epilogue.hpp"
+#include "host.hpp"
+#include "igc.h"
+
+namespace igc {
+
+typedef __attribute__((ext_vector_type(2))) unsigned u32x2n_t;
+
+struct RowArgs {
+    const void* x;      // rows read: x, or h of the backward pass
+    const void* res;    // norm: residual; rows to 8 bits: gate; backward: dh
+    const void* dy;
+    const void* gamma;
+    void* h;
+    void* y;            // norm: y; backward: dx
+    int8_t* q;
+    float* scale;
+    float* rstd;        // written by the norm, read by the backward pass
+    void* dgamma;
+    float* part;        // backward: the workgroups' sums for dgamma, C each
+    int64_t M, ldx, ldr, lddy, ldh, ldy, ldq;
+    int C;
+    float eps;
+    int param_kind, param_vec, act;
+};
+
+// 16 bytes of a row from column c: zeros where the row has ended.  A piece with one value inside is read whole (rows
+// are 16-byte multiples) and what lies past the end is cleared.
+__device__ __forceinline__ u32x4s_t load_piece(const void* base, int64_t off, int left) {
+    u32x4s_t w{0, 0, 0, 0};
+    if (left > 0) w = raw8(base, off);
+    if (left < 8) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) w[i] &= left >= 2 * i + 2 ? 0xffffffffu : (left == 2 * i + 1 ? 0xffffu : 0u);
+    }
+    return w;
+}
+template <bool F16>
+__device__ __forceinline__ void store_piece(void* base, int64_t off, int left, const float (&v)[8]) {
+    if (left > 0) store8(base, off, F16 ? KIND_F16 : KIND_BF16, left, true, v);
+}
+
+template <bool F16>
+__device__ __forceinline__ u32x4s_t add_rounded(u32x4s_t a, u32x4s_t b) {
+    float x[8], y[8];
+    unpack8<F16>(a, x);
+    unpack8<F16>(b, y);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) x[i] += y[i];
+    return pack8<F16>(x);
+}
+
+// gamma of eight columns (zeros past the row's end).
+__device__ __forceinline__ void load_gamma(const RowArgs& a, int c, int left, float (&g)[8]) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) g[i] = a.gamma ? 0.0f : 1.0f;
+    if (a.gamma && left > 0) {
+        load8(a.gamma, c, a.param_kind, left, a.param_vec != 0, g);
+        if (left < 8) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) g[i] = i < left ? g[i] : 0.0f;
+        }
+    }
+}
+
+// The magnitude as an integer, whose order puts infinity above every number and NaN above infinity.
+__device__ __forceinline__ unsigned magnitude(float v) { return __builtin_bit_cast(unsigned, v) & 0x7fffffffu; }
+
+// Sum and largest magnitude over the T threads of a row, in every one of them.  T > 64: through LDS, `red` holds a
+// pair for each wave of the workgroup; every thread of it takes part.
+template <int T>
+__device__ __forceinline__ void row_reduce(float& s, unsigned& m, float (*red)[2]) {
+    constexpr int L = T < 64 ? T : 64;
+#pragma unroll
+    for (int d = L >> 1; d >= 1; d >>= 1) {
+        s += __shfl_xor(s, d);
+        const unsigned o = (unsigned)__shfl_xor((int)m, d);
+        m = o > m ? o : m;
+    }
+    if constexpr (T > 64) {
+        const int wave = (int)threadIdx.x >> 6;
+        if ((threadIdx.x & 63) == 0) {
+            red[wave][0] = s;
+            red[wave][1] = __builtin_bit_cast(float, m);
+        }
+        __syncthreads();
+        const int first = wave / (T / 64) * (T / 64);
+        s = 0.0f;
+        m = 0;
+#pragma unroll
+        for (int w = 0; w < T / 64; ++w) {
+            s += red[first + w][0];
+            const unsigned o = __builtin_bit_cast(unsigned, red[first + w][1]);
+            m = o > m ? o : m;
+        }
+    }
+}
+
+// How a row of largest magnitude `top` goes to 8 bits: q = nearest(v * pre * inv), scale = top / 127.  `pre` keeps
+// 127 / top finite where top is below 2^-100.  A row of zeros has scale 0; one with an infinity or a NaN has that
+// for its scale, and zeros.
+struct ToInt8 {
+    float pre, inv;
+    __device__ __forceinline__ explicit ToInt8(float top) {
+        pre = top < 0x1p-100f ? 0x1p100f : 1.0f;
+        inv = top > 0.0f ? 127.0f / (top * pre) : 0.0f;
+    }
+    // Eight values as bytes: 1.5 * 2^23 added puts the nearest whole number (ties to even) into the low bits.
+    __device__ __forceinline__ u32x2n_t operator()(const float (&v)[8]) const {
+        unsigned b[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            b[i] = __builtin_bit_cast(unsigned, __builtin_fmaf(v[i] * pre, inv, 12582912.0f));
+        u32x2n_t w;
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const unsigned lo = __builtin_amdgcn_perm(b[4 * i + 1], b[4 * i], 0x0c0c0400u);
+            const unsigned hi = __builtin_amdgcn_perm(b[4 * i + 3], b[4 * i + 2], 0x0c0c0400u);
+            w[i] = __builtin_amdgcn_perm(hi, lo, 0x05040100u);
+        }
+        return w;
+    }
+};
+__device__ __forceinline__ void store_int8(int8_t* q, int64_t off, int left, u32x2n_t w) {
+    if (left >= 8) {
+        *(u32x2n_t*)(q + off) = w;
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if (i < left) q[off + i] = (int8_t)(w[i / 4] >> (8 * (i % 4)));
+    }
+}
+
+template <int T>
+constexpr int kRowThreads = T < 256 ? 256 : T;
+
+// ---- norm ----------------------------------------------------------------------------------------------------------
+
+template <bool F16, bool INT8, int T, int V>
+__global__ __launch_bounds__(kRowThreads<T>) void rms_norm_kernel(const RowArgs a) {
+    constexpr int R = kRowThreads<T> / T;
+    __shared__ float red[kRowThreads<T> / 64][2];
+    const int t = (int)threadIdx.x % T;
+    const int64_t row = (int64_t)blockIdx.x * R + (int)threadIdx.x / T;
+    const bool in = row < a.M;
+    u32x4s_t h[V], r[V];
+    float g[V][8];
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+        const int c = (v * T + t) * 8, left = in ? a.C - c : 0;
+        h[v] = load_piece(a.x, row * a.ldx + c, left);
+        if (a.res) r[v] = load_piece(a.res, row * a.ldr + c, left);
+    }
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+        const int c = (v * T + t) * 8;
+        load_gamma(a, c, a.C - c, g[v]);
+    }
+    float s = 0.0f;
+    unsigned m = 0;
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+        if (a.res) h[v] = add_rounded<F16>(h[v], r[v]);
+        float f[8];
+        unpack8<F16>(h[v], f);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            s = __builtin_fmaf(f[i], f[i], s);
+            if constexpr (INT8) {
+                const unsigned o = magnitude(f[i] * g[v][i]);
+                m = o > m ? o : m;
+            }
+        }
+    }
+    row_reduce<T>(s, m, red);
+    const float rstd = 1.0f / __builtin_sqrtf(s / (float)a.C + a.eps);
+    if (!in) return;
+    if (t == 0 && a.rstd) a.rstd[row] = rstd;
+    const float top = __builtin_bit_cast(float, m);
+    [[maybe_unused]] const ToInt8 to(top);
+    if constexpr (INT8)
+        if (t == 0) a.scale[row] = top * rstd / 127.0f;
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+        const int c = (v * T + t) * 8, left = a.C - c;
+        float f[8];
+        unpack8<F16>(h[v], f);
+        if (a.h) store_piece<F16>(a.h, row * a.ldh + c, left, f);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) f[i] = INT8 ? f[i] * g[v][i] : f[i] * rstd * g[v][i];
+        if constexpr (INT8)
+            store_int8(a.q, row * a.ldq + c, left, to(f));
+        else
+            store_piece<F16>(a.y, row * a.ldy + c, left, f);
+    }
+}
+
+// Rows that registers do not hold: one workgroup of 1024 threads, x and residual read twice.
+template <bool F16, bool INT8>
+__global__ __launch_bounds__(1024) void rms_norm_long_kernel(const RowArgs a) {
+    __shared__ float red[16][2];
+    const int64_t row = blockIdx.x;
+    float s = 0.0f;
+    unsigned m = 0;
+    for (int c = (int)threadIdx.x * 8; c < a.C; c += 8192) {
+        u32x4s_t h = load_piece(a.x, row * a.ldx + c, a.C - c);
+        if (a.res) h = add_rounded<F16>(h, load_piece(a.res, row * a.ldr + c, a.C - c));
+        float f[8], g[8];
+        unpack8<F16>(h, f);
+        if constexpr (INT8) load_gamma(a, c, a.C - c, g);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            s = __builtin_fmaf(f[i], f[i], s);
+            if constexpr (INT8) {
+                const unsigned o = magnitude(f[i] * g[i]);
+                m = o > m ? o : m;
+            }
+        }
+    }
+    row_reduce<1024>(s, m, red);
+    const float rstd = 1.0f / __builtin_sqrtf(s / (float)a.C + a.eps);
+    if (threadIdx.x == 0 && a.rstd) a.rstd[row] = rstd;
+    const float top = __builtin_bit_cast(float, m);
+    [[maybe_unused]] const ToInt8 to(top);
+    if constexpr (INT8)
+        if (threadIdx.x == 0) a.scale[row] = top * rstd / 127.0f;
+    for (int c = (int)threadIdx.x * 8; c < a.C; c += 8192) {
+        const int left = a.C - c;
+        u32x4s_t h = load_piece(a.x, row * a.ldx + c, left);
+        if (a.res) h = add_rounded<F16>(h, load_piece(a.res, row * a.ldr + c, left));
+        float f[8], g[8];
+        unpack8<F16>(h, f);
+        load_gamma(a, c, left, g);
+        if (a.h) store_piece<F16>(a.h, row * a.ldh + c, left, f);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) f[i] = INT8 ? f[i] * g[i] : f[i] * rstd * g[i];
+        if constexpr (INT8)
+            store_int8(a.q, row * a.ldq + c, left, to(f));
+        else
+            store_piece<F16>(a.y, row * a.ldy + c, left, f);
+    }
+}
+
+// ---- rows to 8 bits ------------------------------------------------------------------------------------------------
+
+// act(x) * gate of eight columns.
+template <bool F16>
+__device__ __forceinline__ void activated(const RowArgs& a, u32x4s_t x, u32x4s_t gate, float (&f)[8]) {
+    unpack8<F16>(x, f);
+    with_act(a.act, [&](auto A) __attribute__((always_inline)) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) f[i] = act_of<decltype(A)::value>(f[i]);
+    });
+    if (a.res) {
+        float g[8];
+        unpack8<F16>(gate, g);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) f[i] *= g[i];
+    }
+}
+
+template <bool F16, int T, int V>
+__global__ __launch_bounds__(kRowThreads<T>) void quantize_rows_kernel(const RowArgs a) {
+    constexpr int R = kRowThreads<T> / T;
+    __shared__ float red[kRowThreads<T> / 64][2];
+    const int t = (int)threadIdx.x % T;
+    const int64_t row = (int64_t)blockIdx.x * R + (int)threadIdx.x / T;
+    const bool in = row < a.M;
+    u32x4s_t x[V], r[V];
+    float f[V][8];
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+        const int c = (v * T + t) * 8, left = in ? a.C - c : 0;
+        x[v] = load_piece(a.x, row * a.ldx + c, left);
+        if (a.res) r[v] = load_piece(a.res, row * a.ldr + c, left);
+    }
+    float s = 0.0f;
+    unsigned m = 0;
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+        activated<F16>(a, x[v], r[v], f[v]);  // (0 past the row's end: every activation is 0 there)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const unsigned o = magnitude(f[v][i]);
+            m = o > m ? o : m;
+        }
+    }
+    row_reduce<T>(s, m, red);
+    if (!in) return;
+    const float top = __builtin_bit_cast(float, m);
+    const ToInt8 to(top);
+    if (t == 0) a.scale[row] = top / 127.0f;
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+        const int c = (v * T + t) * 8;
+        store_int8(a.q, row * a.ldq + c, a.C - c, to(f[v]));
+    }
+}
+
+template <bool F16>
+__global__ __launch_bounds__(1024) void quantize_rows_long_kernel(const RowArgs a) {
+    __shared__ float red[16][2];
+    const int64_t row = blockIdx.x;
+    const auto values = [&](int c, float (&f)[8]) __attribute__((always_inline)) {
+        u32x4s_t gate{0, 0, 0, 0};
+        if (a.res) gate = load_piece(a.res, row * a.ldr + c, a.C - c);
+        activated<F16>(a, load_piece(a.x, row * a.ldx + c, a.C - c), gate, f);
+    };
+    float s = 0.0f;
+    unsigned m = 0;
+    for (int c = (int)threadIdx.x * 8; c < a.C; c += 8192) {
+        float f[8];
+        values(c, f);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const unsigned o = magnitude(f[i]);
+            m = o > m ? o : m;
+        }
+    }
+    row_reduce<1024>(s, m, red);
+    const float top = __builtin_bit_cast(float, m);
+    const ToInt8 to(top);
+    if (threadIdx.x == 0) a.scale[row] = top / 127.0f;
+    for (int c = (int)threadIdx.x * 8; c < a.C; c += 8192) {
+        float f[8];
+        values(c, f);
+        store_int8(a.q, row * a.ldq + c, a.C - c, to(f));
+    }
+}
+
+// ---- gradient of the norm ------------------------------------------------------------------------------------------
+
+// The workgroups take rows in turn and keep their sums for dgamma in registers; at the end each writes them out, and
+// column_sum adds the workgroups' (or, of a single workgroup, they are dgamma).
+template <bool F16, int T, int V>
+__global__ __launch_bounds__(kRowThreads<T>) void rms_norm_backward_kernel(const RowArgs a) {
+    constexpr int BT = kRowThreads<T>, R = BT / T;
+    __shared__ float red[2][BT / 64][2];
+    __shared__ float cols[R > 1 ? R : 1][R > 1 ? T * V * 8 : 1];
+    const int t = (int)threadIdx.x % T, rl = (int)threadIdx.x / T;
+    const int64_t step = (int64_t)gridDim.x * R;
+    float g[V][8], dg[V][8];
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+        const int c = (v * T + t) * 8;
+        load_gamma(a, c, a.C - c, g[v]);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) dg[v][i] = 0.0f;
+    }
+    u32x4s_t h[V], dy[V], dh[V], nh[V], ndy[V], ndh[V];
+    float rs = 0.0f, nrs = 0.0f;
+    const auto load = [&](int64_t row, u32x4s_t (&ph)[V], u32x4s_t (&pdy)[V], u32x4s_t (&pdh)[V], float& prs)
+                          __attribute__((always_inline)) {
+        const bool in = row < a.M;
+        prs = in ? a.rstd[row] : 0.0f;
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+            const int c = (v * T + t) * 8, left = in ? a.C - c : 0;
+            ph[v] = load_piece(a.x, row * a.ldx + c, left);
+            pdy[v] = load_piece(a.dy, row * a.lddy + c, left);
+            if (a.res) pdh[v] = load_piece(a.res, row * a.ldr + c, left);
+        }
+    };
+    int odd = 0;
+    int64_t base = (int64_t)blockIdx.x * R;
+    if (base < a.M) load(base + rl, h, dy, dh, rs);
+    for (; base < a.M; base += step) {
+        const int64_t row = base + rl;
+        if (base + step < a.M) load(row + step, nh, ndy, ndh, nrs);  // in flight while this row is joined
+        float s = 0.0f;
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+            float fh[8], fd[8];
+            unpack8<F16>(h[v], fh);
+            unpack8<F16>(dy[v], fd);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                s = __builtin_fmaf(fd[i] * g[v][i], fh[i], s);
+                dg[v][i] = __builtin_fmaf(fd[i], fh[i] * rs, dg[v][i]);
+            }
+        }
+        unsigned none = 0;
+        row_reduce<T>(s, none, red[odd]);  // (two sets of sums in turn: one barrier a row)
+        odd ^= 1;
+        const float k = s / (float)a.C * rs * rs;  // xh mean(g xh) = h k
+        if (row < a.M) {
+#pragma unroll
+            for (int v = 0; v < V; ++v) {
+                const int c = (v * T + t) * 8;
+                float fh[8], fd[8];
+                unpack8<F16>(h[v], fh);
+                unpack8<F16>(dy[v], fd);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) fd[i] = rs * __builtin_fmaf(-k, fh[i], fd[i] * g[v][i]);
+                if (a.res) {
+                    unpack8<F16>(dh[v], fh);
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) fd[i] += fh[i];
+                }
+                store_piece<F16>(a.y, row * a.ldy + c, a.C - c, fd);
+            }
+        }
+#pragma unroll
+        for (int v = 0; v < V; ++v) h[v] = nh[v], dy[v] = ndy[v], dh[v] = ndh[v];
+        rs = nrs;
+    }
+    if (!a.dgamma) return;
+    if constexpr (R > 1) {
+#pragma unroll
+        for (int v = 0; v < V; ++v)
+#pragma unroll
+            for (int i = 0; i < 8; ++i) cols[rl][(v * T + t) * 8 + i] = dg[v][i];
+        __syncthreads();
+        if (rl > 0) return;
+#pragma unroll
+        for (int v = 0; v < V; ++v)
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                for (int k = 1; k < R; ++k) dg[v][i] += cols[k][(v * T + t) * 8 + i];
+    }
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+        const int c = (v * T + t) * 8;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            if (c + i >= a.C) continue;
+            if (gridDim.x == 1)
+                store_kind(a.dgamma, c + i, a.param_kind, dg[v][i]);
+            else
+                a.part[(int64_t)blockIdx.x * a.C + c + i] = dg[v][i];
+        }
+    }
+}
+
+// Long rows: each read twice, and the sums for dgamma kept in the workgroup's part of the workspace, where a thread
+// adds to its own columns alone.
+template <bool F16>
+__global__ __launch_bounds__(1024) void rms_norm_backward_long_kernel(const RowArgs a) {
+    __shared__ float red[2][16][2];
+    float* part = a.part ? a.part + (int64_t)blockIdx.x * a.C : nullptr;
+    int odd = 0;
+    bool first = true;
+    for (int64_t row = blockIdx.x; row < a.M; row += gridDim.x) {
+        const float rs = a.rstd[row];
+        float s = 0.0f;
+        for (int c = (int)threadIdx.x * 8; c < a.C; c += 8192) {
+            float fh[8], fd[8], g[8];
+            unpack8<F16>(load_piece(a.x, row * a.ldx + c, a.C - c), fh);
+            unpack8<F16>(load_piece(a.dy, row * a.lddy + c, a.C - c), fd);
+            load_gamma(a, c, a.C - c, g);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) s = __builtin_fmaf(fd[i] * g[i], fh[i], s);
+        }
+        unsigned none = 0;
+        row_reduce<1024>(s, none, red[odd]);
+        odd ^= 1;
+        const float k = s / (float)a.C * rs * rs;
+        for (int c = (int)threadIdx.x * 8; c < a.C; c += 8192) {
+            const int left = a.C - c;
+            float fh[8], fd[8], g[8], dx[8];
+            unpack8<F16>(load_piece(a.x, row * a.ldx + c, left), fh);
+            unpack8<F16>(load_piece(a.dy, row * a.lddy + c, left), fd);
+            load_gamma(a, c, left, g);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) dx[i] = rs * __builtin_fmaf(-k, fh[i], fd[i] * g[i]);
+            if (a.res) {
+                float f[8];
+                unpack8<F16>(load_piece(a.res, row * a.ldr + c, left), f);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) dx[i] += f[i];
+            }
+            store_piece<F16>(a.y, row * a.ldy + c, left, dx);
+            if (part) {
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    if (i < left) part[c + i] = __builtin_fmaf(fd[i], fh[i] * rs, first ? 0.0f : part[c + i]);
+            }
+        }
+        first = false;
+    }
+}
+
+// ---- host ----------------------------------------------------------------------------------------------------------
+
+// Threads and vectors of a row; T == 0: rows that registers do not hold.
+struct RowShape {
+    int T, V;
+    int threads() const { return T == 0 ? 1024 : (T < 256 ? 256 : T); }
+    int rows() const { return T == 0 ? 1 : threads() / T; }
+};
+static RowShape row_shape(int64_t M, int64_t C, bool backward = false) {
+    const int64_t n = (C + 7) / 8;
+    if (n <= 16) return {16, 1};
+    if (n <= 64) return {64, 1};
+    if (n <= 128) return {128, 1};
+    if (n <= 256) return {256, 1};
+    if (n <= 512) return M < 512 ? RowShape{512, 1} : RowShape{256, 2};
+    if (n <= 1024) return M < 512 ? RowShape{1024, 1} : RowShape{512, 2};
+    if (n <= 2048) return {1024, 2};
+    if (n <= 4096 && !backward) return {1024, 4};  // (the backward pass has no registers for four vectors)
+    return {0, 0};
+}
+
+#define IGC_BACK_SHAPES(X) X(16, 1) X(64, 1) X(128, 1) X(256, 1) X(512, 1) X(256, 2) X(1024, 1) X(512, 2) X(1024, 2)
+#define IGC_ROW_SHAPES(X) IGC_BACK_SHAPES(X) X(1024, 4)
+
+template <bool F16, bool INT8>
+static void launch_norm(RowShape s, dim3 grid, hipStream_t st, const RowArgs& a) {
+#define IGC_ROW_CASE(TT, VV)                                                                                    \
+    if (s.T == TT && s.V == VV) {                                                                               \
+        hipLaunchKernelGGL((rms_norm_kernel<F16, INT8, TT, VV>), grid, dim3(s.threads()), 0, st, a);            \
+        return;                                                                                                 \
+    }
+    IGC_ROW_SHAPES(IGC_ROW_CASE)
+#undef IGC_ROW_CASE
+    hipLaunchKernelGGL((rms_norm_long_kernel<F16, INT8>), grid, dim3(1024), 0, st, a);
+}
+template <bool F16>
+static void launch_quantize(RowShape s, dim3 grid, hipStream_t st, const RowArgs& a) {
+#define IGC_ROW_CASE(TT, VV)                                                                                    \
+    if (s.T == TT && s.V == VV) {                                                                               \
+        hipLaunchKernelGGL((quantize_rows_kernel<F16, TT, VV>), grid, dim3(s.threads()), 0, st, a);             \
+        return;                                                                                                 \
+    }
+    IGC_ROW_SHAPES(IGC_ROW_CASE)
+#undef IGC_ROW_CASE
+    hipLaunchKernelGGL((quantize_rows_long_kernel<F16>), grid, dim3(1024), 0, st, a);
+}
+template <bool F16>
+static void launch_backward(RowShape s, dim3 grid, hipStream_t st, const RowArgs& a) {
+#define IGC_ROW_CASE(TT, VV)                                                                                    \
+    if (s.T == TT && s.V == VV) {                                                                               \
+        hipLaunchKernelGGL((rms_norm_backward_kernel<F16, TT, VV>), grid, dim3(s.threads()), 0, st, a);         \
+        return;                                                                                                 \
+    }
+    IGC_BACK_SHAPES(IGC_ROW_CASE)
+#undef IGC_ROW_CASE
+    hipLaunchKernelGGL((rms_norm_backward_long_kernel<F16>), grid, dim3(1024), 0, st, a);
+}
+
+// Rows of `bytes` a value: INVALID without a pointer or with rows that overlap, MISALIGNED by the 16-byte rule.
+static igc_status_t check_rows(const void* ptr, int64_t ld, int64_t C, int bytes) {
+    if (!ptr || ld < C) return IGC_ERR_INVALID_VALUE;
+    return !aligned16(ptr) || ld * bytes % 16 != 0 ? IGC_ERR_MISALIGNED : IGC_OK;
+}
+static bool misplaced(const void* ptr, igc_out_t type) { return reinterpret_cast<uintptr_t>(ptr) % out_size(type) != 0; }
+// Sizes beyond these are refused, as are leading dimensions whose offsets pass 64 bits.
+static bool rows_too_large(int64_t M, int64_t C) { return M >= (1ll << 40) || C >= (1ll << 30); }
+static bool strides_too_large(std::initializer_list<int64_t> lds) {
+    for (const int64_t ld : lds)
+        if (ld >= (1ll << 32)) return true;
+    return false;
+}
+
+static igc_status_t norm_any(bool fp16, bool int8, int64_t M, int64_t C, const void* x, int64_t ldx, const void* res,
+                             int64_t ldr, void* h, int64_t ldh, const void* gamma, igc_out_t pt, float eps, void* y,
+                             int64_t ldy, float* scale, float* rstd, hipStream_t stream) {
+    if (M < 0 || C < 1 || !valid_type(pt) || !(eps >= 0.0f)) return IGC_ERR_INVALID_VALUE;
+    if (M == 0) return IGC_OK;
+    if (const igc_status_t st = check_rows(x, ldx, C, 2)) return st;
+    if (res)
+        if (const igc_status_t st = check_rows(res, ldr, C, 2)) return st;
+    if (h)
+        if (const igc_status_t st = check_rows(h, ldh, C, 2)) return st;
+    if (const igc_status_t st = check_rows(y, ldy, C, int8 ? 1 : 2)) return st;
+    if (int8 && !scale) return IGC_ERR_INVALID_VALUE;
+    if (misplaced(gamma, pt) || misplaced(scale, IGC_OUT_F32) || misplaced(rstd, IGC_OUT_F32)) return IGC_ERR_MISALIGNED;
+    if (rows_too_large(M, C) || strides_too_large({ldx, res ? ldr : 0, h ? ldh : 0, ldy})) return IGC_ERR_UNSUPPORTED;
+    const RowShape s = row_shape(M, C);
+    const int64_t blocks = (M + s.rows() - 1) / s.rows();
+    if (!launchable(blocks, s.threads())) return IGC_ERR_UNSUPPORTED;
+    RowArgs a{};
+    a.x = x;
+    a.res = res;
+    a.h = h;
+    a.gamma = gamma;
+    a.y = int8 ? nullptr : y;
+    a.q = int8 ? (int8_t*)y : nullptr;
+    a.scale = scale;
+    a.rstd = rstd;
+    a.M = M;
+    a.C = (int)C;
+    a.ldx = ldx;
+    a.ldr = ldr;
+    a.ldh = ldh;
+    a.ldy = a.ldq = ldy;
+    a.eps = eps;
+    a.param_kind = (int)pt;
+    a.param_vec = aligned16(gamma);
+    (void)hipGetLastError();
+    const dim3 grid((unsigned)blocks);
+    if (int8 && fp16)
+        launch_norm<true, true>(s, grid, stream, a);
+    else if (int8)
+        launch_norm<false, true>(s, grid, stream, a);
+    else if (fp16)
+        launch_norm<true, false>(s, grid, stream, a);
+    else
+        launch_norm<false, false>(s, grid, stream, a);
+    return hipGetLastError() == hipSuccess ? IGC_OK : IGC_ERR_HIP;
+}
+
+static igc_status_t quantize_any(bool fp16, int64_t M, int64_t C, igc_act_t act, const void* x, int64_t ldx,
+                                 const void* gate, int64_t ldg, int8_t* q, int64_t ldq, float* scale, hipStream_t stream) {
+    if (M < 0 || C < 1 || (int)act < IGC_ACT_NONE || (int)act > IGC_ACT_SILU) return IGC_ERR_INVALID_VALUE;
+    if (M == 0) return IGC_OK;
+    if (const igc_status_t st = check_rows(x, ldx, C, 2)) return st;
+    if (gate)
+        if (const igc_status_t st = check_rows(gate, ldg, C, 2)) return st;
+    if (const igc_status_t st = check_rows(q, ldq, C, 1)) return st;
+    if (!scale) return IGC_ERR_INVALID_VALUE;
+    if (misplaced(scale, IGC_OUT_F32)) return IGC_ERR_MISALIGNED;
+    if (rows_too_large(M, C) || strides_too_large({ldx, gate ? ldg : 0, ldq})) return IGC_ERR_UNSUPPORTED;
+    const RowShape s = row_shape(M, C);
+    const int64_t blocks = (M + s.rows() - 1) / s.rows();
+    if (!launchable(blocks, s.threads())) return IGC_ERR_UNSUPPORTED;
+    RowArgs a{};
+    a.x = x;
+    a.res = gate;
+    a.q = q;
+    a.scale = scale;
+    a.M = M;
+    a.C = (int)C;
+    a.ldx = ldx;
+    a.ldr = ldg;
+    a.ldq = ldq;
+    a.act = (int)act;
+    (void)hipGetLastError();
+    if (fp16)
+        launch_quantize<true>(s, dim3((unsigned)blocks), stream, a);
+    else
+        launch_quantize<false>(s, dim3((unsigned)blocks), stream, a);
+    return hipGetLastError() == hipSuccess ? IGC_OK : IGC_ERR_HIP;
+}
+
+// Workgroups of the backward pass: they take rows in turn, two for each CU (one of 1024 threads), so that the sums for
+// dgamma that they leave stay small beside the rows.
+static int64_t backward_groups(RowShape s, int64_t M) {
+    const int64_t most = s.threads() >= 1024 ? 256 : 512, blocks = (M + s.rows() - 1) / s.rows();
+    return blocks < most ? blocks : most;
+}
+static int64_t backward_bytes(RowShape s, int64_t M, int64_t C) {
+    const int64_t g = backward_groups(s, M);
+    return g > 1 || s.T == 0 ? round_up(g * C * 4, 256) : 0;
+}
+
+static igc_status_t backward_any(bool fp16, int64_t M, int64_t C, const void* h, int64_t ldh, const void* gamma,
+                                 igc_out_t pt, const float* rstd, const void* dy, int64_t lddy, const void* dh,
+                                 int64_t lddh, void* dx, int64_t lddx, void* dgamma, void* user_ws, int64_t user_ws_bytes,
+                                 hipStream_t stream) {
+    if (M < 0 || C < 1 || !valid_type(pt)) return IGC_ERR_INVALID_VALUE;
+    if (M == 0 && !dgamma) return IGC_OK;
+    if (M > 0) {
+        if (const igc_status_t st = check_rows(h, ldh, C, 2)) return st;
+        if (const igc_status_t st = check_rows(dy, lddy, C, 2)) return st;
+        if (dh)
+            if (const igc_status_t st = check_rows(dh, lddh, C, 2)) return st;
+        if (const igc_status_t st = check_rows(dx, lddx, C, 2)) return st;
+        if (!rstd) return IGC_ERR_INVALID_VALUE;
+    }
+    if (misplaced(gamma, pt) || misplaced(dgamma, pt) || misplaced(rstd, IGC_OUT_F32)) return IGC_ERR_MISALIGNED;
+    if (rows_too_large(M, C) || (M > 0 && strides_too_large({ldh, lddy, dh ? lddh : 0, lddx}))) return IGC_ERR_UNSUPPORTED;
+    const RowShape s = row_shape(M, C, true);
+    const int64_t groups = backward_groups(s, M);
+    Workspace ws;
+    if (const igc_status_t st = ws.take(dgamma && M > 0 ? backward_bytes(s, M, C) : 0, user_ws, user_ws_bytes, stream))
+        return st;
+    RowArgs a{};
+    a.x = h;
+    a.res = dh;
+    a.dy = dy;
+    a.gamma = gamma;
+    a.y = dx;
+    a.rstd = const_cast<float*>(rstd);
+    a.dgamma = dgamma;
+    a.part = dgamma ? (float*)ws.ptr : nullptr;
+    a.M = M;
+    a.C = (int)C;
+    a.ldx = ldh;
+    a.ldr = lddh;
+    a.lddy = lddy;
+    a.ldy = lddx;
+    a.param_kind = (int)pt;
+    a.param_vec = aligned16(gamma);
+    (void)hipGetLastError();
+    if (M > 0) {
+        if (fp16)
+            launch_backward<true>(s, dim3((unsigned)groups), stream, a);
+        else
+            launch_backward<false>(s, dim3((unsigned)groups), stream, a);
+        if (hipGetLastError() != hipSuccess) return IGC_ERR_HIP;
+    }
+    // (one workgroup wrote dgamma itself, but of long rows)
+    if (dgamma && (M == 0 || groups > 1 || s.T == 0))
+        if (launch_column_sum((const float*)ws.ptr, C, (int)groups, dgamma, (int)pt, stream) != hipSuccess) return IGC_ERR_HIP;
+    return IGC_OK;
+}
+
+}  // namespace igc
+
+using namespace igc;
+
+extern "C" {
+
+#define IGC_NORM(T, FP16)                                                                                               \
+    igc_status_t rms_norm_##T(int64_t M, int64_t C, const void* x, int64_t ldx, const void* residual, int64_t ldr,      \
+                              void* h, int64_t ldh, const void* gamma, igc_out_t param_type, float eps, void* y,        \
+                              int64_t ldy, float* rstd, igc_stream_t stream) {                                          \
+        return norm_any(FP16, false, M, C, x, ldx, residual, ldr, h, ldh, gamma, param_type, eps, y, ldy, nullptr,      \
+                        rstd, (hipStream_t)stream);                                                                     \
+    }                                                                                                                   \
+    igc_status_t rms_norm_int8_##T(int64_t M, int64_t C, const void* x, int64_t ldx, const void* residual, int64_t ldr, \
+                                   void* h, int64_t ldh, const void* gamma, igc_out_t param_type, float eps, int8_t* q, \
+                                   int64_t ldq, float* scale, igc_stream_t stream) {                                    \
+        return norm_any(FP16, true, M, C, x, ldx, residual, ldr, h, ldh, gamma, param_type, eps, q, ldq, scale,         \
+                        nullptr, (hipStream_t)stream);                                                                  \
+    }                                                                                                                   \
+    igc_status_t rms_norm_backward_##T(int64_t M, int64_t C, const void* h, int64_t ldh, const void* gamma,             \
+                                       igc_out_t param_type, const float* rstd, const void* dy, int64_t lddy,           \
+                                       const void* dh, int64_t lddh, void* dx, int64_t lddx, void* dgamma,              \
+                                       igc_stream_t stream) {                                                           \
+        return backward_any(FP16, M, C, h, ldh, gamma, param_type, rstd, dy, lddy, dh, lddh, dx, lddx, dgamma, nullptr, \
+                            0, (hipStream_t)stream);                                                                    \
+    }                                                                                                                   \
+    igc_status_t rms_norm_backward_##T##_ex(int64_t M, int64_t C, const void* h, int64_t ldh, const void* gamma,        \
+                                            igc_out_t param_type, const float* rstd, const void* dy, int64_t lddy,      \
+                                            const void* dh, int64_t lddh, void* dx, int64_t lddx, void* dgamma,         \
+                                            void* workspace, int64_t workspace_bytes, igc_stream_t stream) {            \
+        return backward_any(FP16, M, C, h, ldh, gamma, param_type, rstd, dy, lddy, dh, lddh, dx, lddx, dgamma,          \
+                            workspace, workspace_bytes, (hipStream_t)stream);                                           \
+    }                                                                                                                   \
+    igc_status_t quantize_rows_int8_##T(int64_t M, int64_t C, igc_act_t act, const void* x, int64_t ldx,                \
+                                        const void* gate, int64_t ldg, int8_t* q, int64_t ldq, float* scale,            \
+                                        igc_stream_t stream) {                                                          \
+        return quantize_any(FP16, M, C, act, x, ldx, gate, ldg, q, ldq, scale, (hipStream_t)stream);                    \
+    }
+IGC_NORM(bf16, false)
+IGC_NORM(fp16, true)
+
+int64_t igc_rms_norm_backward_workspace_bytes(int64_t M, int64_t C) {
+    if (M < 0 || C < 1 || rows_too_large(M, C)) return -1;
+    return M == 0 ? 0 : backward_bytes(row_shape(M, C, true), M, C);
+}
+
+}  // extern "C"

@@ -93,11 +93,14 @@ hipError_t launch_split_reduce(const float* ws, int S, int64_t ws_stride, int64_
 }
 
 // The same sum, then the epilogue: eight outputs of a row a thread, partials added in split order.  VEC:
-// every row of the output, residual and pre is a 16-byte multiple from the next.
-template <bool VEC>
+// every row of the output, residual and pre is a 16-byte multiple from the next.  With EpiInt8 the partials are
+// 32-bit integers, whose sum is exact.
+template <bool VEC, class E>
 __global__ __launch_bounds__(256) void split_epilogue_kernel(const float* __restrict__ ws, int S, int64_t ws_stride,
                                                              int64_t M, int64_t N, int64_t ldws, void* C, int64_t ldc,
-                                                             int kind, const Epi e) {
+                                                             int kind, const E e) {
+    constexpr bool INT8 = std::is_same<E, EpiInt8>::value;
+    using Part = typename std::conditional<INT8, i32x4_t, f32x4r_t>::type;
     const int64_t n8 = (N + 7) / 8;
     const int64_t idx = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
     if (idx >= M * n8) return;
@@ -112,25 +115,34 @@ __global__ __launch_bounds__(256) void split_epilogue_kernel(const float* __rest
     for (int i = 0; i < 8; ++i) b[i] = e.bias && i < left ? load_kind(e.bias, n + i, e.bias_kind) : 0.0f;
     const float* src = ws + m * ldws + n;
     const float* src1 = two ? src + 4 : src;
-    f32x4r_t lo = *(const f32x4r_t*)src, hi = *(const f32x4r_t*)src1;
+    Part lo = *(const Part*)src, hi = *(const Part*)src1;
     int s = 1;
     for (; s + 3 < S; s += 4) {
-        f32x4r_t p0[4], p1[4];
+        Part p0[4], p1[4];
 #pragma unroll
         for (int u = 0; u < 4; ++u) {
-            p0[u] = *(const f32x4r_t*)(src + (s + u) * ws_stride);
-            p1[u] = *(const f32x4r_t*)(src1 + (s + u) * ws_stride);
+            p0[u] = *(const Part*)(src + (s + u) * ws_stride);
+            p1[u] = *(const Part*)(src1 + (s + u) * ws_stride);
         }
 #pragma unroll
         for (int u = 0; u < 4; ++u) lo += p0[u], hi += p1[u];
     }
     for (; s < S; ++s) {
-        lo += *(const f32x4r_t*)(src + s * ws_stride);
-        hi += *(const f32x4r_t*)(src1 + s * ws_stride);
+        lo += *(const Part*)(src + s * ws_stride);
+        hi += *(const Part*)(src1 + s * ws_stride);
     }
     float v[8];
+    if constexpr (INT8) {
+        const float sa = e.sa ? e.sa[m] : 1.0f;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) v[i] = lo[i] + b[i], v[4 + i] = hi[i] + b[4 + i];
+        for (int i = 0; i < 8; ++i) {
+            const float sb = e.sb && i < left ? e.sb[n + i] : 1.0f;
+            v[i] = __builtin_fmaf((float)(i < 4 ? lo[i & 3] : hi[i & 3]) * sa, sb, b[i]);
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v[i] = lo[i] + b[i], v[4 + i] = hi[i] + b[4 + i];
+    }
     if (e.backward) {
         if (e.pre)
             with_act(e.act, [&](auto A) __attribute__((always_inline)) {
@@ -151,19 +163,28 @@ __global__ __launch_bounds__(256) void split_epilogue_kernel(const float* __rest
     store8(C, m * ldc + n, kind, left, VEC, v);
 }
 
-hipError_t launch_split_epilogue(const float* ws, int S, int64_t ws_stride, int64_t M, int64_t N, int64_t ldws,
-                                 void* C, int64_t ldc, int kind, bool vec, const Epi& e, hipStream_t stream) {
+template <class E>
+static hipError_t split_epilogue(const float* ws, int S, int64_t ws_stride, int64_t M, int64_t N, int64_t ldws, void* C,
+                                 int64_t ldc, int kind, bool vec, const E& e, hipStream_t stream) {
     const int64_t work = M * ((N + 7) / 8);
     if (work <= 0) return hipSuccess;
     const int64_t blocks = (work + 255) / 256;
     if (blocks > 0x7fffffff) return hipErrorInvalidValue;
     if (vec)
-        hipLaunchKernelGGL(split_epilogue_kernel<true>, dim3((unsigned)blocks), dim3(256), 0, stream, ws, S, ws_stride,
-                           M, N, ldws, C, ldc, kind, e);
+        hipLaunchKernelGGL((split_epilogue_kernel<true, E>), dim3((unsigned)blocks), dim3(256), 0, stream, ws, S,
+                           ws_stride, M, N, ldws, C, ldc, kind, e);
     else
-        hipLaunchKernelGGL(split_epilogue_kernel<false>, dim3((unsigned)blocks), dim3(256), 0, stream, ws, S,
+        hipLaunchKernelGGL((split_epilogue_kernel<false, E>), dim3((unsigned)blocks), dim3(256), 0, stream, ws, S,
                            ws_stride, M, N, ldws, C, ldc, kind, e);
     return hipGetLastError();
+}
+hipError_t launch_split_epilogue(const float* ws, int S, int64_t ws_stride, int64_t M, int64_t N, int64_t ldws,
+                                 void* C, int64_t ldc, int kind, bool vec, const Epi& e, hipStream_t stream) {
+    return split_epilogue(ws, S, ws_stride, M, N, ldws, C, ldc, kind, vec, e, stream);
+}
+hipError_t launch_split_epilogue(const int* ws, int S, int64_t ws_stride, int64_t M, int64_t N, int64_t ldws, void* C,
+                                 int64_t ldc, int kind, const EpiInt8& e, hipStream_t stream) {
+    return split_epilogue((const float*)ws, S, ws_stride, M, N, ldws, C, ldc, kind, true, e, stream);
 }
 
 // Zeroes n stream-K flags.  System-coherent stores (SC0 | SC1) write through

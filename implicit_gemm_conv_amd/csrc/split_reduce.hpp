@@ -16,6 +16,10 @@ hipError_t launch_split_reduce(const float* ws, int S, int64_t ws_stride, int64_
 struct Epi;
 hipError_t launch_split_epilogue(const float* ws, int S, int64_t ws_stride, int64_t M, int64_t N, int64_t ldws,
                                  void* C, int64_t ldc, int kind, bool vec, const Epi& e, hipStream_t stream);
+// The same for the 32-bit integer partials of a product of 8-bit integers.
+struct EpiInt8;
+hipError_t launch_split_epilogue(const int* ws, int S, int64_t ws_stride, int64_t M, int64_t N, int64_t ldws, void* C,
+                                 int64_t ldc, int kind, const EpiInt8& e, hipStream_t stream);
 
 // Sets flags[0 .. n) to zero, ordered before later work on `stream`.
 hipError_t launch_clear_flags(int* flags, int n, hipStream_t stream);

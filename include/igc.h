@@ -4,7 +4,9 @@
  * convolutions (forward, data gradient, filter gradient), for AMD Instinct
  * MI355X (gfx950); products and forward convolutions with bias, activation and
  * residual in their epilogue, the epilogue's gradient, and group norm with an
- * activation, forward and backward.
+ * activation, forward and backward; products of 8-bit integers with a scale for
+ * each row and column, and the row operators that feed them: the root-mean-square
+ * norm (to 16 or 8 bits, and its gradient) and activations rounded to 8 bits.
  *
  * What is computed follows the "B200 TMA Pipeline Designer" page (section
  * "E -- Executable steps": a tiled matrix product fed by a ring of PIPE_DEPTH
@@ -41,7 +43,7 @@
  * - Leading dimensions are in ELEMENTS, not bytes.
  * - Alignment: every tensor base pointer must be 16-byte aligned and every
  *   leading dimension times the element size a multiple of 16 bytes (8
- *   elements for 16-bit types, 4 for fp32).  Otherwise IGC_ERR_MISALIGNED.
+ *   elements for 16-bit types, 4 for fp32, 16 for 8-bit integers).  Otherwise IGC_ERR_MISALIGNED.
  * - Arguments are checked before anything is launched; on any error nothing
  *   is enqueued and the output is untouched.  No exception crosses the ABI.
  * - Outputs must not alias inputs except where an operation says so (not
@@ -474,6 +476,117 @@ igc_status_t group_norm_nhwc_backward_fp16_ex(int N, int H, int W, int C, int G,
 
 /* Workspace bytes of either direction of the group norm; -1 for bad arguments. */
 int64_t igc_group_norm_workspace_bytes(int N, int H, int W, int C, int G);
+
+/*
+ * Product of 8-bit integers with scales, and an epilogue:
+ *   z[m][n] = scale_a[m] * scale_b[n] * sum_k A[m*lda + k] * B[n*ldb + k] + bias[n]
+ *   pre = z (rounded), D = act(z) + residual
+ * A is M x K and B N x K, K together in both (row-major A, column-major B of
+ * the 16-bit products; the layout of a layer's weights): a row of either stands
+ * for its integers times its scale.  scale_a: M, scale_b: N fp32 values,
+ * 4-byte aligned; NULL: 1.  The sum is exact whatever the schedule; it is
+ * rounded to fp32 once, and once for each scale.  D, the epilogue's tensors and
+ * aliasing are as in gemm_bf16_epilogue; epilogue may be NULL (D = z), and
+ * backward 1 is IGC_ERR_UNSUPPORTED.  K == 0 leaves z = bias, as 0 * scale does;
+ * M == 0 or N == 0 is a no-op.
+ * Requirements: lda, ldb >= K and multiples of 16 (the 16-byte rule), sizes,
+ * pointers and types as everywhere; K < 2^17 (a longer sum may not fit 32 bits),
+ * leading dimensions and the rows of one tile spanning less than 2^31 bytes,
+ * else IGC_ERR_UNSUPPORTED.
+ * Tunes are those of the 16-bit products with IGC_SCOPE_ALL and
+ * IGC_SCOPE_EPILOGUE, a K tile of bk holding 2*bk values; stream-K is
+ * IGC_ERR_UNSUPPORTED.  The parts of a K split are int32 in the workspace, of
+ * igc_gemm_int8_workspace_bytes (-1 for sizes or a tune that the call refuses).
+ * igc_gemm_int8_default_tune tells the built-in choice as
+ * igc_epilogue_default_tune does (bm = 0: the kernel of few rows).
+ */
+igc_status_t gemm_int8(int64_t M, int64_t N, int64_t K, const int8_t *A, int64_t lda, const float *scale_a,
+                       const int8_t *B, int64_t ldb, const float *scale_b, void *D, int64_t ldd, igc_out_t d_type,
+                       const igc_epilogue_t *epilogue, igc_stream_t stream);
+igc_status_t gemm_int8_ex(int64_t M, int64_t N, int64_t K, const int8_t *A, int64_t lda, const float *scale_a,
+                          const int8_t *B, int64_t ldb, const float *scale_b, void *D, int64_t ldd, igc_out_t d_type,
+                          const igc_epilogue_t *epilogue, const igc_tune_t *tune, void *workspace,
+                          int64_t workspace_bytes, igc_stream_t stream);
+int64_t igc_gemm_int8_workspace_bytes(int64_t M, int64_t N, int64_t K, const igc_tune_t *tune);
+int igc_gemm_int8_default_tune(int64_t M, int64_t N, int64_t K, igc_tune_t *out);
+
+/*
+ * Root-mean-square norm of M rows of C values (bf16 or fp16), with the
+ * addition of a residual before it:
+ *   h = x + residual, rounded to their type;  rstd[m] = 1 / sqrt(mean_c h^2 + eps)
+ *   y = h * rstd[m] * gamma[c]     (rounded once)
+ * h is what is normed, so a later call, or the gradient, from the stored h sees
+ * the same numbers.  residual NULL: h = x.  h (the residual stream's new value)
+ * is written when not NULL; rstd likewise (M fp32 values, which the gradient
+ * takes).  gamma: C values of param_type, aligned to their size; NULL: 1.
+ *   rms_norm_int8_*: y goes to 8 bits instead, for gemm_int8's A:
+ *   scale[m] = max_c |y| / 127,  q = y / scale to the nearest integer, ties to
+ *   even, so that q * scale stands for y.  A row of zeros has scale 0 and zeros;
+ *   a row with an infinity or a NaN has scale NaN and zeros, and so gives NaN in
+ *   the product.  Scales below 2^-126 lose bits.
+ * h may be x or residual, and y may be x or residual if h is not the same one
+ * (same leading dimension): a row's values are read before they are written.
+ * A row whose mean square overflows fp32 has rstd 0.
+ * Requirements: M >= 0 (0 is a no-op), C >= 1, leading dimensions >= C, eps >= 0,
+ * else IGC_ERR_INVALID_VALUE; the alignment rule (q: ldq a multiple of 16), any C;
+ * C < 2^30, leading dimensions < 2^32 and fewer than 2^32 threads (M < 2^22 holds
+ * for every C), else IGC_ERR_UNSUPPORTED.  No workspace.
+ */
+igc_status_t rms_norm_bf16(int64_t M, int64_t C, const void *x, int64_t ldx, const void *residual, int64_t ldr, void *h,
+                           int64_t ldh, const void *gamma, igc_out_t param_type, float eps, void *y, int64_t ldy,
+                           float *rstd, igc_stream_t stream);
+igc_status_t rms_norm_fp16(int64_t M, int64_t C, const void *x, int64_t ldx, const void *residual, int64_t ldr, void *h,
+                           int64_t ldh, const void *gamma, igc_out_t param_type, float eps, void *y, int64_t ldy,
+                           float *rstd, igc_stream_t stream);
+igc_status_t rms_norm_int8_bf16(int64_t M, int64_t C, const void *x, int64_t ldx, const void *residual, int64_t ldr,
+                                void *h, int64_t ldh, const void *gamma, igc_out_t param_type, float eps, int8_t *q,
+                                int64_t ldq, float *scale, igc_stream_t stream);
+igc_status_t rms_norm_int8_fp16(int64_t M, int64_t C, const void *x, int64_t ldx, const void *residual, int64_t ldr,
+                                void *h, int64_t ldh, const void *gamma, igc_out_t param_type, float eps, int8_t *q,
+                                int64_t ldq, float *scale, igc_stream_t stream);
+
+/*
+ * Gradient of the norm above, from its h (x where there was no residual),
+ * gamma and rstd.  With g = dy * gamma and xh = h * rstd[m]:
+ *   dx = rstd[m] * (g - xh * mean_c(g * xh)) + dh     (rounded once)
+ *   dgamma[c] = sum_m dy * xh     (summed in fp32, rounded once to param_type)
+ * dh is the gradient that reaches h itself, past the norm (NULL: none).  dx is
+ * the gradient of x and of residual alike.  dgamma NULL: not computed.  dx may be
+ * dy, dh or h (same leading dimension).  M == 0 writes dgamma = 0.
+ * Requirements as the norm's.  Workspace when dgamma is given:
+ * igc_rms_norm_backward_workspace_bytes (-1 for bad or refused sizes).
+ */
+igc_status_t rms_norm_backward_bf16(int64_t M, int64_t C, const void *h, int64_t ldh, const void *gamma,
+                                    igc_out_t param_type, const float *rstd, const void *dy, int64_t lddy,
+                                    const void *dh, int64_t lddh, void *dx, int64_t lddx, void *dgamma,
+                                    igc_stream_t stream);
+igc_status_t rms_norm_backward_fp16(int64_t M, int64_t C, const void *h, int64_t ldh, const void *gamma,
+                                    igc_out_t param_type, const float *rstd, const void *dy, int64_t lddy,
+                                    const void *dh, int64_t lddh, void *dx, int64_t lddx, void *dgamma,
+                                    igc_stream_t stream);
+igc_status_t rms_norm_backward_bf16_ex(int64_t M, int64_t C, const void *h, int64_t ldh, const void *gamma,
+                                       igc_out_t param_type, const float *rstd, const void *dy, int64_t lddy,
+                                       const void *dh, int64_t lddh, void *dx, int64_t lddx, void *dgamma,
+                                       void *workspace, int64_t workspace_bytes, igc_stream_t stream);
+igc_status_t rms_norm_backward_fp16_ex(int64_t M, int64_t C, const void *h, int64_t ldh, const void *gamma,
+                                       igc_out_t param_type, const float *rstd, const void *dy, int64_t lddy,
+                                       const void *dh, int64_t lddh, void *dx, int64_t lddx, void *dgamma,
+                                       void *workspace, int64_t workspace_bytes, igc_stream_t stream);
+int64_t igc_rms_norm_backward_workspace_bytes(int64_t M, int64_t C);
+
+/*
+ * Rows of an activation to 8 bits, the A of a following gemm_int8: with
+ * v = act(x) * gate (gate NULL: act(x)), M rows of C values,
+ *   scale[m] = max_c |v| / 127,  q = v / scale to the nearest integer, ties to even.
+ * v is taken in fp32.  Rows of zeros, infinities, NaN and tiny values as in
+ * rms_norm_int8_*, but that the scale of a row with an infinity (and no NaN) is
+ * infinite.  x and gate of one type; a gate beside x in the same rows (x's columns
+ * C and up) begins at a 16-byte multiple.  Requirements as the norm's.
+ */
+igc_status_t quantize_rows_int8_bf16(int64_t M, int64_t C, igc_act_t act, const void *x, int64_t ldx, const void *gate,
+                                     int64_t ldg, int8_t *q, int64_t ldq, float *scale, igc_stream_t stream);
+igc_status_t quantize_rows_int8_fp16(int64_t M, int64_t C, igc_act_t act, const void *x, int64_t ldx, const void *gate,
+                                     int64_t ldg, int8_t *q, int64_t ldq, float *scale, igc_stream_t stream);
 
 /* Workspace bytes a call needs for operation `op` with GEMM view M x N x K
  * (see each operation above) under `tune` (NULL: the built-in choice): 0 when
