@@ -220,25 +220,38 @@ struct EpiMatrix {
     }
 };
 
-// What a lane's eight columns bring: bias and, after a product of integers, scales.
-template <bool INT8>
-struct EpiColumns {
+// What the epilogue of a lane needs beside its sums: the bias of its eight
+// columns and, after a product of integers, their scales and those of the rows
+// of its accumulators, which are applied as they are staged.
+template <class C>
+struct EpiScales {
     float bias[8];
-    float sb[INT8 ? 8 : 1];
+    float sb[kInt8<C> ? 8 : 1], sa[kInt8<C> ? C::FM : 1];
+    // n0: the lane's first column; m0: its row of the sub-tile's first block row
     template <class E>
-    __device__ __forceinline__ void load(const E& e, int64_t N, int64_t n0) {
+    __device__ __forceinline__ void load(const E& e, int64_t M, int64_t N, int64_t m0, int64_t n0) {
+        if constexpr (kInt8<C>) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) bias[i] = e.bias && n0 + i < N ? load_kind(e.bias, n0 + i, e.bias_kind) : 0.0f;
-        if constexpr (INT8) {
+            for (int i = 0; i < C::FM; ++i) sa[i] = e.sa && m0 + 16 * i < M ? e.sa[m0 + 16 * i] : 1.0f;
+            columns(e.sb, n0, KIND_F32, N, 1.0f, sb);
+        }
+        columns(e.bias, n0, e.bias_kind, N, 0.0f, bias);
+    }
+    // Eight values as 16-byte pieces where they lie so and are all there (the 8-bit product of 1024 x 1024 x 1024 with
+    // a bf16 bias 6.0 us, as without one; 6.6 where each value is asked for by itself).
+    __device__ __forceinline__ static void columns(const void* p, int64_t n0, int kind, int64_t N, float none, float (&v)[8]) {
+        if (p && (reinterpret_cast<uintptr_t>(p) & 15u) == 0 && n0 + 8 <= N) {
+            load8(p, n0, kind, 8, true, v);
+        } else {
 #pragma unroll
-            for (int i = 0; i < 8; ++i) sb[i] = e.sb && n0 + i < N ? e.sb[n0 + i] : 1.0f;
+            for (int i = 0; i < 8; ++i) v[i] = p && n0 + i < N ? load_kind(p, n0 + i, kind) : none;
         }
     }
 };
 
 template <class C, int I0, int NI, bool BWD, class ML, class E>
 __device__ __forceinline__ void epi_rows(ML& ml, const typename C::Acc (&acc)[C::FM][C::FN], IGC_LDS char* reg,
-                                         const Params& p, const E& e, const EpiColumns<kInt8<C>>& cv, int lane) {
+                                         const Params& p, const E& e, const EpiScales<C>& cv, int lane) {
     constexpr int RB = C::WTN * 4, CPR = RB / 16;
     constexpr int LPR = C::WTN / 8;  // lanes per row
     constexpr int RPI = 64 / LPR;    // rows per group
@@ -250,7 +263,14 @@ __device__ __forceinline__ void epi_rows(ML& ml, const typename C::Acc (&acc)[C:
 #pragma unroll
         for (int j = 0; j < C::FN; ++j) {
             const int row = 16 * i + (lane & 15), c = 4 * j + (lane >> 4);
-            *(IGC_LDS typename C::Acc*)(reg + row * RB + ((c ^ (row & (CPR - 1))) << 4)) = acc[I0 + i][j];
+            f32x4_t v;
+            if constexpr (kInt8<C>) {
+#pragma unroll
+                for (int q = 0; q < 4; ++q) v[q] = (float)acc[I0 + i][j][q] * cv.sa[I0 + i];
+            } else {
+                v = acc[I0 + i][j];
+            }
+            *(IGC_LDS f32x4_t*)(reg + row * RB + ((c ^ (row & (CPR - 1))) << 4)) = v;
         }
     const int row0 = lane / LPR, col = (lane % LPR) * 8;
     const int64_t m0 = ml.m0 + ml.wm * C::WTM + 16 * I0, n0 = ml.n0 + ml.wn * C::WTN;
@@ -263,17 +283,7 @@ __device__ __forceinline__ void epi_rows(ML& ml, const typename C::Acc (&acc)[C:
     const bool res_raw = e.res && e.res_kind != KIND_F32;
     const bool pre_raw = BWD && e.pre && e.pre_kind != KIND_F32;
     u32x4s_t rv[UQ], gv[UQ];
-    [[maybe_unused]] float av[UQ];  // the rows' scales
-    [[maybe_unused]] __amdgpu_buffer_rsrc_t sa;
-    if constexpr (kInt8<C>) sa = make_rsrc_u(e.sa ? (const char*)(e.sa + m0) : (const char*)p.C);
     auto fetch = [&](int q) __attribute__((always_inline)) {
-        if constexpr (kInt8<C>) {
-#pragma unroll
-            for (int u = 0; u < UQ; ++u)
-                av[u] = e.sa ? __builtin_bit_cast(float, __builtin_amdgcn_raw_buffer_load_b32(
-                                                             sa, (q + u) * RPI < rows ? (row0 + (q + u) * RPI) * 4 : kOob, 0, 0))
-                             : 1.0f;
-        }
         if (res_raw) {
 #pragma unroll
             for (int u = 0; u < UQ; ++u) rv[u] = res.load(q + u, (q + u) * RPI < rows, 0);
@@ -295,13 +305,13 @@ __device__ __forceinline__ void epi_rows(ML& ml, const typename C::Acc (&acc)[C:
 #pragma unroll
         for (int u = 0; u < UQ; ++u) {
             const int row = (q0 + u) * RPI + row0, c = col / 4, x = row & (CPR - 1);
-            const typename C::Acc lo = *(const IGC_LDS typename C::Acc*)(reg + row * RB + ((c ^ x) << 4));
-            const typename C::Acc hi = *(const IGC_LDS typename C::Acc*)(reg + row * RB + (((c + 1) ^ x) << 4));
+            const f32x4_t lo = *(const IGC_LDS f32x4_t*)(reg + row * RB + ((c ^ x) << 4));
+            const f32x4_t hi = *(const IGC_LDS f32x4_t*)(reg + row * RB + (((c + 1) ^ x) << 4));
             if constexpr (kInt8<C>) {
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    v[u][i] = __builtin_fmaf((float)lo[i] * av[u], cv.sb[i], cv.bias[i]);
-                    v[u][4 + i] = __builtin_fmaf((float)hi[i] * av[u], cv.sb[4 + i], cv.bias[4 + i]);
+                    v[u][i] = __builtin_fmaf(lo[i], cv.sb[i], cv.bias[i]);
+                    v[u][4 + i] = __builtin_fmaf(hi[i], cv.sb[4 + i], cv.bias[4 + i]);
                 }
             } else {
 #pragma unroll
@@ -363,7 +373,7 @@ __device__ __forceinline__ void epi_rows(ML& ml, const typename C::Acc (&acc)[C:
 // Every pass of a wave's sub-tile, at most four block rows each.
 template <class C, int I0, bool BWD, class ML, class E>
 __device__ __forceinline__ void epi_passes(ML& ml, const typename C::Acc (&acc)[C::FM][C::FN], IGC_LDS char* reg,
-                                           const Params& p, const E& e, const EpiColumns<kInt8<C>>& cv, int lane) {
+                                           const Params& p, const E& e, const EpiScales<C>& cv, int lane) {
     if constexpr (I0 < C::FM) {
         constexpr int NI = C::FM - I0 < 4 ? C::FM - I0 : 4;
         epi_rows<C, I0, NI, BWD>(ml, acc, reg, p, e, cv, lane);
@@ -430,18 +440,21 @@ __device__ __forceinline__ void epi_tile(const Params& p, const E& e) {
     const int id = xcd_order((int)blockIdx.x, p.tiles_m * p.tiles_n);
     int tm, tn;
     group_coords(id, p.tiles_m, p.tiles_n, p.group_m, tm, tn);
-    EpiColumns<kInt8<C>> cv;
+    EpiScales<C> cv;
     // The bias of tiles of up to 128 x 128 waits for nothing if it is asked for before the K loop (1000 x 500 x 250
     // 5.96 and 5.80 us, 1024 x 1024 x 1024 7.53 and 7.38); larger ones have no registers to keep it in.
     constexpr bool EARLY = C::BM * C::BN <= 128 * 128;
-    if constexpr (EARLY)
-        cv.load(e, p.N,
-                (int64_t)tn * C::BN + (int)(threadIdx.x >> 6) % C::WN * C::WTN + ((int)threadIdx.x & 63) % (C::WTN / 8) * 8);
+    if constexpr (EARLY) {
+        const int wave = (int)(threadIdx.x >> 6), l = (int)threadIdx.x & 63;
+        cv.load(e, p.M, p.N, (int64_t)tm * C::BM + wave / C::WN * C::WTM + (l & 15),
+                (int64_t)tn * C::BN + wave % C::WN * C::WTN + l % (C::WTN / 8) * 8);
+    }
     run_tile<C, V>(p, tm, tn, 0, p.K, [&](auto& ml, auto& acc) __attribute__((always_inline)) {
         // opaque copy of the lane: nothing derived from it is computed before, and kept through, the K loop
         int lane = ml.lane;
         asm volatile("" : "+v"(lane));
-        if constexpr (!EARLY) cv.load(e, p.N, ml.n0 + ml.wn * C::WTN + (lane % (C::WTN / 8)) * 8);
+        if constexpr (!EARLY)
+            cv.load(e, p.M, p.N, ml.m0 + ml.wm * C::WTM + (lane & 15), ml.n0 + ml.wn * C::WTN + (lane % (C::WTN / 8)) * 8);
         if constexpr (C::OPK == OP_GEMM)
             if (p.k_ragged8) add_k_tail<C>(p, ml, acc, lane);
         ring_barrier();  // every wave has finished reading the ring

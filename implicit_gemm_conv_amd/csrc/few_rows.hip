@@ -281,8 +281,16 @@ FewRowsPlan few_rows_plan(int64_t M, int64_t N, int64_t K, bool b_kc) {
     return pl;
 }
 
-// 8-bit operands: the bytes of a bf16 product of half the K.
-bool few_rows_int8_faster(int64_t M, int64_t N, int64_t K) { return few_rows_faster(M, N, (K + 1) / 2, true); }
+// 8-bit operands, against the tiles (here / there, us; * weights from memory, the others from the last-level cache):
+//   1 row: 4096 x 4096 5.9 / 9.6, 8192 x 2048 5.9 / 7.2, 2048 x 8192 7.6 / 9.8, 16384 x 4096* 16.1 / 18.4;
+//   16 rows: 4096 x 4096 7.2 / 9.7, 8192 x 2048 7.2 / 7.3, 2048 x 8192 10.2 / 10.1, 12000 x 3001 9.3 / 10.2,
+//   16384 x 4096* 19.8 / 19.0;  32 rows, whose A each workgroup reads twice as much of: 4096 x 4096 9.0 / 9.8,
+//   4096 x 1024 4.4 / 4.9, 1024 x 4096 8.0 / 8.1, 8192 x 2048 9.1 / 7.4, 2048 x 8192 13.9 / 10.5.
+bool few_rows_int8_faster(int64_t M, int64_t N, int64_t K) {
+    if (M <= 8) return true;
+    return M <= 16 ? N <= 12288 && K <= 8192 : N <= 4096 && K <= 4096;
+}
+// (K is cut as that of a bf16 product with as many bytes)
 FewRowsPlan few_rows_int8_plan(int64_t M, int64_t N, int64_t K) {
     FewRowsPlan pl = few_rows_plan(M, N, (K + 1) / 2, true);
     pl.per *= 2;  // (splits of K stay: per was rounded up to 128 of 16 bits)
@@ -292,9 +300,10 @@ FewRowsPlan few_rows_int8_plan(int64_t M, int64_t N, int64_t K) {
 template <int IN, bool B_KC, int MT, int NB>
 static hipError_t go(const FewRowsArgs& a, const FewRowsEpi<IN == FEW_INT8>& e, hipStream_t stream) {
     // Eight waves; sixteen for B row-major where 128 registers hold their operands, whose smaller turns spread
-    // better (17 x 8192 x 2048 12.3 -> 11.1 us).  A turn holds 32 KB of B a workgroup (column-major) or 64 KB.
+    // better (17 x 8192 x 2048 12.3 -> 11.1 us).  A turn holds 32 KB of B a workgroup (column-major; 16 KB of 8 bits,
+    // whose K is half as many steps: 12000 x 3001 11.6 -> 8.5 us, elsewhere the same) or 64 KB.
     constexpr int W = !B_KC && NB <= 4 ? 16 : 8;
-    constexpr int U = B_KC ? 4 : (W == 16 ? 4 / NB : 8 / NB);
+    constexpr int U = IN == FEW_INT8 ? 2 : (B_KC ? 4 : (W == 16 ? 4 / NB : 8 / NB));
     hipLaunchKernelGGL((few_rows_kernel<IN, B_KC, MT, NB, W, U>), dim3((unsigned)(a.cols * a.splits)), dim3(64 * W), 0,
                        stream, a, e);
     return hipGetLastError();

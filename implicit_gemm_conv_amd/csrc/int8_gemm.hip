@@ -37,6 +37,43 @@ static const Int8Instance* find_int8(const igc_tune_t& q) {
 // |A[m][k] B[n][k]| <= 2^14: a sum of fewer than 2^17 of them stays inside 32 bits.
 constexpr int64_t kMaxK = (1ll << 17) - 1;
 
+// The cheapest tile and K split by what they cost, in us: launch, first loads
+// and epilogue; a K tile of 128 values, whose time grows with what all busy CUs
+// load for it; a further round; for a split a second launch and the partials
+// twice through memory.  Fitted to 62 shapes with every tile and up to 16 parts,
+// where the choice takes 1.5% more than the best of them all (geometric mean);
+// that of the 16-bit products for half of K takes 2.2% more, and up to 21%
+// (1500 x 3000 x 700 17.9 us, here 14.7; 6539 x 669 x 1040 19.7 and 16.3).
+static igc_tune_t int8_tune(int64_t M, int64_t N, int64_t K) {
+    constexpr struct {
+        int bm, bn, depth, half;
+        double fixed, step, round;
+    } kinds[] = {{64, 64, 4, 0, 4.65, 0.14, 1.4},
+                 {64, 128, 4, 0, 5.2, 0.20, 3.1},
+                 {128, 128, 4, 0, 6.5, 0.26, 4.5},
+                 {256, 128, 3, 0, 8.6, 0.42, 7.4},
+                 {256, 256, 2, 1, 13.7, 0.90, 13.2}};
+    constexpr double kLoad = 0.0087;  // us for each KB of a K tile with every CU busy
+    igc_tune_t t = {};
+    double best = -1;
+    for (const auto& q : kinds) {
+        const int64_t tiles = ((M + q.bm - 1) / q.bm) * ((N + q.bn - 1) / q.bn), steps = (K + 127) / 128;
+        const double kb = ((double)(M < q.bm ? M : q.bm) + (double)(N < q.bn ? N : q.bn)) * 128.0 / 1024.0;
+        for (int64_t s = 1; s <= 16 && (s == 1 || (K / s >= 512 && tiles * s <= 256 && q.bm * q.bn <= 256 * 128)); ++s) {
+            const int64_t work = tiles * s, rounds = (work + 255) / 256;
+            const double last = (double)(work - (rounds - 1) * 256) / 256.0;  // of the CUs
+            double cost = q.fixed + (double)(rounds - 1) * q.round +
+                          (double)((steps + s - 1) / s) * (q.step * (double)rounds + kb * kLoad * ((double)(rounds - 1) + last));
+            if (s > 1) cost += 2.6 + (double)s * (0.025 + (double)M * (double)N * 8.0 / 5.4e6);
+            if (best < 0 || cost < best) {
+                best = cost;
+                t = igc_tune_t{q.bm, q.bn, 64, q.depth, 8, 16, q.half, 4, s > 1 ? (int)s : 0, 0, 0, 0};
+            }
+        }
+    }
+    return t;
+}
+
 struct Int8Plan {
     igc_tune_t tune = {};
     const Int8Instance* inst = nullptr;
@@ -57,7 +94,7 @@ static Int8Plan plan_of(const igc_tune_t* tune, int64_t M, int64_t N, int64_t K)
         pl.bytes = pl.rows.splits > 1 ? round_up(pl.rows.splits * M * pl.ldws * 4, 256) : 0;
         return pl;
     }
-    pl.tune = tune ? *tune : epilogue_tune(M, N, (K + 1) / 2, IGC_OP_GEMM, true);
+    pl.tune = tune ? *tune : int8_tune(M, N, K);
     pl.inst = find_int8(pl.tune);
     pl.valid = pl.tune.stream_k >= 0 && pl.tune.sk_hybrid == 0 && !(pl.tune.k_splits > 1 && pl.tune.stream_k > 0);
     if (!pl.inst || pl.tune.k_splits <= 1 || pairs == 0) return pl;

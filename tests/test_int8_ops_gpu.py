@@ -150,7 +150,8 @@ def test_product_in_parts(cfg, M, N, K, splits):
     assert torch.equal(D[:M, :N], whole[:M, :N])
 
 
-@pytest.mark.parametrize("M,N,K", [(1, 40, 30000), (5, 300, 12345), (8, 1000, 16400), (20, 24, 4000), (32, 500, 4095)])
+@pytest.mark.parametrize("M,N,K", [(1, 40, 30000), (5, 300, 12345), (8, 1000, 16400), (20, 24, 4000), (32, 500, 4095),
+                                   (16, 130, 8191), (7, 12, 100003)])
 def test_product_of_few_rows(M, N, K):
     t = igc.igc_gemm_int8_default_tune(M, N, K)
     assert t.bm == 0, "the kernel of few rows"
