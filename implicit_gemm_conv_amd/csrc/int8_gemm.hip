@@ -207,7 +207,7 @@ static igc_status_t int8_any(int64_t M, int64_t N, int64_t K, const int8_t* A, i
         (split && !launchable((M * ((N + 7) / 8) + 255) / 256, 256)) ||
         (!split && (span(ldd, (int)dt) || (e.res && span(e.ldr, e.res_kind)) || (e.pre && span(e.ldp, e.pre_kind)))))
         return IGC_ERR_UNSUPPORTED;
-    const void* fn = split ? pl.inst->part : pl.inst->fn;
+    const void* fn = split ? pl.inst->part : (e.act == ACT_NONE && !e.pre ? pl.inst->lean : pl.inst->fn);
     if (!fn) return IGC_ERR_UNSUPPORTED;
     Workspace ws;
     if (const igc_status_t st = ws.take(pl.bytes, user_ws, user_ws_bytes, stream)) return st;

@@ -7,6 +7,7 @@ namespace igc {
 struct Int8Instance {
     Instance tile;     // the configuration; its K tile of bk counts pairs of values
     const void* fn;    // whole products
+    const void* lean;  // those without activation and kept pre-activation
     const void* part;  // one part of a K split, for the epilogue to follow
 };
 

@@ -22,9 +22,9 @@ struct Int8Cfg : Cfg<false, BM, BN, BK, D, NW, MI, HALF, NL, SYNC, true, true, O
 using Here = Int8Cfg<IGC_BM, IGC_BN, IGC_BK, IGC_D, IGC_W, IGC_MI, IGC_HALF, IGC_LW, IGC_SYNC>;
 static_assert(kInt8<Here> && Here::MI == 16, "the integer instruction is 16x16x64");
 
-template <class C>
+template <class C, int PATH>
 __global__ __launch_bounds__(C::NT) void gemm_int8_kernel(const Params p, const EpiInt8 e) {
-    epi_tile<C, PLAIN, false>(p, e);
+    epi_tile<C, PLAIN, false, PATH>(p, e);
 }
 
 template <class C>
@@ -40,7 +40,8 @@ struct Registrar {
     Registrar() {
         register_int8(Int8Instance{Instance{IGC_BM, IGC_BN, IGC_BK, IGC_D, IGC_W, IGC_MI, IGC_HALF, Here::NL, IGC_SYNC,
                                             OP_GEMM, false, true, true, true, {}, {}, Here::LDS_BYTES},
-                                   reinterpret_cast<const void*>(&gemm_int8_kernel<Here>), part_of<Here>()});
+                                   reinterpret_cast<const void*>(&gemm_int8_kernel<Here, EPI_ALL>),
+                                   reinterpret_cast<const void*>(&gemm_int8_kernel<Here, EPI_LEAN>), part_of<Here>()});
     }
 };
 const Registrar registrar;
