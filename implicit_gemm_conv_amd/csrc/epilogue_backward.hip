@@ -104,28 +104,33 @@ __global__ __launch_bounds__(THREADS) void epilogue_backward_kernel(const BackAr
     }
 }
 
-// dbias = the chunks' partial sums: 32 columns by 16 chunk lanes a workgroup.
-constexpr int kSumLanes = 16;
-__global__ __launch_bounds__(32 * kSumLanes) void column_sum_kernel(const float* part, int64_t N, int chunks, void* out,
-                                                                    int kind) {
-    __shared__ float red[kSumLanes][32];
+// Sums of the chunks' partial sums: 32 columns by LANES chunk lanes a workgroup, U loads of a lane in flight.
+template <int LANES, int U>
+__global__ __launch_bounds__(32 * LANES) void column_sum_kernel(const float* part, int64_t N, int chunks, void* out,
+                                                                int kind) {
+    __shared__ float red[LANES][32];
     const int c = (int)threadIdx.x & 31, l = (int)threadIdx.x >> 5;
     const int64_t n = (int64_t)blockIdx.x * 32 + c;
     float s = 0.0f;
     if (n < N) {
-#pragma unroll 4
-        for (int k = l; k < chunks; k += kSumLanes) s += part[(int64_t)k * N + n];
+#pragma unroll U
+        for (int k = l; k < chunks; k += LANES) s += part[(int64_t)k * N + n];
     }
     red[l][c] = s;
     __syncthreads();
     if (l == 0 && n < N) {
 #pragma unroll
-        for (int k = 1; k < kSumLanes; ++k) s += red[k][c];
+        for (int k = 1; k < LANES; ++k) s += red[k][c];
         store_kind(out, n, kind, s);
     }
 }
+static hipError_t launch_dbias_sum(const float* part, int64_t N, int chunks, void* out, int kind, hipStream_t stream) {
+    hipLaunchKernelGGL((column_sum_kernel<16, 4>), dim3((unsigned)((N + 31) / 32)), dim3(512), 0, stream, part, N, chunks,
+                       out, kind);
+    return hipGetLastError();
+}
 hipError_t launch_column_sum(const float* part, int64_t N, int chunks, void* out, int kind, hipStream_t stream) {
-    hipLaunchKernelGGL(column_sum_kernel, dim3((unsigned)((N + 31) / 32)), dim3(32 * kSumLanes), 0, stream, part, N, chunks,
+    hipLaunchKernelGGL((column_sum_kernel<32, 8>), dim3((unsigned)((N + 31) / 32)), dim3(1024), 0, stream, part, N, chunks,
                        out, kind);
     return hipGetLastError();
 }
@@ -220,7 +225,7 @@ static igc_status_t backward_any(bool fp16, int64_t M, int64_t N, igc_act_t act,
         hipLaunchKernelGGL((epilogue_backward_kernel<false, kBackThreads>), grid, dim3(kBackThreads), 0, stream, a);
     hipError_t e = hipGetLastError();
     if (e == hipSuccess && dbias && pl.chunks > 1)
-        e = launch_column_sum(a.part, N, pl.chunks, dbias, (int)bias_type, stream);
+        e = launch_dbias_sum(a.part, N, pl.chunks, dbias, (int)bias_type, stream);
     return e == hipSuccess ? IGC_OK : IGC_ERR_HIP;
 }
 

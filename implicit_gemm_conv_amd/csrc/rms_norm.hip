@@ -354,52 +354,85 @@ __global__ __launch_bounds__(1024) void quantize_rows_long_kernel(const RowArgs 
 
 // ---- gradient of the norm ------------------------------------------------------------------------------------------
 
+// gamma of a workgroup's columns, which every row needs: in registers, or, of rows so wide that it would spill beside
+// their values and sums, in LDS (2048 x 16384: 90 and 67 us).
+template <int T, int V>
+struct RowGamma {
+    static constexpr bool kLds = T * V > 1024;
+    float reg[kLds ? 1 : V][8];
+    IGC_LDS f32x4s_t* lds;
+    // one row a workgroup (kLds): a thread writes what it reads, so nothing waits for another
+    __device__ __forceinline__ void load(const RowArgs& a, int t) {
+        if constexpr (kLds) {
+            __shared__ f32x4s_t store[2 * V * T];
+            lds = (IGC_LDS f32x4s_t*)store + t;
+        }
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+            const int c = (v * T + t) * 8;
+            if constexpr (kLds) {
+                float g[8];
+                load_gamma(a, c, a.C - c, g);
+                lds[2 * v * T] = f32x4s_t{g[0], g[1], g[2], g[3]};
+                lds[(2 * v + 1) * T] = f32x4s_t{g[4], g[5], g[6], g[7]};
+            } else {
+                load_gamma(a, c, a.C - c, reg[v]);
+            }
+        }
+    }
+    __device__ __forceinline__ void get(int v, float (&g)[8]) const {
+        if constexpr (kLds) {
+            const f32x4s_t lo = lds[2 * v * T], hi = lds[(2 * v + 1) * T];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) g[i] = lo[i], g[4 + i] = hi[i];
+        } else {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) g[i] = reg[v][i];
+        }
+    }
+};
+
 // The workgroups take rows in turn and keep their sums for dgamma in registers; at the end each writes them out, and
-// column_sum adds the workgroups' (or, of a single workgroup, they are dgamma).
+// column_sum adds the workgroups' (or, of a single workgroup, they are dgamma).  Other workgroups of the CU, not loads of
+// a next row, cover a row's loads (asking for it ahead measured the same).
 template <bool F16, int T, int V>
 __global__ __launch_bounds__(kRowThreads<T>) void rms_norm_backward_kernel(const RowArgs a) {
     constexpr int BT = kRowThreads<T>, R = BT / T;
+    static_assert(R == 1 || !RowGamma<T, V>::kLds, "wide rows are one to a workgroup");
     __shared__ float red[2][BT / 64][2];
     __shared__ float cols[R > 1 ? R : 1][R > 1 ? T * V * 8 : 1];
     const int t = (int)threadIdx.x % T, rl = (int)threadIdx.x / T;
     const int64_t step = (int64_t)gridDim.x * R;
-    float g[V][8], dg[V][8];
+    RowGamma<T, V> gamma;
+    gamma.load(a, t);
+    float dg[V][8];
 #pragma unroll
-    for (int v = 0; v < V; ++v) {
-        const int c = (v * T + t) * 8;
-        load_gamma(a, c, a.C - c, g[v]);
+    for (int v = 0; v < V; ++v)
 #pragma unroll
         for (int i = 0; i < 8; ++i) dg[v][i] = 0.0f;
-    }
-    u32x4s_t h[V], dy[V], dh[V], nh[V], ndy[V], ndh[V];
-    float rs = 0.0f, nrs = 0.0f;
-    const auto load = [&](int64_t row, u32x4s_t (&ph)[V], u32x4s_t (&pdy)[V], u32x4s_t (&pdh)[V], float& prs)
-                          __attribute__((always_inline)) {
+    int odd = 0;
+    for (int64_t base = (int64_t)blockIdx.x * R; base < a.M; base += step) {
+        const int64_t row = base + rl;
         const bool in = row < a.M;
-        prs = in ? a.rstd[row] : 0.0f;
+        const float rs = in ? a.rstd[row] : 0.0f;
+        u32x4s_t h[V], dy[V], dh[V];
 #pragma unroll
         for (int v = 0; v < V; ++v) {
             const int c = (v * T + t) * 8, left = in ? a.C - c : 0;
-            ph[v] = load_piece(a.x, row * a.ldx + c, left);
-            pdy[v] = load_piece(a.dy, row * a.lddy + c, left);
-            if (a.res) pdh[v] = load_piece(a.res, row * a.ldr + c, left);
+            h[v] = load_piece(a.x, row * a.ldx + c, left);
+            dy[v] = load_piece(a.dy, row * a.lddy + c, left);
+            if (a.res) dh[v] = load_piece(a.res, row * a.ldr + c, left);
         }
-    };
-    int odd = 0;
-    int64_t base = (int64_t)blockIdx.x * R;
-    if (base < a.M) load(base + rl, h, dy, dh, rs);
-    for (; base < a.M; base += step) {
-        const int64_t row = base + rl;
-        if (base + step < a.M) load(row + step, nh, ndy, ndh, nrs);  // in flight while this row is joined
         float s = 0.0f;
 #pragma unroll
         for (int v = 0; v < V; ++v) {
-            float fh[8], fd[8];
+            float fh[8], fd[8], g[8];
+            gamma.get(v, g);
             unpack8<F16>(h[v], fh);
             unpack8<F16>(dy[v], fd);
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
-                s = __builtin_fmaf(fd[i] * g[v][i], fh[i], s);
+                s = __builtin_fmaf(fd[i] * g[i], fh[i], s);
                 dg[v][i] = __builtin_fmaf(fd[i], fh[i] * rs, dg[v][i]);
             }
         }
@@ -407,26 +440,23 @@ __global__ __launch_bounds__(kRowThreads<T>) void rms_norm_backward_kernel(const
         row_reduce<T>(s, none, red[odd]);  // (two sets of sums in turn: one barrier a row)
         odd ^= 1;
         const float k = s / (float)a.C * rs * rs;  // xh mean(g xh) = h k
-        if (row < a.M) {
+        if (!in) continue;
 #pragma unroll
-            for (int v = 0; v < V; ++v) {
-                const int c = (v * T + t) * 8;
-                float fh[8], fd[8];
-                unpack8<F16>(h[v], fh);
-                unpack8<F16>(dy[v], fd);
+        for (int v = 0; v < V; ++v) {
+            const int c = (v * T + t) * 8;
+            float fh[8], fd[8], g[8];
+            gamma.get(v, g);
+            unpack8<F16>(h[v], fh);
+            unpack8<F16>(dy[v], fd);
 #pragma unroll
-                for (int i = 0; i < 8; ++i) fd[i] = rs * __builtin_fmaf(-k, fh[i], fd[i] * g[v][i]);
-                if (a.res) {
-                    unpack8<F16>(dh[v], fh);
+            for (int i = 0; i < 8; ++i) fd[i] = rs * __builtin_fmaf(-k, fh[i], fd[i] * g[i]);
+            if (a.res) {
+                unpack8<F16>(dh[v], fh);
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) fd[i] += fh[i];
-                }
-                store_piece<F16>(a.y, row * a.ldy + c, a.C - c, fd);
+                for (int i = 0; i < 8; ++i) fd[i] += fh[i];
             }
+            store_piece<F16>(a.y, row * a.ldy + c, a.C - c, fd);
         }
-#pragma unroll
-        for (int v = 0; v < V; ++v) h[v] = nh[v], dy[v] = ndy[v], dh[v] = ndh[v];
-        rs = nrs;
     }
     if (!a.dgamma) return;
     if constexpr (R > 1) {
@@ -456,29 +486,44 @@ __global__ __launch_bounds__(kRowThreads<T>) void rms_norm_backward_kernel(const
     }
 }
 
-// Long rows: each read twice, and the sums for dgamma kept in the workgroup's part of the workspace, where a thread
-// adds to its own columns alone.
-template <bool F16>
+// Long rows: each read twice.  The sums for dgamma, of which a thread adds to its own columns alone, are in LDS where
+// 128 KB hold them (SUMS: C <= 32768), otherwise in the workgroup's part of the workspace, which takes them at the end.
+template <bool F16, bool SUMS>
 __global__ __launch_bounds__(1024) void rms_norm_backward_long_kernel(const RowArgs a) {
     __shared__ float red[2][16][2];
+    __shared__ f32x4s_t sums[SUMS ? 8192 : 1];
     float* part = a.part ? a.part + (int64_t)blockIdx.x * a.C : nullptr;
+    if constexpr (SUMS) {
+        for (int k = 0; k < 8; ++k) sums[k * 1024 + (int)threadIdx.x] = f32x4s_t{0, 0, 0, 0};
+    }
     int odd = 0;
     bool first = true;
     for (int64_t row = blockIdx.x; row < a.M; row += gridDim.x) {
         const float rs = a.rstd[row];
         float s = 0.0f;
-        for (int c = (int)threadIdx.x * 8; c < a.C; c += 8192) {
+        int k = (int)threadIdx.x;
+        for (int c = (int)threadIdx.x * 8; c < a.C; c += 8192, k += 2048) {
             float fh[8], fd[8], g[8];
             unpack8<F16>(load_piece(a.x, row * a.ldx + c, a.C - c), fh);
             unpack8<F16>(load_piece(a.dy, row * a.lddy + c, a.C - c), fd);
             load_gamma(a, c, a.C - c, g);
+            if constexpr (SUMS) {
+                f32x4s_t lo = sums[k], hi = sums[k + 1024];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    lo[i] = __builtin_fmaf(fd[i], fh[i] * rs, lo[i]);
+                    hi[i] = __builtin_fmaf(fd[4 + i], fh[4 + i] * rs, hi[i]);
+                }
+                sums[k] = lo;
+                sums[k + 1024] = hi;
+            }
 #pragma unroll
             for (int i = 0; i < 8; ++i) s = __builtin_fmaf(fd[i] * g[i], fh[i], s);
         }
         unsigned none = 0;
         row_reduce<1024>(s, none, red[odd]);
         odd ^= 1;
-        const float k = s / (float)a.C * rs * rs;
+        const float m = s / (float)a.C * rs * rs;
         for (int c = (int)threadIdx.x * 8; c < a.C; c += 8192) {
             const int left = a.C - c;
             float fh[8], fd[8], g[8], dx[8];
@@ -486,7 +531,7 @@ __global__ __launch_bounds__(1024) void rms_norm_backward_long_kernel(const RowA
             unpack8<F16>(load_piece(a.dy, row * a.lddy + c, left), fd);
             load_gamma(a, c, left, g);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) dx[i] = rs * __builtin_fmaf(-k, fh[i], fd[i] * g[i]);
+            for (int i = 0; i < 8; ++i) dx[i] = rs * __builtin_fmaf(-m, fh[i], fd[i] * g[i]);
             if (a.res) {
                 float f[8];
                 unpack8<F16>(load_piece(a.res, row * a.ldr + c, left), f);
@@ -494,13 +539,23 @@ __global__ __launch_bounds__(1024) void rms_norm_backward_long_kernel(const RowA
                 for (int i = 0; i < 8; ++i) dx[i] += f[i];
             }
             store_piece<F16>(a.y, row * a.ldy + c, left, dx);
-            if (part) {
+            if (!SUMS && part) {
 #pragma unroll
                 for (int i = 0; i < 8; ++i)
                     if (i < left) part[c + i] = __builtin_fmaf(fd[i], fh[i] * rs, first ? 0.0f : part[c + i]);
             }
         }
         first = false;
+    }
+    if constexpr (SUMS) {
+        if (!part) return;
+        int k = (int)threadIdx.x;
+        for (int c = (int)threadIdx.x * 8; c < a.C; c += 8192, k += 2048) {
+            const f32x4s_t lo = sums[k], hi = sums[k + 1024];
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                if (c + i < a.C) part[c + i] = i < 4 ? lo[i & 3] : hi[i & 3];
+        }
     }
 }
 
@@ -512,22 +567,27 @@ struct RowShape {
     int threads() const { return T == 0 ? 1024 : (T < 256 ? 256 : T); }
     int rows() const { return T == 0 ? 1 : threads() / T; }
 };
-static RowShape row_shape(int64_t M, int64_t C, bool backward = false) {
+// Measured (many rows; us): norm 8192 x 4096 (512, 1) 48 and (256, 2) 52, to 8 bits 45 and 47, rows to 8 bits 32.2 and
+// 31.0; norm 4096 x 8192 (512, 2) 54, to 8 bits 48.5, (1024, 1) 52 and 50; gradient 8192 x 4096 (512, 1) 57, (256, 2) 60,
+// 4096 x 8192 (512, 2) 59, (1024, 1) 62.  A single row is fastest with one vector a thread: norm of 8192 values (1024, 1)
+// 4.0, (512, 2) 4.3, of 4096 (512, 1) 3.6, (256, 2) 4.0.
+enum RowOp : int { ROW_NORM = 0, ROW_QUANTIZE = 1, ROW_BACKWARD = 2 };
+static RowShape row_shape(int64_t M, int64_t C, RowOp op) {
     const int64_t n = (C + 7) / 8;
     if (n <= 16) return {16, 1};
     if (n <= 64) return {64, 1};
     if (n <= 128) return {128, 1};
     if (n <= 256) return {256, 1};
-    if (n <= 512) return M < 512 ? RowShape{512, 1} : RowShape{256, 2};
-    if (n <= 1024) return M < 512 ? RowShape{1024, 1} : RowShape{512, 2};
+    if (n <= 512) return op == ROW_QUANTIZE && M >= 512 ? RowShape{256, 2} : RowShape{512, 1};
+    if (n <= 1024) return op != ROW_BACKWARD && M < 512 ? RowShape{1024, 1} : RowShape{512, 2};
     if (n <= 2048) return {1024, 2};
-    if (n <= 4096 && !backward) return {1024, 4};  // (the backward pass has no registers for four vectors)
+    if (n <= 4096 && op != ROW_BACKWARD) return {1024, 4};  // (the backward pass has no registers for it)
     return {0, 0};
 }
 
-#define IGC_BACK_SHAPES(X) X(16, 1) X(64, 1) X(128, 1) X(256, 1) X(512, 1) X(256, 2) X(1024, 1) X(512, 2) X(1024, 2)
-#define IGC_ROW_SHAPES(X) IGC_BACK_SHAPES(X) X(1024, 4)
-
+#define IGC_ROW_SHAPES(X) \
+    X(16, 1) X(64, 1) X(128, 1) X(256, 1) X(512, 1) X(256, 2) X(1024, 1) X(512, 2) X(1024, 2) X(1024, 4)
+#define IGC_BACK_SHAPES(X) X(16, 1) X(64, 1) X(128, 1) X(256, 1) X(512, 1) X(512, 2) X(1024, 2)
 template <bool F16, bool INT8>
 static void launch_norm(RowShape s, dim3 grid, hipStream_t st, const RowArgs& a) {
 #define IGC_ROW_CASE(TT, VV)                                                                                    \
@@ -559,7 +619,10 @@ static void launch_backward(RowShape s, dim3 grid, hipStream_t st, const RowArgs
     }
     IGC_BACK_SHAPES(IGC_ROW_CASE)
 #undef IGC_ROW_CASE
-    hipLaunchKernelGGL((rms_norm_backward_long_kernel<F16>), grid, dim3(1024), 0, st, a);
+    if (a.C <= 32768)
+        hipLaunchKernelGGL((rms_norm_backward_long_kernel<F16, true>), grid, dim3(1024), 0, st, a);
+    else
+        hipLaunchKernelGGL((rms_norm_backward_long_kernel<F16, false>), grid, dim3(1024), 0, st, a);
 }
 
 // Rows of `bytes` a value: INVALID without a pointer or with rows that overlap, MISALIGNED by the 16-byte rule.
@@ -590,7 +653,7 @@ static igc_status_t norm_any(bool fp16, bool int8, int64_t M, int64_t C, const v
     if (int8 && !scale) return IGC_ERR_INVALID_VALUE;
     if (misplaced(gamma, pt) || misplaced(scale, IGC_OUT_F32) || misplaced(rstd, IGC_OUT_F32)) return IGC_ERR_MISALIGNED;
     if (rows_too_large(M, C) || strides_too_large({ldx, res ? ldr : 0, h ? ldh : 0, ldy})) return IGC_ERR_UNSUPPORTED;
-    const RowShape s = row_shape(M, C);
+    const RowShape s = row_shape(M, C, ROW_NORM);
     const int64_t blocks = (M + s.rows() - 1) / s.rows();
     if (!launchable(blocks, s.threads())) return IGC_ERR_UNSUPPORTED;
     RowArgs a{};
@@ -635,7 +698,7 @@ static igc_status_t quantize_any(bool fp16, int64_t M, int64_t C, igc_act_t act,
     if (!scale) return IGC_ERR_INVALID_VALUE;
     if (misplaced(scale, IGC_OUT_F32)) return IGC_ERR_MISALIGNED;
     if (rows_too_large(M, C) || strides_too_large({ldx, gate ? ldg : 0, ldq})) return IGC_ERR_UNSUPPORTED;
-    const RowShape s = row_shape(M, C);
+    const RowShape s = row_shape(M, C, ROW_QUANTIZE);
     const int64_t blocks = (M + s.rows() - 1) / s.rows();
     if (!launchable(blocks, s.threads())) return IGC_ERR_UNSUPPORTED;
     RowArgs a{};
@@ -657,11 +720,14 @@ static igc_status_t quantize_any(bool fp16, int64_t M, int64_t C, igc_act_t act,
     return hipGetLastError() == hipSuccess ? IGC_OK : IGC_ERR_HIP;
 }
 
-// Workgroups of the backward pass: they take rows in turn, two for each CU (one of 1024 threads), so that the sums for
-// dgamma that they leave stay small beside the rows.
+// Workgroups of the backward pass, which take rows in turn: as many as the CUs hold and no more, at four rows' time
+// each or more where that leaves one for every CU, so that the sums for dgamma that they leave stay small beside the
+// rows (777 x 1001: 256 of them 9.0 us, 389 9.9; 512 x 2048: 256 8.9, 512 9.5; 8192 x 2048: 768 32.4, 512 34.6).
 static int64_t backward_groups(RowShape s, int64_t M) {
-    const int64_t most = s.threads() >= 1024 ? 256 : 512, blocks = (M + s.rows() - 1) / s.rows();
-    return blocks < most ? blocks : most;
+    const int64_t blocks = (M + s.rows() - 1) / s.rows();
+    const int64_t most = s.threads() >= 1024 || s.T * s.V > 512 ? 256 : (s.T == 512 ? 384 : (s.T == 256 ? 768 : 512));
+    const int64_t want = blocks / 4 < 256 ? 256 : (blocks / 4 < most ? blocks / 4 : most);
+    return blocks < want ? blocks : want;
 }
 static int64_t backward_bytes(RowShape s, int64_t M, int64_t C) {
     const int64_t g = backward_groups(s, M);
@@ -684,7 +750,7 @@ static igc_status_t backward_any(bool fp16, int64_t M, int64_t C, const void* h,
     }
     if (misplaced(gamma, pt) || misplaced(dgamma, pt) || misplaced(rstd, IGC_OUT_F32)) return IGC_ERR_MISALIGNED;
     if (rows_too_large(M, C) || (M > 0 && strides_too_large({ldh, lddy, dh ? lddh : 0, lddx}))) return IGC_ERR_UNSUPPORTED;
-    const RowShape s = row_shape(M, C, true);
+    const RowShape s = row_shape(M, C, ROW_BACKWARD);
     const int64_t groups = backward_groups(s, M);
     Workspace ws;
     if (const igc_status_t st = ws.take(dgamma && M > 0 ? backward_bytes(s, M, C) : 0, user_ws, user_ws_bytes, stream))
@@ -763,7 +829,7 @@ IGC_NORM(fp16, true)
 
 int64_t igc_rms_norm_backward_workspace_bytes(int64_t M, int64_t C) {
     if (M < 0 || C < 1 || rows_too_large(M, C)) return -1;
-    return M == 0 ? 0 : backward_bytes(row_shape(M, C, true), M, C);
+    return M == 0 ? 0 : backward_bytes(row_shape(M, C, ROW_BACKWARD), M, C);
 }
 
 }  // extern "C"
