@@ -39,32 +39,37 @@ constexpr int64_t kMaxK = (1ll << 17) - 1;
 
 // The cheapest tile and K split by what they cost, in us: launch, first loads
 // and epilogue; a K tile of 128 values, whose time grows with what all busy CUs
-// load for it; a further round; for a split a second launch and the partials
-// twice through memory.  Fitted to 62 shapes with every tile and up to 16 parts,
-// where the choice takes 1.5% more than the best of them all (geometric mean);
-// that of the 16-bit products for half of K takes 2.2% more, and up to 21%
-// (1500 x 3000 x 700 17.9 us, here 14.7; 6539 x 669 x 1040 19.7 and 16.3).
+// load for it, and by a quarter where rows of K values do not begin on whole
+// cache lines; a further round; for a split a second launch and the partials
+// twice through memory.  Fitted to 140 shapes whose K is a multiple of 128, with
+// every tile and up to 16 parts: the choice takes 0.4% more there than the best
+// of them all (geometric mean; 15% at most), and 1.0% on 147 others (25% at
+// most).  That of the 16-bit products for half of K takes 2.2% more, and up to
+// 21% (1500 x 3000 x 700 17.9 us against 14.7).
 static igc_tune_t int8_tune(int64_t M, int64_t N, int64_t K) {
     constexpr struct {
         int bm, bn, depth, half;
-        double fixed, step, round;
-    } kinds[] = {{64, 64, 4, 0, 4.65, 0.14, 1.4},
-                 {64, 128, 4, 0, 5.2, 0.20, 3.1},
-                 {128, 128, 4, 0, 6.5, 0.26, 4.5},
-                 {256, 128, 3, 0, 8.6, 0.42, 7.4},
-                 {256, 256, 2, 1, 13.7, 0.90, 13.2}};
-    constexpr double kLoad = 0.0087;  // us for each KB of a K tile with every CU busy
+        double fixed, round, least, step, load;  // load: for each KB of a K tile with every CU busy
+    } kinds[] = {{64, 64, 4, 0, 3.8, 0.85, 0.0, 0.15, 0.0037},
+                 {64, 128, 4, 0, 4.3, 2.3, 0.0, 0.20, 0.0042},
+                 {128, 128, 4, 0, 5.2, 3.5, 0.0, 0.25, 0.0065},
+                 {256, 128, 3, 0, 6.7, 5.1, 0.47, 0.28, 0.011},
+                 {256, 256, 2, 1, 11.1, 8.1, 0.87, 0.64, 0.0121}};
     igc_tune_t t = {};
     double best = -1;
     for (const auto& q : kinds) {
         const int64_t tiles = ((M + q.bm - 1) / q.bm) * ((N + q.bn - 1) / q.bn), steps = (K + 127) / 128;
         const double kb = ((double)(M < q.bm ? M : q.bm) + (double)(N < q.bn ? N : q.bn)) * 128.0 / 1024.0;
+        const auto step = [&](double busy) {
+            const double us = (q.step + kb * q.load * busy) * (K % 128 ? 1.25 : 1.0);
+            return us > q.least ? us : q.least;
+        };
         for (int64_t s = 1; s <= 16 && (s == 1 || (K / s >= 512 && tiles * s <= 256 && q.bm * q.bn <= 256 * 128)); ++s) {
             const int64_t work = tiles * s, rounds = (work + 255) / 256;
             const double last = (double)(work - (rounds - 1) * 256) / 256.0;  // of the CUs
             double cost = q.fixed + (double)(rounds - 1) * q.round +
-                          (double)((steps + s - 1) / s) * (q.step * (double)rounds + kb * kLoad * ((double)(rounds - 1) + last));
-            if (s > 1) cost += 2.6 + (double)s * (0.025 + (double)M * (double)N * 8.0 / 5.4e6);
+                          (double)((steps + s - 1) / s) * ((double)(rounds - 1) * step(1.0) + step(last));
+            if (s > 1) cost += 3.7 + (double)s * (double)M * (double)N * 8.0 / 5e6;
             if (best < 0 || cost < best) {
                 best = cost;
                 t = igc_tune_t{q.bm, q.bn, 64, q.depth, 8, 16, q.half, 4, s > 1 ? (int)s : 0, 0, 0, 0};
