@@ -83,11 +83,15 @@ struct Int8Plan {
     igc_tune_t tune = {};
     const Int8Instance* inst = nullptr;
     bool valid = true, few = false;
+    bool fits = true;         // a schedule that is compiled, in a grid that can be launched
     FewRowsPlan rows = {};
     int S = 1;                // K parts
     int64_t per = 0;          // pairs of K a part
     int64_t ldws = 0, bytes = 0;
 };
+
+// Sizes beyond these are refused before a schedule is looked for.
+static bool sizes_too_large(int64_t M, int64_t N, int64_t K) { return K > kMaxK || M >= (1ll << 31) || N >= (1ll << 31); }
 
 static Int8Plan plan_of(const igc_tune_t* tune, int64_t M, int64_t N, int64_t K) {
     Int8Plan pl;
@@ -95,6 +99,7 @@ static Int8Plan plan_of(const igc_tune_t* tune, int64_t M, int64_t N, int64_t K)
     if (!tune && M >= 1 && M <= kFewRows && few_rows_int8_faster(M, N, K)) {
         pl.few = true;
         pl.rows = few_rows_int8_plan(M, N, K);
+        pl.fits = N < (1ll << 30) && launchable(pl.rows.cols * pl.rows.splits, 512);
         pl.ldws = round_up(N, 4);
         pl.bytes = pl.rows.splits > 1 ? round_up(pl.rows.splits * M * pl.ldws * 4, 256) : 0;
         return pl;
@@ -102,13 +107,19 @@ static Int8Plan plan_of(const igc_tune_t* tune, int64_t M, int64_t N, int64_t K)
     pl.tune = tune ? *tune : int8_tune(M, N, K);
     pl.inst = find_int8(pl.tune);
     pl.valid = pl.tune.stream_k >= 0 && pl.tune.sk_hybrid == 0 && !(pl.tune.k_splits > 1 && pl.tune.stream_k > 0);
-    if (!pl.inst || pl.tune.k_splits <= 1 || pairs == 0) return pl;
-    // each part a whole number of ring periods
+    pl.fits = pl.inst && pl.tune.stream_k <= 0;
+    if (!pl.fits) return pl;
     const Instance& t = pl.inst->tile;
-    const int64_t unit = (int64_t)t.bk * Ring::period(Ring::units(t.d, t.half));
-    pl.per = round_up((pairs + pl.tune.k_splits - 1) / pl.tune.k_splits, unit);
-    pl.S = (int)((pairs + pl.per - 1) / pl.per);
-    if (pl.S > 1) {
+    if (pl.tune.k_splits > 1 && pairs > 0) {
+        // each part a whole number of ring periods
+        const int64_t unit = (int64_t)t.bk * Ring::period(Ring::units(t.d, t.half));
+        pl.per = round_up((pairs + pl.tune.k_splits - 1) / pl.tune.k_splits, unit);
+        pl.S = (int)((pairs + pl.per - 1) / pl.per);
+    }
+    const int64_t tiles = ((M + t.bm - 1) / t.bm) * ((N + t.bn - 1) / t.bn);
+    pl.fits = tiles <= 0x7fffffff && launchable(tiles * pl.S, 64 * t.waves);
+    if (pl.fits && pl.S > 1) {
+        pl.fits = pl.inst->part && launchable((M * ((N + 7) / 8) + 255) / 256, 256);
         pl.ldws = round_up(N, 4);
         pl.bytes = round_up((int64_t)pl.S * M * pl.ldws * 4, 256);
     }
@@ -156,10 +167,10 @@ static igc_status_t int8_any(int64_t M, int64_t N, int64_t K, const int8_t* A, i
     if (const igc_status_t st = check_epilogue(epi, N, e)) return st;
     e.sa = sa;
     e.sb = sb;
-    if (K > kMaxK || M >= (1ll << 40) || N >= (1ll << 40)) return IGC_ERR_UNSUPPORTED;
+    if (sizes_too_large(M, N, K)) return IGC_ERR_UNSUPPORTED;
     const Int8Plan pl = plan_of(tune, M, N, K);
     if (!pl.valid) return IGC_ERR_INVALID_VALUE;
-    if (!pl.few && (!pl.inst || pl.tune.stream_k > 0)) return IGC_ERR_UNSUPPORTED;
+    if (!pl.fits) return IGC_ERR_UNSUPPORTED;
     if (M == 0 || N == 0) return IGC_OK;
     if (!D || ldd < N) return IGC_ERR_INVALID_VALUE;
     if (K > 0) {
@@ -174,9 +185,7 @@ static igc_status_t int8_any(int64_t M, int64_t N, int64_t K, const int8_t* A, i
     constexpr int64_t kSpan = 0x7fff0000ll;
     if (lda > kSpan || ldb > kSpan || ldd > kSpan || e.ldr > kSpan || e.ldp > kSpan) return IGC_ERR_UNSUPPORTED;
     if (pl.few) {
-        if (M * lda >= kSpan || 64 * ldb + 256 >= kSpan || N >= (1ll << 30) ||
-            !launchable(pl.rows.cols * pl.rows.splits, 512))
-            return IGC_ERR_UNSUPPORTED;
+        if (M * lda >= kSpan || 64 * ldb + 256 >= kSpan) return IGC_ERR_UNSUPPORTED;
         Workspace ws;
         if (const igc_status_t st = ws.take(pl.bytes, user_ws, user_ws_bytes, stream)) return st;
         (void)hipGetLastError();
@@ -207,13 +216,10 @@ static igc_status_t int8_any(int64_t M, int64_t N, int64_t K, const int8_t* A, i
     const int64_t tiles_m = (M + t.bm - 1) / t.bm, tiles_n = (N + t.bn - 1) / t.bn;
     const auto span = [&](int64_t ld, int kind) { return t.bm * ld * (kind == OUT_F32 ? 4 : 2) >= kSpan; };
     const bool split = pl.S > 1;
-    if (t.bm * lda + 2 * t.bk >= kSpan || t.bn * ldb + 2 * t.bk >= kSpan || tiles_m * tiles_n > 0x7fffffff ||
-        !launchable(tiles_m * tiles_n * pl.S, 64 * t.waves) || (split && t.bm * pl.ldws * 4 >= kSpan) ||
-        (split && !launchable((M * ((N + 7) / 8) + 255) / 256, 256)) ||
+    if (t.bm * lda + 2 * t.bk >= kSpan || t.bn * ldb + 2 * t.bk >= kSpan || (split && t.bm * pl.ldws * 4 >= kSpan) ||
         (!split && (span(ldd, (int)dt) || (e.res && span(e.ldr, e.res_kind)) || (e.pre && span(e.ldp, e.pre_kind)))))
         return IGC_ERR_UNSUPPORTED;
     const void* fn = split ? pl.inst->part : (e.act == ACT_NONE && !e.pre ? pl.inst->lean : pl.inst->fn);
-    if (!fn) return IGC_ERR_UNSUPPORTED;
     Workspace ws;
     if (const igc_status_t st = ws.take(pl.bytes, user_ws, user_ws_bytes, stream)) return st;
     (void)hipGetLastError();  // launch errors below are ours alone
@@ -268,15 +274,16 @@ igc_status_t gemm_int8_ex(int64_t M, int64_t N, int64_t K, const int8_t* A, int6
 }
 
 int64_t igc_gemm_int8_workspace_bytes(int64_t M, int64_t N, int64_t K, const igc_tune_t* tune) {
-    if (M < 0 || N < 0 || K < 0 || K > kMaxK || M >= (1ll << 40) || N >= (1ll << 40)) return -1;
+    if (M < 0 || N < 0 || K < 0 || sizes_too_large(M, N, K)) return -1;
     const Int8Plan pl = plan_of(tune, M, N, K);
-    if (!pl.valid || (!pl.few && (!pl.inst || pl.tune.stream_k > 0))) return -1;
+    if (!pl.valid || !pl.fits) return -1;
     return M == 0 || N == 0 ? 0 : pl.bytes;
 }
 
 int igc_gemm_int8_default_tune(int64_t M, int64_t N, int64_t K, igc_tune_t* out) {
-    if (!out || M < 0 || N < 0 || K < 0 || K > kMaxK || M >= (1ll << 40) || N >= (1ll << 40)) return 0;
+    if (!out || M < 0 || N < 0 || K < 0 || sizes_too_large(M, N, K)) return 0;
     const Int8Plan pl = plan_of(nullptr, M, N, K);
+    if (!pl.fits) return 0;
     if (pl.few) {
         *out = igc_tune_t{};
         out->bn = 16 * pl.rows.nb;
@@ -284,7 +291,7 @@ int igc_gemm_int8_default_tune(int64_t M, int64_t N, int64_t K, igc_tune_t* out)
         return 1;
     }
     *out = pl.tune;
-    return pl.inst && pl.tune.stream_k == 0 && (pl.S > 1 ? pl.inst->part : pl.inst->fn) ? 1 : 0;
+    return 1;
 }
 
 }  // extern "C"

@@ -631,8 +631,10 @@ static igc_status_t check_rows(const void* ptr, int64_t ld, int64_t C, int bytes
     return !aligned16(ptr) || ld * bytes % 16 != 0 ? IGC_ERR_MISALIGNED : IGC_OK;
 }
 static bool misplaced(const void* ptr, igc_out_t type) { return reinterpret_cast<uintptr_t>(ptr) % out_size(type) != 0; }
-// Sizes beyond these are refused, as are leading dimensions whose offsets pass 64 bits.
-static bool rows_too_large(int64_t M, int64_t C) { return M >= (1ll << 40) || C >= (1ll << 30); }
+// Sizes beyond these are refused, as are leading dimensions whose offsets pass 64 bits (and, for the gradient, a dgamma
+// of more columns than column_sum's grid takes).
+static bool rows_too_large(int64_t M, int64_t C) { return M >= (1ll << 30) || C >= (1ll << 30); }
+static bool sums_too_large(int64_t C) { return !launchable((C + 31) / 32, 1024); }
 static bool strides_too_large(std::initializer_list<int64_t> lds) {
     for (const int64_t ld : lds)
         if (ld >= (1ll << 32)) return true;
@@ -749,7 +751,9 @@ static igc_status_t backward_any(bool fp16, int64_t M, int64_t C, const void* h,
         if (!rstd) return IGC_ERR_INVALID_VALUE;
     }
     if (misplaced(gamma, pt) || misplaced(dgamma, pt) || misplaced(rstd, IGC_OUT_F32)) return IGC_ERR_MISALIGNED;
-    if (rows_too_large(M, C) || (M > 0 && strides_too_large({ldh, lddy, dh ? lddh : 0, lddx}))) return IGC_ERR_UNSUPPORTED;
+    if (rows_too_large(M, C) || (dgamma && sums_too_large(C)) ||
+        (M > 0 && strides_too_large({ldh, lddy, dh ? lddh : 0, lddx})))
+        return IGC_ERR_UNSUPPORTED;
     const RowShape s = row_shape(M, C, ROW_BACKWARD);
     const int64_t groups = backward_groups(s, M);
     Workspace ws;
@@ -828,7 +832,7 @@ IGC_NORM(bf16, false)
 IGC_NORM(fp16, true)
 
 int64_t igc_rms_norm_backward_workspace_bytes(int64_t M, int64_t C) {
-    if (M < 0 || C < 1 || rows_too_large(M, C)) return -1;
+    if (M < 0 || C < 1 || rows_too_large(M, C) || sums_too_large(C)) return -1;
     return M == 0 ? 0 : backward_bytes(row_shape(M, C, ROW_BACKWARD), M, C);
 }
 

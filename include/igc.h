@@ -491,8 +491,8 @@ int64_t igc_group_norm_workspace_bytes(int N, int H, int W, int C, int G);
  * M == 0 or N == 0 is a no-op.
  * Requirements: lda, ldb >= K and multiples of 16 (the 16-byte rule), sizes,
  * pointers and types as everywhere; K < 2^17 (a longer sum may not fit 32 bits),
- * leading dimensions and the rows of one tile spanning less than 2^31 bytes,
- * else IGC_ERR_UNSUPPORTED.
+ * M and N < 2^31 and a grid of fewer than 2^32 threads, leading dimensions and
+ * the rows of one tile spanning less than 2^31 bytes, else IGC_ERR_UNSUPPORTED.
  * Tunes are those of the 16-bit products with IGC_SCOPE_ALL and
  * IGC_SCOPE_EPILOGUE, a K tile of bk holding 2*bk values; stream-K is
  * IGC_ERR_UNSUPPORTED.  The parts of a K split are int32 in the workspace, of
@@ -522,15 +522,16 @@ int igc_gemm_int8_default_tune(int64_t M, int64_t N, int64_t K, igc_tune_t *out)
  *   rms_norm_int8_*: y goes to 8 bits instead, for gemm_int8's A:
  *   scale[m] = max_c |y| / 127,  q = y / scale to the nearest integer, ties to
  *   even, so that q * scale stands for y.  A row of zeros has scale 0 and zeros;
- *   a row with an infinity or a NaN has scale NaN and zeros, and so gives NaN in
- *   the product.  Scales below 2^-126 lose bits.
+ *   a row with an infinity or a NaN, its own or of h * gamma, has scale NaN and
+ *   zeros, and so gives NaN in the product.  Scales below 2^-126 lose bits.
  * h may be x or residual, and y may be x or residual if h is not the same one
  * (same leading dimension): a row's values are read before they are written.
- * A row whose mean square overflows fp32 has rstd 0.
+ * A row whose mean square overflows fp32 has rstd 0.  With eps 0 a row of zeros
+ * has rstd infinite and gives NaN (y, and the scale with zeros), as the formula does.
  * Requirements: M >= 0 (0 is a no-op), C >= 1, leading dimensions >= C, eps >= 0,
  * else IGC_ERR_INVALID_VALUE; the alignment rule (q: ldq a multiple of 16), any C;
- * C < 2^30, leading dimensions < 2^32 and fewer than 2^32 threads (M < 2^22 holds
- * for every C), else IGC_ERR_UNSUPPORTED.  No workspace.
+ * M and C < 2^30, leading dimensions < 2^32 and fewer than 2^32 threads (M < 2^22
+ * holds for every C), else IGC_ERR_UNSUPPORTED.  No workspace.
  */
 igc_status_t rms_norm_bf16(int64_t M, int64_t C, const void *x, int64_t ldx, const void *residual, int64_t ldr, void *h,
                            int64_t ldh, const void *gamma, igc_out_t param_type, float eps, void *y, int64_t ldy,
@@ -553,7 +554,8 @@ igc_status_t rms_norm_int8_fp16(int64_t M, int64_t C, const void *x, int64_t ldx
  * dh is the gradient that reaches h itself, past the norm (NULL: none).  dx is
  * the gradient of x and of residual alike.  dgamma NULL: not computed.  dx may be
  * dy, dh or h (same leading dimension).  M == 0 writes dgamma = 0.
- * Requirements as the norm's.  Workspace when dgamma is given:
+ * Requirements as the norm's, but that the grid is small for every M, and
+ * dgamma takes C < 2^27.  Workspace when dgamma is given:
  * igc_rms_norm_backward_workspace_bytes (-1 for bad or refused sizes).
  */
 igc_status_t rms_norm_backward_bf16(int64_t M, int64_t C, const void *h, int64_t ldh, const void *gamma,

@@ -78,6 +78,20 @@ def test_product_workspaces_and_choices():
                 assert (need > 0) == (t.k_splits > 1), (M, N, K, t.k_splits, need)
 
 
+def test_products_too_large_for_a_grid():
+    """Sizes whose product of tiles, or of partial sums, would not fit 64 bits are refused by the call and its queries."""
+    big, cut = (1 << 40) - 1, (64, 64, 64, 4, 8, 16, 0, 4, 16, 0)
+    for M, N, tune in ((big, big, None), (big, 64, None), (64, big, None), ((1 << 31) - 1, (1 << 31) - 16, None),
+                       ((1 << 31) - 1, (1 << 31) - 16, cut), (1 << 20, 1 << 20, cut), (1, 1 << 30, None),
+                       (512, 512, (256, 256, 64, 2, 8, 16, 1, 4, 2, 0))):
+        assert igc.igc_gemm_int8_workspace_bytes(M, N, 8192, tune) == -1, (M, N)
+        assert igc.gemm_int8_ex(M, N, 8192, P, 8192, P, P, 8192, P, P, -(-N // 16) * 16, 0, None, tune, workspace=P,
+                                workspace_bytes=1 << 62, stream=0) == UNSUPPORTED, (M, N)
+        if tune is None:
+            with pytest.raises(ValueError):
+                igc.igc_gemm_int8_default_tune(M, N, 8192)
+
+
 NORM = dict(M=4, C=24, x=P, ldx=24, residual=P, ldr=24, h=P, ldh=24, gamma=P, param_type=0, eps=1e-6, y=P, ldy=32, last=P)
 ROWS = [(dict(M=-1), INVALID), (dict(C=0), INVALID), (dict(C=-8), INVALID), (dict(param_type=3), INVALID),
         (dict(x=None), INVALID), (dict(ldx=23), INVALID), (dict(ldr=16), INVALID), (dict(ldh=8), INVALID),
@@ -125,6 +139,14 @@ def test_norm_backward_workspaces():
     assert need(-1, 8) == need(8, 0) == need(1 << 40, 8) == need(8, 1 << 30) == -1
     assert need(0, 1000) == need(1, 1000) == 0
     assert need(8192, 4096) % 256 == 0 and 0 < need(8192, 4096) <= 64 << 20
+
+
+def test_norm_backward_too_large():
+    wide = dict(C=1 << 27, ldh=1 << 27, lddy=1 << 27, lddh=1 << 27, lddx=1 << 27)
+    for call in (wide, {**wide, "M": 0}, dict(M=1 << 30)):
+        assert igc.rms_norm_backward_bf16(*{**BACK, **call}.values(), stream=0) == UNSUPPORTED, call
+    need = igc.igc_rms_norm_backward_workspace_bytes
+    assert need(4, 1 << 27) == need(0, 1 << 27) == need(1 << 30, 8) == -1
 
 
 QUANT = dict(M=4, C=24, act="silu", x=P, ldx=24, gate=P, ldg=24, q=P, ldq=32, scale=P)

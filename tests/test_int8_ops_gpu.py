@@ -472,6 +472,26 @@ def test_rows_that_are_not_ordinary(C):
     assert torch.isfinite(scale[[0, 1, 2, 3, 6, 7]]).all()
 
 
+@pytest.mark.parametrize("C", [60, 40000])
+def test_norm_without_eps(C):
+    """eps 0: rows of zeros are NaN, as 0 / 0 is; the others are exact to the same bounds."""
+    t, M = torch.bfloat16, 3
+    x = normal(generator(C), M, C, dtype=t)
+    x[1] = 0
+    x, _ = padded(x, round8(C))
+    ld = x.stride(0)
+    y, rstd, scale = torch.empty(M, ld, dtype=t, device="cuda"), torch.empty(M, device="cuda"), torch.empty(M, device="cuda")
+    q = torch.full((M, up16(C)), 99, dtype=torch.int8, device="cuda")
+    igc.check(igc.rms_norm_bf16(M, C, x, ld, None, 0, None, 0, None, 0, 0.0, y, ld, rstd))
+    igc.check(igc.rms_norm_int8_bf16(M, C, x, ld, None, 0, None, 0, None, 0, 0.0, q, up16(C), scale))
+    synchronize()
+    assert rstd[1] == float("inf") and torch.isnan(y[1, :C]).all() and torch.isnan(scale[1]) and (q[1, :C] == 0).all()
+    for m in (0, 2):
+        d = x[m, :C].double()
+        want = d / torch.sqrt((d * d).mean())
+        assert_within(y[m, :C], want, want.abs() * ((DEPTH(C) + 2) / 2 + 6) * U32, f"row {m}")
+
+
 def test_ties_go_to_even():
     C = 256
     x = torch.zeros(2, C, dtype=torch.bfloat16)
