@@ -8,7 +8,16 @@
 // product of K/2 with another instruction (16x16x64 on integers, twice the
 // operations in the same time) and integer accumulators: the sum is exact,
 // whatever order, tile or split it is taken in.  The epilogue turns it into
-// fp32 and scales it as it reads the staged rows back.
+// fp32, times the row's scale, as it stages rows, and applies the column's and
+// the bias in one step as it reads them back.
+//
+// 8192 x 8192 x 8192 393 us, 2800 TOP/s (a loop of the instruction alone: 4150);
+// 512 x 16384 x 2048 in 256 x 128 tiles 21.8, one round of them.  Smaller tiles
+// are bound by the path from memory to LDS: 2048 x 1024 x 16384 in 64 x 128
+// tiles 39.5 us, 35 of the 42 bytes a clock that a CU reaches when it does
+// nothing but load.  Operands straight to registers (64-byte pieces of rows) took
+// 1.5 to 2.5 times as long; K cut among the waves of a workgroup, deeper rings,
+// and more or fewer loading waves measured the same.
 #include "epilogue.hpp"
 #include "int8_gemm.hpp"
 

@@ -729,3 +729,40 @@ def test_pinned_tensors():
     igc.check(igc.quantize_rows_int8_bf16(4, 64, "none", x, 64, None, 0, q, 64, s))
     synchronize()
     check_int8(q, torch.full((1, 64), 99), s, x.double(), 2 * U32, "pinned")
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+@pytest.mark.parametrize("M,C", [(300, 8192), (40, 1001), (3, 40000)])
+def test_every_tie_goes_to_even(M, C, dtype):
+    """Products of two 16-bit values are exact in fp32, and under a largest one that 127 divides many lie half-way between
+    two integers (127 over it is 3.2 here, which fp32 rounds): q is the nearest integer of the exact ratio, or at a tie the
+    even one.
+
+    A value that is no tie may lie within 2^-24 of a step beside one and go either way; 2^-20 is left out here."""
+    t = DT[dtype]
+    g = generator(C + M)
+    x, u = normal(g, M, C, dtype=t), normal(g, M, C, dtype=t)
+    gamma = torch.where(normal(g, C) > 0, 1.0, -0.5).to(t)
+    x[::2], u[::2] = (8 * x[::2]).round().clamp(-50, 50) * 5 / 32, gamma
+    x[:, 5], u[:, 5], gamma[5] = 127 / 8, 2.5, 2.5  # the largest of a row: 127 * 5 / 16; odd multiples of 5 / 32 are ties
+    x[1], u[1] = x[1] * 2.0 ** -9, u[1] * 2.0 ** -3
+    x, _ = padded(x, round8(C))
+    u, _ = padded(u, round8(C))
+    gamma = gamma.cuda()
+    q, scale = torch.full((M, up16(C)), 99, dtype=torch.int8, device="cuda"), torch.empty(M, device="cuda")
+
+    def check(v):
+        steps = v * 127 / v.abs().amax(1, keepdim=True)
+        beside = (steps - steps.floor() - 0.5).abs()
+        ties = beside == 0
+        assert ties.sum() >= C // 100, ties.sum()
+        wrong = (q[:, :C].double() != steps.round()) & (ties | (beside > 2.0 ** -20))
+        assert not wrong.any(), (wrong.nonzero()[:4], wrong.sum(), ties.sum())
+
+    igc.check(QUANT[dtype](M, C, "none", x, x.stride(0), u, u.stride(0), q, up16(C), scale))
+    synchronize()
+    check(x[:, :C].double() * u[:, :C].double())
+    q.fill_(99)
+    igc.check(NORM8[dtype](M, C, x, x.stride(0), None, 0, None, 0, gamma, igc.out_code(t), EPS, q, up16(C), scale))
+    synchronize()
+    check(x[:, :C].double() * gamma.double())
