@@ -522,7 +522,7 @@ int igc_gemm_int8_default_tune(int64_t M, int64_t N, int64_t K, igc_tune_t *out)
  *   rms_norm_int8_*: y goes to 8 bits instead, for gemm_int8's A:
  *   scale[m] = max_c |y| / 127,  q = y / scale to the nearest integer, ties to
  *   even, so that q * scale stands for y (rstd cancels in q: it is taken of
- *   h * gamma in fp32, and exactly so, up to 2^-24 of a step beside a tie).  A row of zeros has scale 0 and zeros;
+ *   h * gamma in fp32, rounded to fp32 once before it is to an integer).  A row of zeros has scale 0 and zeros;
  *   a row with an infinity or a NaN, its own or of h * gamma, has scale NaN and
  *   zeros, and so gives NaN in the product.  Scales below 2^-126 lose bits.
  * h may be x or residual, and y may be x or residual if h is not the same one
