@@ -65,11 +65,12 @@ static igc_tune_t int8_tune(int64_t M, int64_t N, int64_t K) {
             return us > q.least ? us : q.least;
         };
         for (int64_t s = 1; s <= 16 && (s == 1 || (K / s >= 512 && tiles * s <= 256 && q.bm * q.bn <= 256 * 128)); ++s) {
+            const double join = s > 1 ? 3.7 + (double)s * (double)M * (double)N * 8.0 / 5e6 : 0.0;
+            if (s > 1 && q.fixed + join >= best) break;  // (the join grows with the parts)
             const int64_t work = tiles * s, rounds = (work + 255) / 256;
             const double last = (double)(work - (rounds - 1) * 256) / 256.0;  // of the CUs
-            double cost = q.fixed + (double)(rounds - 1) * q.round +
-                          (double)((steps + s - 1) / s) * ((double)(rounds - 1) * step(1.0) + step(last));
-            if (s > 1) cost += 3.7 + (double)s * (double)M * (double)N * 8.0 / 5e6;
+            const double cost = q.fixed + (double)(rounds - 1) * q.round +
+                          (double)((steps + s - 1) / s) * ((double)(rounds - 1) * step(1.0) + step(last)) + join;
             if (best < 0 || cost < best) {
                 best = cost;
                 t = igc_tune_t{q.bm, q.bn, 64, q.depth, 8, 16, q.half, 4, s > 1 ? (int)s : 0, 0, 0, 0};
