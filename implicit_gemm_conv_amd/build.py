@@ -39,6 +39,10 @@ FAMILIES_FULL = (0, 1, 2, 3, 4)   # bf16 GEMM, fp16 GEMM, forward conv, data gra
 FAMILIES_STUDY = (0, 1, 2)        # bf16 and fp16 GEMM (row-major A), bf16 forward conv
 
 
+# Tiles that only the product of 8-bit integers has, in the fields of tile_configs.hpp up to SYNC (why: int8_gemm.hip).
+INT8_TILES = ((64, 64, 64, 5, 8, 16, 0, 4, 0), (32, 64, 64, 5, 4, 16, 0, 0, 0))
+
+
 def tile_configs():
     """(bm, bn, bk, depth, waves, mfma, half, loaders, sync, scope) per X(...) line of tile_configs.hpp."""
     text = open(os.path.join(CSRC, "tile_configs.hpp")).read()
@@ -58,6 +62,13 @@ def _run(cmd):
     if r.returncode != 0:
         raise RuntimeError(f"{' '.join(cmd)}\n{out}")
     return out
+
+
+def int8_unit(bm, bn, bk, d, w, mi, h, lw, sy):
+    obj = os.path.join(OBJ_DIR, f"int8_{bm}x{bn}x{bk}x{d}x{w}x{mi}x{h}x{lw}x{sy}.o")
+    return [HIPCC, *FLAGS, f"-DIGC_BM={bm}", f"-DIGC_BN={bn}", f"-DIGC_BK={bk}", f"-DIGC_D={d}", f"-DIGC_W={w}",
+            f"-DIGC_MI={mi}", f"-DIGC_HALF={h}", f"-DIGC_LW={lw}", f"-DIGC_SYNC={sy}", "-c",
+            os.path.join(CSRC, "int8_instances.hip"), "-o", obj]
 
 
 def instance_units(configs=None):
@@ -87,10 +98,8 @@ def instance_units(configs=None):
                               f"-DIGC_SYNC={sy}", f"-DIGC_FAMILY={fam}", "-c",
                               os.path.join(CSRC, "epilogue_instances.hip"), "-o", obj])
             if full:  # and the product of 8-bit integers
-                obj = os.path.join(OBJ_DIR, f"int8_{bm}x{bn}x{bk}x{d}x{w}x{mi}x{h}x{lw}x{sy}.o")
-                units.append([HIPCC, *FLAGS, f"-DIGC_BM={bm}", f"-DIGC_BN={bn}", f"-DIGC_BK={bk}", f"-DIGC_D={d}",
-                              f"-DIGC_W={w}", f"-DIGC_MI={mi}", f"-DIGC_HALF={h}", f"-DIGC_LW={lw}",
-                              f"-DIGC_SYNC={sy}", "-c", os.path.join(CSRC, "int8_instances.hip"), "-o", obj])
+                units.append(int8_unit(bm, bn, bk, d, w, mi, h, lw, sy))
+    units += [int8_unit(*c) for c in INT8_TILES if not only or "x".join(map(str, c)) in only]
     # the epilogue units with every operand layout take longest: first, so that none is left at the end
     units.sort(key=lambda u: "epi_256x256" not in u[-1])
     return units

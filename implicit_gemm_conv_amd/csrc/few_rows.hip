@@ -282,10 +282,11 @@ FewRowsPlan few_rows_plan(int64_t M, int64_t N, int64_t K, bool b_kc) {
 }
 
 // 8-bit operands, against the tiles (here / there, us; * weights from memory, the others from the last-level cache):
-//   1 row: 4096 x 4096 5.9 / 9.6, 8192 x 2048 5.9 / 7.2, 2048 x 8192 7.6 / 9.8, 16384 x 4096* 16.1 / 18.4;
-//   16 rows: 4096 x 4096 7.2 / 9.7, 8192 x 2048 7.2 / 7.3, 2048 x 8192 10.2 / 10.1, 12000 x 3001 9.3 / 10.2,
-//   16384 x 4096* 19.8 / 19.0;  32 rows, whose A each workgroup reads twice as much of: 4096 x 4096 9.0 / 9.8,
-//   4096 x 1024 4.4 / 4.9, 1024 x 4096 8.0 / 8.1, 8192 x 2048 9.1 / 7.4, 2048 x 8192 13.9 / 10.5.
+//   1 row: 4096 x 4096 6.0 / 8.3, 8192 x 2048 5.3 / 6.1, * 6.0 / 7.4, 2048 x 8192 7.8 / 9.5, 16384 x 4096 13.1 / 12.6,
+//   * 16.6 / 17.3;  16 rows: 4096 x 4096 7.2 / 8.5, 8192 x 2048 7.0 / 6.2, * 7.3 / 8.1, 2048 x 8192 10.2 / 10.0,
+//   12000 x 3001 9.3 / 9.8, 8192 x 8192* 20.3 / 18.8, 16384 x 4096 13.3 / 12.9;  32 rows, whose A each workgroup reads
+//   twice as much of: 4096 x 4096 9.0 / 8.3, * 9.4 / 11.0, 4096 x 1024 4.5 / 4.6, 1024 x 4096 8.2 / 7.3, * 8.9 / 10.6,
+//   4096 x 2048 5.8 / 5.4, * 6.7 / 7.4.
 bool few_rows_int8_faster(int64_t M, int64_t N, int64_t K) {
     if (M <= 8) return true;
     return M <= 16 ? N <= 12288 && K <= 8192 : N <= 4096 && K <= 4096;

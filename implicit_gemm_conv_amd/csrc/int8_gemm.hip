@@ -39,33 +39,38 @@ constexpr int64_t kMaxK = (1ll << 17) - 1;
 
 // The cheapest tile and K split by what they cost, in us: launch, first loads
 // and epilogue; a K tile of 128 values, whose time grows with what all busy CUs
-// load for it, and by a quarter where rows of K values do not begin on whole
+// load for it, and by a third where rows of K values do not begin on whole
 // cache lines; a further round; for a split a second launch and the partials
-// twice through memory.  Fitted to 140 shapes whose K is a multiple of 128, with
-// every tile and up to 16 parts: the choice takes 0.4% more there than the best
-// of them all (geometric mean; 15% at most), and 1.0% on 147 others (25% at
-// most).  That of the 16-bit products for half of K takes 2.2% more, and up to
-// 21% (1500 x 3000 x 700 17.9 us against 14.7).
+// twice through memory.  Fitted to 287 shapes, 140 of them with K a multiple of
+// 128, with every tile and up to 16 parts: the choice takes 0.5% more than the
+// best of them all (geometric mean; 13% at most), and 0.4% on 130 others (9%).
+//
+// Two tiles are this product's own.  32 x 64 is for grids that leave CUs idle,
+// where a K tile takes what one CU needs to load it: 64 x 4096 x 4096 8.3 us (64 x
+// 64: 9.7), 256 x 2048 x 8192 12.8 (15.8), but 512 x 4096 x 4096 21.9 (16.7).  64 x 64
+// in a ring of 5 stages, of which two workgroups still share a CU, takes 16.2 us
+// for 512 x 2048 x 8192 (4 stages: 18.3; 8: 16.8) and 0.15 more in the smallest calls.
 static igc_tune_t int8_tune(int64_t M, int64_t N, int64_t K) {
     constexpr struct {
-        int bm, bn, depth, half;
+        int bm, bn, depth, waves, loaders, half;
         double fixed, round, least, step, load;  // load: for each KB of a K tile with every CU busy
-    } kinds[] = {{64, 64, 4, 0, 3.8, 0.85, 0.0, 0.15, 0.0037},
-                 {64, 128, 4, 0, 4.3, 2.3, 0.0, 0.20, 0.0042},
-                 {128, 128, 4, 0, 5.2, 3.5, 0.0, 0.25, 0.0065},
-                 {256, 128, 3, 0, 6.7, 5.1, 0.47, 0.28, 0.011},
-                 {256, 256, 2, 1, 11.1, 8.1, 0.87, 0.64, 0.0121}};
+    } kinds[] = {{32, 64, 5, 4, 0, 0, 4.0, 0.67, 0.0, 0.107, 0.0032},
+                 {64, 64, 5, 8, 4, 0, 4.3, 1.0, 0.0, 0.122, 0.0051},
+                 {64, 128, 4, 8, 4, 0, 4.75, 2.6, 0.0, 0.183, 0.0051},
+                 {128, 128, 4, 8, 4, 0, 5.9, 3.9, 0.0, 0.233, 0.0068},
+                 {256, 128, 3, 8, 4, 0, 7.8, 6.1, 0.26, 0.353, 0.0084},
+                 {256, 256, 2, 8, 4, 1, 12.4, 9.1, 0.84, 0.474, 0.0136}};
     igc_tune_t t = {};
     double best = -1;
     for (const auto& q : kinds) {
         const int64_t tiles = ((M + q.bm - 1) / q.bm) * ((N + q.bn - 1) / q.bn), steps = (K + 127) / 128;
         const double kb = ((double)(M < q.bm ? M : q.bm) + (double)(N < q.bn ? N : q.bn)) * 128.0 / 1024.0;
         const auto step = [&](double busy) {
-            const double us = (q.step + kb * q.load * busy) * (K % 128 ? 1.25 : 1.0);
+            const double us = (q.step + kb * q.load * busy) * (K % 128 ? 1.35 : 1.0);
             return us > q.least ? us : q.least;
         };
         for (int64_t s = 1; s <= 16 && (s == 1 || (K / s >= 512 && tiles * s <= 256 && q.bm * q.bn <= 256 * 128)); ++s) {
-            const double join = s > 1 ? 3.7 + (double)s * (double)M * (double)N * 8.0 / 5e6 : 0.0;
+            const double join = s > 1 ? 3.4 + (double)s * (double)M * (double)N * 8.0 / 5.2e6 : 0.0;
             if (s > 1 && q.fixed + join >= best) break;  // (the join grows with the parts)
             const int64_t work = tiles * s, rounds = (work + 255) / 256;
             const double last = (double)(work - (rounds - 1) * 256) / 256.0;  // of the CUs
@@ -73,7 +78,7 @@ static igc_tune_t int8_tune(int64_t M, int64_t N, int64_t K) {
                           (double)((steps + s - 1) / s) * ((double)(rounds - 1) * step(1.0) + step(last)) + join;
             if (best < 0 || cost < best) {
                 best = cost;
-                t = igc_tune_t{q.bm, q.bn, 64, q.depth, 8, 16, q.half, 4, s > 1 ? (int)s : 0, 0, 0, 0};
+                t = igc_tune_t{q.bm, q.bn, 64, q.depth, q.waves, 16, q.half, q.loaders, s > 1 ? (int)s : 0, 0, 0, 0};
             }
         }
     }

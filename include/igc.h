@@ -494,7 +494,9 @@ int64_t igc_group_norm_workspace_bytes(int N, int H, int W, int C, int G);
  * M and N < 2^31 and a grid of fewer than 2^32 threads, leading dimensions and
  * the rows of one tile spanning less than 2^31 bytes, else IGC_ERR_UNSUPPORTED.
  * Tunes are those of the 16-bit products with IGC_SCOPE_ALL and
- * IGC_SCOPE_EPILOGUE, a K tile of bk holding 2*bk values; stream-K is
+ * IGC_SCOPE_EPILOGUE, and two more tiles: 64 x 64 x 64 of depth 5 (8 waves, 4 of
+ * them loading) and 32 x 64 x 64 of depth 5 (4 waves); a K tile of bk holds 2*bk
+ * values; stream-K is
  * IGC_ERR_UNSUPPORTED.  The parts of a K split are int32 in the workspace, of
  * igc_gemm_int8_workspace_bytes (-1 for sizes or a tune that the call refuses).
  * igc_gemm_int8_default_tune tells the built-in choice as

@@ -767,3 +767,21 @@ def test_every_tie_goes_to_even(M, C, dtype):
     igc.check(NORM8[dtype](M, C, x, x.stride(0), None, 0, None, 0, gamma, igc.out_code(t), EPS, q, up16(C), scale))
     synchronize()
     check(x[:, :C].double() * gamma.double())
+
+
+OWN_TILES = [(64, 64, 64, 5, 8, 16, 0, 4), (32, 64, 64, 5, 4, 16, 0, 0)]
+
+
+@pytest.mark.parametrize("cfg", OWN_TILES, ids=str)
+@pytest.mark.parametrize("K", [1, 16, 127, 128, 640, 1001, 1300])
+def test_product_of_its_own_tiles(cfg, K):
+    bm, bn = cfg[:2]
+    for M, N, act in ((bm, bn, "gelu_tanh"), (bm + 3, 2 * bn + 5, "silu"), (1, 7, "none"), (3 * bm, 9 * bn, "none")):
+        p = Product(M, N, K, "bf16", act=act, seed=K)
+        p.check(p.run(igc.tune(cfg)), f"{cfg} {M}x{N}x{K}")
+
+
+@pytest.mark.parametrize("cfg", OWN_TILES, ids=str)
+@pytest.mark.parametrize("M,N,K,splits", [(70, 130, 4097, 3), (300, 131, 8200, 5), (33, 64, 2048, 16)])
+def test_product_in_parts_of_its_own_tiles(cfg, M, N, K, splits):
+    test_product_in_parts(cfg, M, N, K, splits)
