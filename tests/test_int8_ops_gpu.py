@@ -785,3 +785,20 @@ def test_product_of_its_own_tiles(cfg, K):
 @pytest.mark.parametrize("M,N,K,splits", [(70, 130, 4097, 3), (300, 131, 8200, 5), (33, 64, 2048, 16)])
 def test_product_in_parts_of_its_own_tiles(cfg, M, N, K, splits):
     test_product_in_parts(cfg, M, N, K, splits)
+
+
+@pytest.mark.parametrize("C", [200, 40000])
+def test_rows_of_every_magnitude(C):
+    """A row times a power of two goes to the same integers, and its scale is that much larger, exactly."""
+    row = normal(generator(C), 1, C, dtype=torch.bfloat16).clamp(-60, 60)
+    row[0, ::3] = (4 * row[0, ::3]).round() / 4
+    row[0, 5] = 127 / 2  # odd multiples of 1 / 4 are ties
+    powers = [0, 110, 120, -60, -97, -101, -115]
+    x = torch.cat([row.float() * 2.0 ** p for p in powers]).to(torch.bfloat16)
+    x, _ = padded(x, round8(C))
+    q, scale = torch.full((len(powers), up16(C)), 99, dtype=torch.int8, device="cuda"), torch.empty(len(powers), device="cuda")
+    igc.check(igc.quantize_rows_int8_bf16(len(powers), C, "none", x, x.stride(0), None, 0, q, up16(C), scale))
+    synchronize()
+    for i, p in enumerate(powers):
+        assert torch.equal(q[i, :C], q[0, :C]), f"2^{p}"
+        assert scale[i].item() == scale[0].item() * 2.0 ** p, f"2^{p}"
