@@ -6,6 +6,7 @@
 #pragma once
 #include "activation.hpp"
 #include "mainloop.hpp"
+#include "row_io.hpp"
 
 namespace igc {
 
@@ -30,48 +31,6 @@ struct EpiInt8 : Epi {
 // Whether a configuration's accumulators are integers.
 template <class C>
 constexpr bool kInt8 = std::is_same<typename C::Acc, i32x4_t>::value;
-
-// Eight consecutive values of row storage, element `off` first.  vec: whole
-// 16-byte pieces may be read as long as they hold one value below `left` (how
-// many of the eight lie inside the row); rows are then 16-byte multiples, so
-// the rest of such a piece is the row's own padding.
-__device__ __forceinline__ u32x4s_t raw8(const void* base, int64_t off) {
-    return *(const u32x4s_t*)((const char*)base + off * 2);
-}
-__device__ __forceinline__ void decode8(u32x4s_t w, int kind, float (&v)[8]) {
-    if (kind == KIND_BF16)
-        unpack8<false>(w, v);
-    else
-        unpack8<true>(w, v);
-}
-__device__ __forceinline__ void load8(const void* base, int64_t off, int kind, int left, bool vec, float (&v)[8]) {
-    if (!vec) {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] = i < left ? load_kind(base, off + i, kind) : 0.0f;
-    } else if (kind == KIND_F32) {
-        const f32x4s_t lo = *(const f32x4s_t*)((const float*)base + off);
-        f32x4s_t hi{0, 0, 0, 0};
-        if (left > 4) hi = *(const f32x4s_t*)((const float*)base + off + 4);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) v[i] = lo[i], v[4 + i] = hi[i];
-    } else {
-        decode8(raw8(base, off), kind, v);
-    }
-}
-__device__ __forceinline__ void store8(void* base, int64_t off, int kind, int left, bool vec, const float (&v)[8]) {
-    if (vec && left >= 8) {
-        if (kind == KIND_F32) {
-            *(f32x4s_t*)((float*)base + off) = f32x4s_t{v[0], v[1], v[2], v[3]};
-            *(f32x4s_t*)((float*)base + off + 4) = f32x4s_t{v[4], v[5], v[6], v[7]};
-        } else {
-            *(u32x4s_t*)((char*)base + off * 2) = kind == KIND_BF16 ? pack8<false>(v) : pack8<true>(v);
-        }
-    } else {
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-            if (i < left) store_kind(base, off + i, kind, v[i]);
-    }
-}
 
 // Epilogue of one element: what it reads, then the rest.
 struct EpiElement {

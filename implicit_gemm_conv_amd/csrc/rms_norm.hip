@@ -52,7 +52,7 @@ struct RowArgs {
     int64_t M, ldx, ldr, lddy, ldh, ldy, ldq;
     int C;
     float eps;
-    int param_kind, param_vec, act;
+    int param_kind, act;
 };
 
 // 16 bytes of a row from column c: zeros where the row has ended.  A piece with one value inside is read whole (rows
@@ -81,17 +81,8 @@ __device__ __forceinline__ u32x4s_t add_rounded(u32x4s_t a, u32x4s_t b) {
     return pack8<F16>(x);
 }
 
-// gamma of eight columns (zeros past the row's end).
-__device__ __forceinline__ void load_gamma(const RowArgs& a, int c, int left, float (&g)[8]) {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) g[i] = a.gamma ? 0.0f : 1.0f;
-    if (a.gamma && left > 0) {
-        load8(a.gamma, c, a.param_kind, left, a.param_vec != 0, g);
-        if (left < 8) {
-#pragma unroll
-            for (int i = 0; i < 8; ++i) g[i] = i < left ? g[i] : 0.0f;
-        }
-    }
+__device__ __forceinline__ void load_gamma(const RowArgs& a, int c, float (&g)[8]) {
+    load_gamma(a.gamma, a.param_kind, c, a.C, g);
 }
 
 // The magnitude as an integer, whose order puts infinity above every number and NaN above infinity.
@@ -195,7 +186,7 @@ __global__ __launch_bounds__(kRowThreads<T>) void rms_norm_kernel(const RowArgs 
 #pragma unroll
     for (int v = 0; v < V; ++v) {
         const int c = (v * T + t) * 8;
-        load_gamma(a, c, a.C - c, g[v]);
+        load_gamma(a, c, g[v]);
     }
     float s = 0.0f;
     unsigned m = 0;
@@ -248,7 +239,7 @@ __global__ __launch_bounds__(1024) void rms_norm_long_kernel(const RowArgs a) {
         if (a.res) h = add_rounded<F16>(h, load_piece(a.res, row * a.ldr + c, a.C - c));
         float f[8], g[8];
         unpack8<F16>(h, f);
-        if constexpr (INT8) load_gamma(a, c, a.C - c, g);
+        if constexpr (INT8) load_gamma(a, c, g);
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
             s = __builtin_fmaf(f[i], f[i], s);
@@ -271,7 +262,7 @@ __global__ __launch_bounds__(1024) void rms_norm_long_kernel(const RowArgs a) {
         if (a.res) h = add_rounded<F16>(h, load_piece(a.res, row * a.ldr + c, left));
         float f[8], g[8];
         unpack8<F16>(h, f);
-        load_gamma(a, c, left, g);
+        load_gamma(a, c, g);
         if (a.h) store_piece<F16>(a.h, row * a.ldh + c, left, f);
 #pragma unroll
         for (int i = 0; i < 8; ++i) f[i] = INT8 ? f[i] * g[i] : f[i] * rstd * g[i];
@@ -389,11 +380,11 @@ struct RowGamma {
             const int c = (v * T + t) * 8;
             if constexpr (kLds) {
                 float g[8];
-                load_gamma(a, c, a.C - c, g);
+                load_gamma(a, c, g);
                 lds[2 * v * T] = f32x4s_t{g[0], g[1], g[2], g[3]};
                 lds[(2 * v + 1) * T] = f32x4s_t{g[4], g[5], g[6], g[7]};
             } else {
-                load_gamma(a, c, a.C - c, reg[v]);
+                load_gamma(a, c, reg[v]);
             }
         }
     }
@@ -523,7 +514,7 @@ __global__ __launch_bounds__(1024) void rms_norm_backward_long_kernel(const RowA
             float fh[8], fd[8], g[8];
             unpack8<F16>(load_piece(a.x, row * a.ldx + c, a.C - c), fh);
             unpack8<F16>(load_piece(a.dy, row * a.lddy + c, a.C - c), fd);
-            load_gamma(a, c, a.C - c, g);
+            load_gamma(a, c, g);
             if constexpr (SUMS) {
                 f32x4s_t lo = sums[k], hi = sums[k + 1024];
 #pragma unroll
@@ -546,7 +537,7 @@ __global__ __launch_bounds__(1024) void rms_norm_backward_long_kernel(const RowA
             float fh[8], fd[8], g[8], dx[8];
             unpack8<F16>(load_piece(a.x, row * a.ldx + c, left), fh);
             unpack8<F16>(load_piece(a.dy, row * a.lddy + c, left), fd);
-            load_gamma(a, c, left, g);
+            load_gamma(a, c, g);
 #pragma unroll
             for (int i = 0; i < 8; ++i) dx[i] = rs * __builtin_fmaf(-m, fh[i], fd[i] * g[i]);
             if (a.res) {
@@ -692,7 +683,6 @@ static igc_status_t norm_any(bool fp16, bool int8, int64_t M, int64_t C, const v
     a.ldy = a.ldq = ldy;
     a.eps = eps;
     a.param_kind = (int)pt;
-    a.param_vec = aligned16(gamma);
     (void)hipGetLastError();
     const dim3 grid((unsigned)blocks);
     if (int8 && fp16)
@@ -792,7 +782,6 @@ static igc_status_t backward_any(bool fp16, int64_t M, int64_t C, const void* h,
     a.lddy = lddy;
     a.ldy = lddx;
     a.param_kind = (int)pt;
-    a.param_vec = aligned16(gamma);
     (void)hipGetLastError();
     if (M > 0) {
         if (fp16)

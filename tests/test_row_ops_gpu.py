@@ -1,0 +1,51 @@
+"""Row operators (RMS norm to 16 and 8 bits, its gradient, rows to 8 bits) where their forms cross: every type and address
+of gamma with every remainder of a row's length by 8, gradients whose sums are exact, rows at the ends of the number range.
+Definitions and tolerances are those of test_int8_ops_gpu.py unless a test says otherwise."""
+import pytest
+import torch
+
+import implicit_gemm_conv_amd as igc
+from fused_util import DT, U32
+from gpu_util import synchronize
+from test_int8_ops_gpu import NORM8, Norm, check_int8, up16
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _gpu():
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+    igc.lib()
+
+
+def place(v, odd):
+    """A view of v's values at a 16-byte multiple, or one value past it, with NaN before and after them."""
+    buf = torch.full((v.numel() + 16,), float("nan"), dtype=v.dtype, device="cuda")
+    at = 16 // v.element_size() + odd
+    out = buf[at:at + v.numel()]
+    out.copy_(v)
+    assert (out.data_ptr() % 16 == 0) == (not odd)
+    return out
+
+
+@pytest.mark.parametrize("gamma", ["f32", "bf16", "f16"])
+@pytest.mark.parametrize("odd", [False, True])
+@pytest.mark.parametrize("C", [1, 2, 3, 5, 6, 7, 9, 61, 131, 413, 1006, 1535, 2051, 4101, 8195, 16389, 20003, 32773])
+def test_gamma_of_every_type_and_address(C, odd, gamma):
+    """NaN lies around gamma: a value that is not gamma's own would reach the largest magnitude and the gradient's sums."""
+    for M, dtype, residual, dh in ((3, "bf16", True, False), (3, "fp16", False, True)):
+        n = Norm(M, C, dtype, residual=residual, gamma=gamma, seed=C)
+        n.gamma = place(n.gamma, odd)
+        what = f"{M}x{C} {dtype} gamma {gamma} odd {odd}"
+        y, h, rstd, scale = n.out(), n.out(), torch.empty(M, device="cuda"), torch.empty(M, device="cuda")
+        n.forward(y, h, rstd)
+        n.check(y, h, rstd, what)
+        qbuf = torch.full((M + 2, up16(C) + 16), 99, dtype=torch.int8, device="cuda")
+        a, b = n.args()
+        igc.check(NORM8[dtype](M, C, *a, None, 0, *b, qbuf, qbuf.stride(0), scale))
+        synchronize()
+        check_int8(qbuf[:M, :C], qbuf, scale, n.y, n.rstd_rel + 2 * U32, what)
+        dgamma, dx = place(torch.zeros(C, dtype=DT[gamma]), odd), n.out()
+        n.backward(dx, dgamma, dh)
+        n.check_backward(dx, dgamma, dh, what)
