@@ -81,8 +81,10 @@ __device__ __forceinline__ u32x4s_t add_rounded(u32x4s_t a, u32x4s_t b) {
     return pack8<F16>(x);
 }
 
+// of a row that T threads hold (short ones, 16)
+template <int T>
 __device__ __forceinline__ void load_gamma(const RowArgs& a, int c, float (&g)[8]) {
-    load_gamma(a.gamma, a.param_kind, c, a.C, g);
+    load_gamma<T == 16>(a.gamma, a.param_kind, c, a.C, g);
 }
 
 // The magnitude as an integer, whose order puts infinity above every number and NaN above infinity.
@@ -186,7 +188,7 @@ __global__ __launch_bounds__(kRowThreads<T>) void rms_norm_kernel(const RowArgs 
 #pragma unroll
     for (int v = 0; v < V; ++v) {
         const int c = (v * T + t) * 8;
-        load_gamma(a, c, g[v]);
+        load_gamma<T>(a, c, g[v]);
     }
     float s = 0.0f;
     unsigned m = 0;
@@ -239,7 +241,7 @@ __global__ __launch_bounds__(1024) void rms_norm_long_kernel(const RowArgs a) {
         if (a.res) h = add_rounded<F16>(h, load_piece(a.res, row * a.ldr + c, a.C - c));
         float f[8], g[8];
         unpack8<F16>(h, f);
-        if constexpr (INT8) load_gamma(a, c, g);
+        if constexpr (INT8) load_gamma<1024>(a, c, g);
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
             s = __builtin_fmaf(f[i], f[i], s);
@@ -262,7 +264,7 @@ __global__ __launch_bounds__(1024) void rms_norm_long_kernel(const RowArgs a) {
         if (a.res) h = add_rounded<F16>(h, load_piece(a.res, row * a.ldr + c, left));
         float f[8], g[8];
         unpack8<F16>(h, f);
-        load_gamma(a, c, g);
+        load_gamma<1024>(a, c, g);
         if (a.h) store_piece<F16>(a.h, row * a.ldh + c, left, f);
 #pragma unroll
         for (int i = 0; i < 8; ++i) f[i] = INT8 ? f[i] * g[i] : f[i] * rstd * g[i];
@@ -380,11 +382,11 @@ struct RowGamma {
             const int c = (v * T + t) * 8;
             if constexpr (kLds) {
                 float g[8];
-                load_gamma(a, c, g);
+                load_gamma<T>(a, c, g);
                 lds[2 * v * T] = f32x4s_t{g[0], g[1], g[2], g[3]};
                 lds[(2 * v + 1) * T] = f32x4s_t{g[4], g[5], g[6], g[7]};
             } else {
-                load_gamma(a, c, reg[v]);
+                load_gamma<T>(a, c, reg[v]);
             }
         }
     }
@@ -514,7 +516,7 @@ __global__ __launch_bounds__(1024) void rms_norm_backward_long_kernel(const RowA
             float fh[8], fd[8], g[8];
             unpack8<F16>(load_piece(a.x, row * a.ldx + c, a.C - c), fh);
             unpack8<F16>(load_piece(a.dy, row * a.lddy + c, a.C - c), fd);
-            load_gamma(a, c, g);
+            load_gamma<1024>(a, c, g);
             if constexpr (SUMS) {
                 f32x4s_t lo = sums[k], hi = sums[k + 1024];
 #pragma unroll
@@ -537,7 +539,7 @@ __global__ __launch_bounds__(1024) void rms_norm_backward_long_kernel(const RowA
             float fh[8], fd[8], g[8], dx[8];
             unpack8<F16>(load_piece(a.x, row * a.ldx + c, left), fh);
             unpack8<F16>(load_piece(a.dy, row * a.lddy + c, left), fd);
-            load_gamma(a, c, g);
+            load_gamma<1024>(a, c, g);
 #pragma unroll
             for (int i = 0; i < 8; ++i) dx[i] = rs * __builtin_fmaf(-m, fh[i], fd[i] * g[i]);
             if (a.res) {

@@ -51,20 +51,23 @@ __device__ __forceinline__ void store8(void* base, int64_t off, int kind, int le
 // its last value, unlike a matrix row's, and it need not begin at a 16-byte multiple.  The last C % 8 values are read as
 // the eight that end with the last one and moved down, so that every lane waits for one load (norm of 1 x 1001 with a
 // gamma in 16 bits 2.86 us, in fp32 2.96; 3.05 with a branch for the lane that has the end and reads each value).
+// SHORT: C may be below 8.
 typedef u32x4s_t __attribute__((aligned(2))) u32x4v_t;
 typedef f32x4s_t __attribute__((aligned(4))) f32x4v_t;
 typedef __attribute__((ext_vector_type(2))) uint64_t u64x2_t;
+template <bool SHORT>
 __device__ __forceinline__ void load_gamma(const void* gamma, int kind, int c, int C, float (&g)[8]) {
     const int left = C - c;
 #pragma unroll
     for (int i = 0; i < 8; ++i) g[i] = gamma ? 0.0f : 1.0f;
     if (!gamma || left <= 0) return;
+    if constexpr (SHORT)
+        if (C < 8) {
+            load8(gamma, c, kind, left, false, g);
+            return;
+        }
     const int at = left < 8 ? C - 8 : c, past = left < 8 ? 8 - left : 0;
-    if (__builtin_expect(C < 8, 0)) {
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-            if (i < left) g[i] = load_kind(gamma, c + i, kind);
-    } else if (kind == KIND_F32) {
+    if (kind == KIND_F32) {
         const f32x4v_t* p = (const f32x4v_t*)((const float*)gamma + at);
         const f32x4s_t lo = p[0], hi = p[1];
 #pragma unroll

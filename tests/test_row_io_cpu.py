@@ -38,9 +38,13 @@ int main() {
                 }
                 for (int c = 0; c < C + 8; c += 8) {
                     float g[8];
-                    igc::load_gamma(gamma, kind, c, C, g);
+                    igc::load_gamma<true>(gamma, kind, c, C, g);
                     for (int i = 0; i < 8; ++i) bad += g[i] != (c + i < C ? (float)(c + i + 1) : 0.0f);
-                    igc::load_gamma(nullptr, kind, c, C, g);
+                    if (C >= 8) {
+                        igc::load_gamma<false>(gamma, kind, c, C, g);
+                        for (int i = 0; i < 8; ++i) bad += g[i] != (c + i < C ? (float)(c + i + 1) : 0.0f);
+                    }
+                    igc::load_gamma<true>(nullptr, kind, c, C, g);
                     for (int i = 0; i < 8; ++i) bad += g[i] != 1.0f;
                 }
                 free(own);
