@@ -120,6 +120,29 @@ __device__ __forceinline__ void row_reduce(float& s, unsigned& m, float (*red)[2
     }
 }
 
+// 1 / sqrt(mean + eps) of a row whose sum of squares is s.  In bf16 the squares may leave fp32's range where their root
+// does not: above it rstd comes out as 0, and below it as more than 2^45, which needs an eps near 0.  Such a row is
+// summed once more, its values times a power of two that brings them back, for which `squares(by)` gives a thread's sum
+// of (by h)^2.  The branch is one of whole waves, its code behind the kernel's end, and ordinary rows pay its test (8192 x
+// 1024 13.4 -> 13.5 us, 1 x 4096 the same).  Every thread that shares row_reduce<T>'s barriers calls this after it with
+// the same s.
+template <bool F16, int T, int W, class Squares>
+__device__ __forceinline__ float row_rstd(const RowArgs& a, float s, float (&red)[2][W][2], Squares&& squares) {
+    static_assert(T <= 64 || W == T / 64, "one row to the waves that share barriers");
+    float rstd = 1.0f / __builtin_sqrtf(s / (float)a.C + a.eps);
+    if constexpr (!F16) {
+        const bool far = !(rstd > 0.0f && rstd < 0x1p45f);
+        if (__builtin_expect(__ballot(far) != 0, 0)) {
+            const float by = s > 1.0f ? 0x1p-80f : 0x1p70f;
+            float again = squares(by);
+            unsigned none = 0;
+            row_reduce<T>(again, none, red[1]);
+            if (far) rstd = by / __builtin_sqrtf(again / (float)a.C + a.eps * by * by);
+        }
+    }
+    return rstd;
+}
+
 // How a row of largest magnitude `top` goes to 8 bits: q = nearest(127 v / top), ties to even, scale = top / 127.
 // `pre` keeps 127 / top and 127 top finite.  A row of zeros has scale 0; one with an infinity or a NaN has that for its
 // scale, and zeros.
@@ -165,15 +188,18 @@ __device__ __forceinline__ void store_int8(int8_t* q, int64_t off, int left, u32
     }
 }
 
+// Threads of a workgroup.  The norm's has one row to the waves that share barriers.
 template <int T>
 constexpr int kRowThreads = T < 256 ? 256 : T;
+template <int T>
+constexpr int kNormThreads = T < 128 ? 256 : T;
 
 // ---- norm ----------------------------------------------------------------------------------------------------------
 
 template <bool F16, bool INT8, int T, int V>
-__global__ __launch_bounds__(kRowThreads<T>) void rms_norm_kernel(const RowArgs a) {
-    constexpr int R = kRowThreads<T> / T;
-    __shared__ float red[kRowThreads<T> / 64][2];
+__global__ __launch_bounds__(kNormThreads<T>) void rms_norm_kernel(const RowArgs a) {
+    constexpr int R = kNormThreads<T> / T;
+    __shared__ float red[2][kNormThreads<T> / 64][2];
     const int t = (int)threadIdx.x % T;
     const int64_t row = (int64_t)blockIdx.x * R + (int)threadIdx.x / T;
     const bool in = row < a.M;
@@ -206,8 +232,18 @@ __global__ __launch_bounds__(kRowThreads<T>) void rms_norm_kernel(const RowArgs 
             }
         }
     }
-    row_reduce<T>(s, m, red);
-    const float rstd = 1.0f / __builtin_sqrtf(s / (float)a.C + a.eps);
+    row_reduce<T>(s, m, red[0]);
+    const float rstd = row_rstd<F16, T>(a, s, red, [&](float by) __attribute__((always_inline)) {
+        float sum = 0.0f;
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+            float f[8];
+            unpack8<F16>(h[v], f);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) sum = __builtin_fmaf(f[i] * by, f[i] * by, sum);
+        }
+        return sum;
+    });
     if (!in) return;
     if (t == 0 && a.rstd) a.rstd[row] = rstd;
     const float top = __builtin_bit_cast(float, m);
@@ -232,7 +268,7 @@ __global__ __launch_bounds__(kRowThreads<T>) void rms_norm_kernel(const RowArgs 
 // Rows that registers do not hold: one workgroup of 1024 threads, x and residual read twice.
 template <bool F16, bool INT8>
 __global__ __launch_bounds__(1024) void rms_norm_long_kernel(const RowArgs a) {
-    __shared__ float red[16][2];
+    __shared__ float red[2][16][2];
     const int64_t row = blockIdx.x;
     float s = 0.0f;
     unsigned m = 0;
@@ -251,8 +287,19 @@ __global__ __launch_bounds__(1024) void rms_norm_long_kernel(const RowArgs a) {
             }
         }
     }
-    row_reduce<1024>(s, m, red);
-    const float rstd = 1.0f / __builtin_sqrtf(s / (float)a.C + a.eps);
+    row_reduce<1024>(s, m, red[0]);
+    const float rstd = row_rstd<F16, 1024>(a, s, red, [&](float by) __attribute__((always_inline)) {
+        float sum = 0.0f;
+        for (int c = (int)threadIdx.x * 8; c < a.C; c += 8192) {
+            u32x4s_t h = load_piece(a.x, row * a.ldx + c, a.C - c);
+            if (a.res) h = add_rounded<F16>(h, load_piece(a.res, row * a.ldr + c, a.C - c));
+            float f[8];
+            unpack8<F16>(h, f);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) sum = __builtin_fmaf(f[i] * by, f[i] * by, sum);
+        }
+        return sum;
+    });
     if (threadIdx.x == 0 && a.rstd) a.rstd[row] = rstd;
     const float top = __builtin_bit_cast(float, m);
     [[maybe_unused]] const ToInt8 to(top);
@@ -571,22 +618,23 @@ __global__ __launch_bounds__(1024) void rms_norm_backward_long_kernel(const RowA
 
 // ---- host ----------------------------------------------------------------------------------------------------------
 
+enum RowOp : int { ROW_NORM = 0, ROW_QUANTIZE = 1, ROW_BACKWARD = 2 };
 // Threads and vectors of a row; T == 0: rows that registers do not hold.
 struct RowShape {
     int T, V;
-    int threads() const { return T == 0 ? 1024 : (T < 256 ? 256 : T); }
+    int least = 256;  // threads of a workgroup with rows of fewer are 256
+    int threads() const { return T == 0 ? 1024 : (T < least ? 256 : T); }
     int rows() const { return T == 0 ? 1 : threads() / T; }
 };
 // Measured (many rows; us): norm 8192 x 4096 (512, 1) 48 and (256, 2) 52, to 8 bits 45 and 47, rows to 8 bits 32.2 and
 // 31.0; norm 4096 x 8192 (512, 2) 54, to 8 bits 48.5, (1024, 1) 52 and 50; gradient 8192 x 4096 (512, 1) 57, (256, 2) 60,
 // 4096 x 8192 (512, 2) 59, (1024, 1) 62.  A single row is fastest with one vector a thread: norm of 8192 values (1024, 1)
 // 4.0, (512, 2) 4.3, of 4096 (512, 1) 3.6, (256, 2) 4.0.
-enum RowOp : int { ROW_NORM = 0, ROW_QUANTIZE = 1, ROW_BACKWARD = 2 };
 static RowShape row_shape(int64_t M, int64_t C, RowOp op) {
     const int64_t n = (C + 7) / 8;
     if (n <= 16) return {16, 1};
     if (n <= 64) return {64, 1};
-    if (n <= 128) return {128, 1};
+    if (n <= 128) return {128, 1, op == ROW_NORM ? 128 : 256};
     if (n <= 256) return {256, 1};
     if (n <= 512) return op == ROW_QUANTIZE && M >= 512 ? RowShape{256, 2} : RowShape{512, 1};
     if (n <= 1024) return op != ROW_BACKWARD && M < 512 ? RowShape{1024, 1} : RowShape{512, 2};

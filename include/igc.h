@@ -529,7 +529,9 @@ int igc_gemm_int8_default_tune(int64_t M, int64_t N, int64_t K, igc_tune_t *out)
  *   zeros, and so gives NaN in the product.  Scales below 2^-126 lose bits.
  * h may be x or residual, and y may be x or residual if h is not the same one
  * (same leading dimension): a row's values are read before they are written.
- * A row whose mean square overflows fp32 has rstd 0.  With eps 0 a row of zeros
+ * A row's mean square need not fit fp32 (bf16's squares do not from 2^64 on, or
+ * below 2^-63), only rstd: beyond 2^126 a root mean square leaves rstd few bits,
+ * and with eps 0 one below 2^-128 makes it infinite.  With eps 0 a row of zeros
  * has rstd infinite and gives NaN (y, and the scale with zeros), as the formula does.
  * Requirements: M >= 0 (0 is a no-op), C >= 1, leading dimensions >= C, eps >= 0,
  * else IGC_ERR_INVALID_VALUE; the alignment rule (q: ldq a multiple of 16), any C;

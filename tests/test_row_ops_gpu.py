@@ -7,7 +7,7 @@ import torch
 import implicit_gemm_conv_amd as igc
 from fused_util import DT, U32
 from gpu_util import synchronize
-from test_int8_ops_gpu import NORM8, Norm, check_int8, up16
+from test_int8_ops_gpu import EPS, NORM8, Norm, check_int8, up16
 
 pytestmark = pytest.mark.gpu
 
@@ -49,3 +49,34 @@ def test_gamma_of_every_type_and_address(C, odd, gamma):
         dgamma, dx = place(torch.zeros(C, dtype=DT[gamma]), odd), n.out()
         n.backward(dx, dgamma, dh)
         n.check_backward(dx, dgamma, dh, what)
+
+
+POWERS = [0, 62, 90, 110, -40, -60, -75, -100, -115]
+
+
+@pytest.mark.parametrize("eps", [EPS, 0.0])
+@pytest.mark.parametrize("C", [60, 400, 1000, 2000, 5000, 16384, 20000, 40000])
+def test_norm_of_every_magnitude(C, eps):
+    """Rows whose squares leave fp32's range though their root mean square does not, beside ordinary ones: each is normed as
+    any other, forward, to 8 bits and back."""
+    M = 3 * len(POWERS)
+    n = Norm(M, C, "bf16", residual=C % 16 == 0, seed=C)
+    scale2 = torch.tensor(POWERS * 3, dtype=torch.float32, device="cuda").exp2()[:, None]
+    n.x.copy_(n.x.float() * scale2)
+    if n.res is not None:
+        n.res.copy_(n.res.float() * scale2)
+    n.define()
+    hd = n.h.double()
+    n.rstd = 1 / torch.sqrt((hd * hd).mean(1) + eps)
+    n.y = hd * n.rstd[:, None] * n.g64
+    a, _ = n.args()
+    y, rstd = n.out(), torch.empty(M, device="cuda")
+    igc.check(igc.rms_norm_bf16(M, C, *a, None, 0, n.gamma, igc.OUT_F32, eps, y, n.ld, rstd))
+    n.check(y, None, rstd, f"eps {eps}")
+    qbuf, scale = torch.full((M + 2, up16(C) + 16), 99, dtype=torch.int8, device="cuda"), torch.empty(M, device="cuda")
+    igc.check(igc.rms_norm_int8_bf16(M, C, *a, None, 0, n.gamma, igc.OUT_F32, eps, qbuf, qbuf.stride(0), scale))
+    synchronize()
+    check_int8(qbuf[:M, :C], qbuf, scale, n.y, n.rstd_rel + 2 * U32, f"eps {eps} to 8 bits")
+    dx, dgamma = n.out(), torch.empty(C, device="cuda")
+    n.backward(dx, dgamma, dh=False, rstd=rstd)
+    n.check_backward(dx, dgamma, dh=False, what=f"eps {eps}")
