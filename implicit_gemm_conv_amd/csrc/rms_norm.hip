@@ -194,6 +194,12 @@ constexpr int kRowThreads = T < 256 ? 256 : T;
 template <int T>
 constexpr int kNormThreads = T < 128 ? 256 : T;
 
+// A row's scale in the norm, whose largest |h gamma| is `top`: without one (an infinity or a NaN, or a product past
+// fp32, though h rstd gamma might fit), NaN.
+__device__ __forceinline__ float norm_scale(float top, float rstd) {
+    return top < __builtin_inff() ? top * rstd / 127.0f : __builtin_nanf("");
+}
+
 // ---- norm ----------------------------------------------------------------------------------------------------------
 
 template <bool F16, bool INT8, int T, int V>
@@ -249,7 +255,7 @@ __global__ __launch_bounds__(kNormThreads<T>) void rms_norm_kernel(const RowArgs
     const float top = __builtin_bit_cast(float, m);
     [[maybe_unused]] const ToInt8 to(top);
     if constexpr (INT8)
-        if (t == 0) a.scale[row] = top * rstd / 127.0f;
+        if (t == 0) a.scale[row] = norm_scale(top, rstd);
 #pragma unroll
     for (int v = 0; v < V; ++v) {
         const int c = (v * T + t) * 8, left = a.C - c;
@@ -304,7 +310,7 @@ __global__ __launch_bounds__(1024) void rms_norm_long_kernel(const RowArgs a) {
     const float top = __builtin_bit_cast(float, m);
     [[maybe_unused]] const ToInt8 to(top);
     if constexpr (INT8)
-        if (threadIdx.x == 0) a.scale[row] = top * rstd / 127.0f;
+        if (threadIdx.x == 0) a.scale[row] = norm_scale(top, rstd);
     for (int c = (int)threadIdx.x * 8; c < a.C; c += 8192) {
         const int left = a.C - c;
         u32x4s_t h = load_piece(a.x, row * a.ldx + c, left);

@@ -526,7 +526,8 @@ int igc_gemm_int8_default_tune(int64_t M, int64_t N, int64_t K, igc_tune_t *out)
  *   even, so that q * scale stands for y (rstd cancels in q: it is taken of
  *   h * gamma in fp32, rounded to fp32 once before it is to an integer).  A row of zeros has scale 0 and zeros;
  *   a row with an infinity or a NaN, its own or of h * gamma, has scale NaN and
- *   zeros, and so gives NaN in the product.  Scales below 2^-126 lose bits.
+ *   zeros, and so gives NaN in the product: h * gamma has to fit fp32, and loses
+ *   bits below 2^-126, as scales do.
  * h may be x or residual, and y may be x or residual if h is not the same one
  * (same leading dimension): a row's values are read before they are written.
  * A row's mean square need not fit fp32 (bf16's squares do not from 2^64 on, or

@@ -80,3 +80,31 @@ def test_norm_of_every_magnitude(C, eps):
     dx, dgamma = n.out(), torch.empty(C, device="cuda")
     n.backward(dx, dgamma, dh=False, rstd=rstd)
     n.check_backward(dx, dgamma, dh=False, what=f"eps {eps}")
+
+
+def norm_to_8_bits(n, x, gamma):
+    """(q, scale) of rows x with n's sizes."""
+    qbuf, scale = torch.full((n.M, up16(n.C)), 99, dtype=torch.int8, device="cuda"), torch.zeros(n.M, device="cuda")
+    igc.check(NORM8[n.dtype](n.M, n.C, x, n.ld, None, 0, None, 0, gamma, igc.OUT_F32, EPS, qbuf, up16(n.C), scale))
+    synchronize()
+    assert (qbuf[:, n.C:] == 99).all()
+    return qbuf[:, :n.C], scale
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+@pytest.mark.parametrize("C", [60, 1000, 4096, 40000])
+def test_rows_to_8_bits_without_a_largest_value(C, dtype):
+    """An infinity or a NaN in gamma, or an h * gamma that passes fp32: scale NaN and zeros, so that a product of the row is
+    NaN.  A row of zeros meets 0 * infinity, but not a gamma that is merely large."""
+    n = Norm(5, C, dtype, residual=False, gamma="f32", seed=C)
+    n.x[1] = 0
+    for g in (float("inf"), float("-inf"), float("nan")):
+        gamma = n.gamma.clone()
+        gamma[C // 2] = g
+        q, scale = norm_to_8_bits(n, n.xbuf, gamma)
+        assert torch.isnan(scale).all() and (q == 0).all(), (g, scale, q.unique())
+    gamma, x = n.gamma.clone(), n.xbuf.clone()
+    gamma[C // 2], x[:, C // 2] = 1e38, 50
+    x[1] = 0
+    q, scale = norm_to_8_bits(n, x, gamma)
+    assert torch.isnan(scale[[0, 2, 3, 4]]).all() and scale[1] == 0 and (q == 0).all()
