@@ -151,9 +151,14 @@ __device__ __forceinline__ float row_rstd(const RowArgs& a, float s, float (&red
 // is to a whole number, so that a tie (one value in 5000 to 100000 in rows of 16-bit values times a 16-bit gamma) is met
 // exactly: with `inv` alone half of them went the wrong way.  Looking again at values near a tie instead is a branch that
 // is seldom taken, whose code is then fetched: 512 rows of 8192, gated, 6.6 -> 7.7 us.
+//
+// LOW: a NaN among the values may have low bits (gamma's may; a 16-bit type's are 0), which are not to be taken for one.
+template <bool LOW>
 struct ToInt8 {
     float pre, inv, rest;
+    unsigned keep;  // (LOW) the bytes of a row that has a largest magnitude
     __device__ __forceinline__ explicit ToInt8(float t) {
+        keep = t < __builtin_inff() ? 0xffffffffu : 0u;
         pre = t < 0x1p-100f ? 0x1p100f : (t > 0x1p100f ? 0x1p-100f : 1.0f);
         const float top = t * pre;
         inv = t > 0.0f ? 127.0f / top : 0.0f;
@@ -174,6 +179,7 @@ struct ToInt8 {
             const unsigned lo = __builtin_amdgcn_perm(b[4 * i + 1], b[4 * i], 0x0c0c0400u);
             const unsigned hi = __builtin_amdgcn_perm(b[4 * i + 3], b[4 * i + 2], 0x0c0c0400u);
             w[i] = __builtin_amdgcn_perm(hi, lo, 0x05040100u);
+            if constexpr (LOW) w[i] &= keep;
         }
         return w;
     }
@@ -253,7 +259,7 @@ __global__ __launch_bounds__(kNormThreads<T>) void rms_norm_kernel(const RowArgs
     if (!in) return;
     if (t == 0 && a.rstd) a.rstd[row] = rstd;
     const float top = __builtin_bit_cast(float, m);
-    [[maybe_unused]] const ToInt8 to(top);
+    [[maybe_unused]] const ToInt8<true> to(top);
     if constexpr (INT8)
         if (t == 0) a.scale[row] = norm_scale(top, rstd);
 #pragma unroll
@@ -308,7 +314,7 @@ __global__ __launch_bounds__(1024) void rms_norm_long_kernel(const RowArgs a) {
     });
     if (threadIdx.x == 0 && a.rstd) a.rstd[row] = rstd;
     const float top = __builtin_bit_cast(float, m);
-    [[maybe_unused]] const ToInt8 to(top);
+    [[maybe_unused]] const ToInt8<true> to(top);
     if constexpr (INT8)
         if (threadIdx.x == 0) a.scale[row] = norm_scale(top, rstd);
     for (int c = (int)threadIdx.x * 8; c < a.C; c += 8192) {
@@ -375,7 +381,7 @@ __global__ __launch_bounds__(kRowThreads<T>) void quantize_rows_kernel(const Row
     row_reduce<T>(s, m, red);
     if (!in) return;
     const float top = __builtin_bit_cast(float, m);
-    const ToInt8 to(top);
+    const ToInt8<false> to(top);
     if (t == 0) a.scale[row] = top / 127.0f;
 #pragma unroll
     for (int v = 0; v < V; ++v) {
@@ -406,7 +412,7 @@ __global__ __launch_bounds__(1024) void quantize_rows_long_kernel(const RowArgs 
     }
     row_reduce<1024>(s, m, red);
     const float top = __builtin_bit_cast(float, m);
-    const ToInt8 to(top);
+    const ToInt8<false> to(top);
     if (threadIdx.x == 0) a.scale[row] = top / 127.0f;
     for (int c = (int)threadIdx.x * 8; c < a.C; c += 8192) {
         float f[8];

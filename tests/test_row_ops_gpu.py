@@ -108,3 +108,15 @@ def test_rows_to_8_bits_without_a_largest_value(C, dtype):
     x[1] = 0
     q, scale = norm_to_8_bits(n, x, gamma)
     assert torch.isnan(scale[[0, 2, 3, 4]]).all() and scale[1] == 0 and (q == 0).all()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+@pytest.mark.parametrize("C", [60, 1000, 4096, 40000])
+def test_nan_of_gamma_gives_zeros_in_8_bits(C, dtype):
+    """Whatever a NaN's sign and low bits."""
+    n = Norm(5, C, dtype, residual=False, gamma="f32", seed=C)
+    gamma = n.gamma.clone()
+    gamma[C // 2:C // 2 + 5] = torch.tensor([0x7FC00000, 0x7FC00001, 0x7FFFFFFF, -1, 0x7F80007F],
+                                            dtype=torch.int32).view(torch.float32).cuda()
+    q, scale = norm_to_8_bits(n, n.xbuf, gamma)
+    assert torch.isnan(scale).all() and (q == 0).all(), q.unique()
