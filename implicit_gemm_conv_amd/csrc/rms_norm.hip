@@ -635,14 +635,14 @@ enum RowOp : int { ROW_NORM = 0, ROW_QUANTIZE = 1, ROW_BACKWARD = 2 };
 struct RowShape {
     int T, V;
     int least = 256;  // threads of a workgroup with rows of fewer are 256
-    int threads() const { return T == 0 ? 1024 : (T < least ? 256 : T); }
-    int rows() const { return T == 0 ? 1 : threads() / T; }
+    constexpr int threads() const { return T == 0 ? 1024 : (T < least ? 256 : T); }
+    constexpr int rows() const { return T == 0 ? 1 : threads() / T; }
 };
 // Measured (many rows; us): norm 8192 x 4096 (512, 1) 48 and (256, 2) 52, to 8 bits 45 and 47, rows to 8 bits 32.2 and
 // 31.0; norm 4096 x 8192 (512, 2) 54, to 8 bits 48.5, (1024, 1) 52 and 50; gradient 8192 x 4096 (512, 1) 57, (256, 2) 60,
 // 4096 x 8192 (512, 2) 59, (1024, 1) 62.  A single row is fastest with one vector a thread: norm of 8192 values (1024, 1)
 // 4.0, (512, 2) 4.3, of 4096 (512, 1) 3.6, (256, 2) 4.0.
-static RowShape row_shape(int64_t M, int64_t C, RowOp op) {
+static constexpr RowShape row_shape(int64_t M, int64_t C, RowOp op) {
     const int64_t n = (C + 7) / 8;
     if (n <= 16) return {16, 1};
     if (n <= 64) return {64, 1};
@@ -655,44 +655,59 @@ static RowShape row_shape(int64_t M, int64_t C, RowOp op) {
     return {0, 0};
 }
 
-#define IGC_ROW_SHAPES(X) \
+// The kernels of each operator: the shapes that row_shape gives it, all of them and no others.
+#define IGC_NORM_SHAPES(X) \
+    X(16, 1) X(64, 1) X(128, 1) X(256, 1) X(512, 1) X(1024, 1) X(512, 2) X(1024, 2) X(1024, 4)
+#define IGC_QUANTIZE_SHAPES(X) \
     X(16, 1) X(64, 1) X(128, 1) X(256, 1) X(512, 1) X(256, 2) X(1024, 1) X(512, 2) X(1024, 2) X(1024, 4)
-#define IGC_BACK_SHAPES(X) X(16, 1) X(64, 1) X(128, 1) X(256, 1) X(512, 1) X(512, 2) X(1024, 2)
+#define IGC_BACKWARD_SHAPES(X) X(16, 1) X(64, 1) X(128, 1) X(256, 1) X(512, 1) X(512, 2) X(1024, 2)
+#define IGC_SHAPE(TT, VV) RowShape{TT, VV},
+constexpr RowShape kNormShapes[] = {IGC_NORM_SHAPES(IGC_SHAPE)}, kQuantizeShapes[] = {IGC_QUANTIZE_SHAPES(IGC_SHAPE)},
+                   kBackwardShapes[] = {IGC_BACKWARD_SHAPES(IGC_SHAPE)};
+#undef IGC_SHAPE
+template <int N>
+constexpr bool are_those_of(const RowShape (&list)[N], RowOp op) {
+    bool given[N] = {};
+    for (int64_t n = 1; n <= 4097; ++n)
+        for (const int64_t M : {1, 511, 512}) {
+            const RowShape s = row_shape(M, 8 * n, op);
+            int at = 0;
+            while (at < N && (list[at].T != s.T || list[at].V != s.V)) ++at;
+            if (at == N && s.T != 0) return false;
+            if (at < N) given[at] = true;
+        }
+    for (const bool g : given)
+        if (!g) return false;
+    return true;
+}
+static_assert(are_those_of(kNormShapes, ROW_NORM));
+static_assert(are_those_of(kQuantizeShapes, ROW_QUANTIZE));
+static_assert(are_those_of(kBackwardShapes, ROW_BACKWARD));
+
+// The kernel of shape s, or (T == 0) that of long rows.
 template <bool F16, bool INT8>
-static void launch_norm(RowShape s, dim3 grid, hipStream_t st, const RowArgs& a) {
-#define IGC_ROW_CASE(TT, VV)                                                                                    \
-    if (s.T == TT && s.V == VV) {                                                                               \
-        hipLaunchKernelGGL((rms_norm_kernel<F16, INT8, TT, VV>), grid, dim3(s.threads()), 0, st, a);            \
-        return;                                                                                                 \
-    }
-    IGC_ROW_SHAPES(IGC_ROW_CASE)
+static auto norm_kernel(RowShape s) {
+#define IGC_ROW_CASE(TT, VV) \
+    if (s.T == TT && s.V == VV) return &rms_norm_kernel<F16, INT8, TT, VV>;
+    IGC_NORM_SHAPES(IGC_ROW_CASE)
 #undef IGC_ROW_CASE
-    hipLaunchKernelGGL((rms_norm_long_kernel<F16, INT8>), grid, dim3(1024), 0, st, a);
+    return &rms_norm_long_kernel<F16, INT8>;
 }
 template <bool F16>
-static void launch_quantize(RowShape s, dim3 grid, hipStream_t st, const RowArgs& a) {
-#define IGC_ROW_CASE(TT, VV)                                                                                    \
-    if (s.T == TT && s.V == VV) {                                                                               \
-        hipLaunchKernelGGL((quantize_rows_kernel<F16, TT, VV>), grid, dim3(s.threads()), 0, st, a);             \
-        return;                                                                                                 \
-    }
-    IGC_ROW_SHAPES(IGC_ROW_CASE)
+static auto quantize_kernel(RowShape s) {
+#define IGC_ROW_CASE(TT, VV) \
+    if (s.T == TT && s.V == VV) return &quantize_rows_kernel<F16, TT, VV>;
+    IGC_QUANTIZE_SHAPES(IGC_ROW_CASE)
 #undef IGC_ROW_CASE
-    hipLaunchKernelGGL((quantize_rows_long_kernel<F16>), grid, dim3(1024), 0, st, a);
+    return &quantize_rows_long_kernel<F16>;
 }
 template <bool F16>
-static void launch_backward(RowShape s, dim3 grid, hipStream_t st, const RowArgs& a) {
-#define IGC_ROW_CASE(TT, VV)                                                                                    \
-    if (s.T == TT && s.V == VV) {                                                                               \
-        hipLaunchKernelGGL((rms_norm_backward_kernel<F16, TT, VV>), grid, dim3(s.threads()), 0, st, a);         \
-        return;                                                                                                 \
-    }
-    IGC_BACK_SHAPES(IGC_ROW_CASE)
+static auto backward_kernel(RowShape s, int64_t C) {
+#define IGC_ROW_CASE(TT, VV) \
+    if (s.T == TT && s.V == VV) return &rms_norm_backward_kernel<F16, TT, VV>;
+    IGC_BACKWARD_SHAPES(IGC_ROW_CASE)
 #undef IGC_ROW_CASE
-    if (a.C <= 32768)
-        hipLaunchKernelGGL((rms_norm_backward_long_kernel<F16, true>), grid, dim3(1024), 0, st, a);
-    else
-        hipLaunchKernelGGL((rms_norm_backward_long_kernel<F16, false>), grid, dim3(1024), 0, st, a);
+    return C <= 32768 ? &rms_norm_backward_long_kernel<F16, true> : &rms_norm_backward_long_kernel<F16, false>;
 }
 
 // Rows of `bytes` a value: INVALID without a pointer or with rows that overlap, MISALIGNED by the 16-byte rule.
@@ -746,15 +761,9 @@ static igc_status_t norm_any(bool fp16, bool int8, int64_t M, int64_t C, const v
     a.eps = eps;
     a.param_kind = (int)pt;
     (void)hipGetLastError();
-    const dim3 grid((unsigned)blocks);
-    if (int8 && fp16)
-        launch_norm<true, true>(s, grid, stream, a);
-    else if (int8)
-        launch_norm<false, true>(s, grid, stream, a);
-    else if (fp16)
-        launch_norm<true, false>(s, grid, stream, a);
-    else
-        launch_norm<false, false>(s, grid, stream, a);
+    const auto kernel = int8 ? (fp16 ? norm_kernel<true, true>(s) : norm_kernel<false, true>(s))
+                             : (fp16 ? norm_kernel<true, false>(s) : norm_kernel<false, false>(s));
+    hipLaunchKernelGGL(kernel, dim3((unsigned)blocks), dim3(s.threads()), 0, stream, a);
     return hipGetLastError() == hipSuccess ? IGC_OK : IGC_ERR_HIP;
 }
 
@@ -784,10 +793,8 @@ static igc_status_t quantize_any(bool fp16, int64_t M, int64_t C, igc_act_t act,
     a.ldq = ldq;
     a.act = (int)act;
     (void)hipGetLastError();
-    if (fp16)
-        launch_quantize<true>(s, dim3((unsigned)blocks), stream, a);
-    else
-        launch_quantize<false>(s, dim3((unsigned)blocks), stream, a);
+    hipLaunchKernelGGL(fp16 ? quantize_kernel<true>(s) : quantize_kernel<false>(s), dim3((unsigned)blocks),
+                       dim3(s.threads()), 0, stream, a);
     return hipGetLastError() == hipSuccess ? IGC_OK : IGC_ERR_HIP;
 }
 
@@ -846,10 +853,8 @@ static igc_status_t backward_any(bool fp16, int64_t M, int64_t C, const void* h,
     a.param_kind = (int)pt;
     (void)hipGetLastError();
     if (M > 0) {
-        if (fp16)
-            launch_backward<true>(s, dim3((unsigned)groups), stream, a);
-        else
-            launch_backward<false>(s, dim3((unsigned)groups), stream, a);
+        hipLaunchKernelGGL(fp16 ? backward_kernel<true>(s, C) : backward_kernel<false>(s, C), dim3((unsigned)groups),
+                           dim3(s.threads()), 0, stream, a);
         if (hipGetLastError() != hipSuccess) return IGC_ERR_HIP;
     }
     // (one workgroup wrote dgamma itself, but of long rows)
