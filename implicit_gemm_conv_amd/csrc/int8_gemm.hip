@@ -34,6 +34,16 @@ static const Int8Instance* find_int8(const igc_tune_t& q) {
     return nullptr;
 }
 
+// A K loop over `pairs` of values in at most s parts, each a whole number of ring periods of K tiles of bk pairs.
+struct Int8Parts {
+    int count;
+    int64_t per;
+};
+static Int8Parts parts_of(int64_t pairs, int64_t s, int bk, int depth, int half) {
+    const int64_t unit = (int64_t)bk * Ring::period(Ring::units(depth, half)), per = round_up((pairs + s - 1) / s, unit);
+    return {(int)((pairs + per - 1) / per), per};
+}
+
 // |A[m][k] B[n][k]| <= 2^14: a sum of fewer than 2^17 of them stays inside 32 bits.
 constexpr int64_t kMaxK = (1ll << 17) - 1;
 
@@ -44,6 +54,10 @@ constexpr int64_t kMaxK = (1ll << 17) - 1;
 // twice through memory.  Fitted to 287 shapes, 140 of them with K a multiple of
 // 128, with every tile and up to 16 parts: the choice takes 0.5% more than the
 // best of them all (geometric mean; 13% at most), and 0.4% on 130 others (9%).
+// A split is priced as K / s, which the constants were fitted with, and told as
+// the parts that run, which whole ring periods may make fewer.  Priced by those
+// parts, 245 of 7695 sizes take another schedule, 0.3% slower (geometric mean;
+// 0.84 to 1.28).
 //
 // Two tiles are this product's own.  32 x 64 is for grids that leave CUs idle,
 // where a K tile takes what one CU needs to load it: 64 x 4096 x 4096 8.3 us (64 x
@@ -82,6 +96,10 @@ static igc_tune_t int8_tune(int64_t M, int64_t N, int64_t K) {
             }
         }
     }
+    if (t.k_splits > 1) {
+        const int count = parts_of(K / 16 * 8, t.k_splits, t.bk, t.pipe_depth, t.half_stage).count;
+        t.k_splits = count > 1 ? count : 0;
+    }
     return t;
 }
 
@@ -117,10 +135,9 @@ static Int8Plan plan_of(const igc_tune_t* tune, int64_t M, int64_t N, int64_t K)
     if (!pl.fits) return pl;
     const Instance& t = pl.inst->tile;
     if (pl.tune.k_splits > 1 && pairs > 0) {
-        // each part a whole number of ring periods
-        const int64_t unit = (int64_t)t.bk * Ring::period(Ring::units(t.d, t.half));
-        pl.per = round_up((pairs + pl.tune.k_splits - 1) / pl.tune.k_splits, unit);
-        pl.S = (int)((pairs + pl.per - 1) / pl.per);
+        const Int8Parts parts = parts_of(pairs, pl.tune.k_splits, t.bk, t.d, t.half);
+        pl.per = parts.per;
+        pl.S = parts.count;
     }
     const int64_t tiles = ((M + t.bm - 1) / t.bm) * ((N + t.bn - 1) / t.bn);
     pl.fits = tiles <= 0x7fffffff && launchable(tiles * pl.S, 64 * t.waves);
