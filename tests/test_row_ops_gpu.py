@@ -5,9 +5,9 @@ import pytest
 import torch
 
 import implicit_gemm_conv_amd as igc
-from fused_util import DT, U32
+from fused_util import DT, U32, generator, padded, round8
 from gpu_util import synchronize
-from test_int8_ops_gpu import EPS, NORM8, Norm, check_int8, up16
+from test_int8_ops_gpu import BACK, EPS, NORM8, Norm, check_int8, up16
 
 pytestmark = pytest.mark.gpu
 
@@ -120,3 +120,24 @@ def test_nan_of_gamma_gives_zeros_in_8_bits(C, dtype):
                                             dtype=torch.int32).view(torch.float32).cuda()
     q, scale = norm_to_8_bits(n, n.xbuf, gamma)
     assert torch.isnan(scale).all() and (q == 0).all(), q.unique()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+@pytest.mark.parametrize("M,C", [(1, 72), (7, 72), (17, 72), (4111, 72), (20011, 72), (33, 300), (9001, 300), (3, 700),
+                                 (4099, 700), (3001, 1500), (1601, 4000), (1031, 8000), (1029, 16000), (777, 20000),
+                                 (261, 40000), (1, 40000)])
+def test_norm_gradient_sums_every_row_once(M, C, dtype):
+    """With whole numbers and rstd 1 every sum for dgamma is exact: rows in several turns of a workgroup, the last of them
+    part of one, each count once.  NaN lies behind the last row and each row's end."""
+    g, t = generator(M + C), DT[dtype]
+    ld = round8(C) + 8
+    h, hbuf = padded(torch.randint(-3, 4, (M, C), generator=g).to(t), ld, extra_rows=16)
+    dy, dybuf = padded(torch.randint(-3, 4, (M, C), generator=g).to(t), ld, extra_rows=16)
+    rstd = torch.full((M + 16,), float("nan"), device="cuda")
+    rstd[:M] = 1
+    want = (h.double() * dy.double()).sum(0)
+    for out in (torch.float32, torch.bfloat16):
+        dx, dgamma = torch.empty(M, ld, dtype=t, device="cuda"), torch.full((C + 8,), 99, dtype=out, device="cuda")
+        igc.check(BACK[dtype](M, C, hbuf, ld, None, igc.out_code(out), rstd, dybuf, ld, None, 0, dx, ld, dgamma))
+        synchronize()
+        assert torch.equal(dgamma[:C], want.float().to(out)) and (dgamma[C:] == 99).all()
