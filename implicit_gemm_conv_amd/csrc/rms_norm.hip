@@ -120,23 +120,38 @@ __device__ __forceinline__ void row_reduce(float& s, unsigned& m, float (*red)[2
     }
 }
 
+// Sum over a row's threads as row_reduce takes it, in loops: for a path that is seldom taken, it needs few registers.
+template <int T>
+__device__ __forceinline__ float row_sum(float s, float* red) {
+    constexpr int L = T < 64 ? T : 64;
+#pragma unroll 1
+    for (int d = L >> 1; d >= 1; d >>= 1) s += __shfl_xor(s, d);
+    if constexpr (T > 64) {
+        if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = s;
+        __syncthreads();
+        s = 0.0f;
+#pragma unroll 1
+        for (int w = 0; w < T / 64; ++w) s += red[w];
+    }
+    return s;
+}
+
 // 1 / sqrt(mean + eps) of a row whose sum of squares is s.  In bf16 the squares may leave fp32's range where their root
 // does not: above it rstd comes out as 0, and below it as more than 2^45, which needs an eps near 0.  Such a row is
 // summed once more, its values times a power of two that brings them back, for which `squares(by)` gives a thread's sum
 // of (by h)^2.  The branch is one of whole waves, its code behind the kernel's end, and ordinary rows pay its test (8192 x
-// 1024 13.4 -> 13.5 us, 1 x 4096 the same).  Every thread that shares row_reduce<T>'s barriers calls this after it with
-// the same s.
+// 1024 13.3 -> 13.5 us, 1 x 4096 and 4096 x 8192 nothing).  Every thread that shares row_reduce<T>'s barriers calls this
+// after it with the same s.  Unrolled as row_reduce is, the second sum took the kernels' occupancy from 8 waves to 7 (300
+// x 6000 to 8 bits 6.5 -> 7.5 us).
 template <bool F16, int T, int W, class Squares>
-__device__ __forceinline__ float row_rstd(const RowArgs& a, float s, float (&red)[2][W][2], Squares&& squares) {
+__device__ __forceinline__ float row_rstd(const RowArgs& a, float s, float (&red)[W], Squares&& squares) {
     static_assert(T <= 64 || W == T / 64, "one row to the waves that share barriers");
     float rstd = 1.0f / __builtin_sqrtf(s / (float)a.C + a.eps);
     if constexpr (!F16) {
         const bool far = !(rstd > 0.0f && rstd < 0x1p45f);
         if (__builtin_expect(__ballot(far) != 0, 0)) {
             const float by = s > 1.0f ? 0x1p-80f : 0x1p70f;
-            float again = squares(by);
-            unsigned none = 0;
-            row_reduce<T>(again, none, red[1]);
+            const float again = row_sum<T>(squares(by), red);
             if (far) rstd = by / __builtin_sqrtf(again / (float)a.C + a.eps * by * by);
         }
     }
@@ -211,7 +226,7 @@ __device__ __forceinline__ float norm_scale(float top, float rstd) {
 template <bool F16, bool INT8, int T, int V>
 __global__ __launch_bounds__(kNormThreads<T>) void rms_norm_kernel(const RowArgs a) {
     constexpr int R = kNormThreads<T> / T;
-    __shared__ float red[2][kNormThreads<T> / 64][2];
+    __shared__ float red[kNormThreads<T> / 64][2], again[kNormThreads<T> / 64];
     const int t = (int)threadIdx.x % T;
     const int64_t row = (int64_t)blockIdx.x * R + (int)threadIdx.x / T;
     const bool in = row < a.M;
@@ -244,8 +259,8 @@ __global__ __launch_bounds__(kNormThreads<T>) void rms_norm_kernel(const RowArgs
             }
         }
     }
-    row_reduce<T>(s, m, red[0]);
-    const float rstd = row_rstd<F16, T>(a, s, red, [&](float by) __attribute__((always_inline)) {
+    row_reduce<T>(s, m, red);
+    const float rstd = row_rstd<F16, T>(a, s, again, [&](float by) __attribute__((always_inline)) {
         float sum = 0.0f;
 #pragma unroll
         for (int v = 0; v < V; ++v) {
@@ -280,7 +295,7 @@ __global__ __launch_bounds__(kNormThreads<T>) void rms_norm_kernel(const RowArgs
 // Rows that registers do not hold: one workgroup of 1024 threads, x and residual read twice.
 template <bool F16, bool INT8>
 __global__ __launch_bounds__(1024) void rms_norm_long_kernel(const RowArgs a) {
-    __shared__ float red[2][16][2];
+    __shared__ float red[16][2], again[16];
     const int64_t row = blockIdx.x;
     float s = 0.0f;
     unsigned m = 0;
@@ -299,8 +314,8 @@ __global__ __launch_bounds__(1024) void rms_norm_long_kernel(const RowArgs a) {
             }
         }
     }
-    row_reduce<1024>(s, m, red[0]);
-    const float rstd = row_rstd<F16, 1024>(a, s, red, [&](float by) __attribute__((always_inline)) {
+    row_reduce<1024>(s, m, red);
+    const float rstd = row_rstd<F16, 1024>(a, s, again, [&](float by) __attribute__((always_inline)) {
         float sum = 0.0f;
         for (int c = (int)threadIdx.x * 8; c < a.C; c += 8192) {
             u32x4s_t h = load_piece(a.x, row * a.ldx + c, a.C - c);
