@@ -287,6 +287,10 @@ FewRowsPlan few_rows_plan(int64_t M, int64_t N, int64_t K, bool b_kc) {
 //   12000 x 3001 9.3 / 9.8, 8192 x 8192* 20.3 / 18.8, 16384 x 4096 13.3 / 12.9;  32 rows, whose A each workgroup reads
 //   twice as much of: 4096 x 4096 9.0 / 8.3, * 9.4 / 11.0, 4096 x 1024 4.5 / 4.6, 1024 x 4096 8.2 / 7.3, * 8.9 / 10.6,
 //   4096 x 2048 5.8 / 5.4, * 6.7 / 7.4.
+// Up to 8 rows the rule goes by weights from memory, as a decoder's are, for which every layer but a short wide one is faster
+// here: 4 rows 16384 x 4096* 16.0 / 17.9, 28672 x 4096* 23.6 / 26.5, 65536 x 4096* 51 / 56;  8 rows 16384 x 4096* 17.1 / 17.8,
+// 28672 x 4096* 26.3 / 26.5, 65536 x 4096* 55.7 / 56.7, 8192 x 8192* 16.8 / 18.5, 16384 x 2048* 9.5 / 8.9.  From the cache 8 rows
+// are slower here from 12288 columns on: 12288 x 4096 11.9 / 10.7, 16384 x 4096 14.9 / 12.6.
 bool few_rows_int8_faster(int64_t M, int64_t N, int64_t K) {
     if (M <= 8) return true;
     return M <= 16 ? N <= 12288 && K <= 8192 : N <= 4096 && K <= 4096;

@@ -18,10 +18,13 @@
 // as many, as it keeps its sums beside them) are read twice.  All sums are fp32
 // and taken in a fixed order.
 //
-// 8192 rows of 4096 in bf16, residual read, h kept (a copy reaches 4.9 TB/s):
-//   norm 49 us, 268 MB at 5.4 TB/s; to 8 bits 47, 235 MB at 5.0; gated rows to
-//   8 bits 32, 168 MB at 5.2; gradient with dh and dgamma 58, 268 MB at 4.6.
-// One row of 4096: 3.6, 3.9, 3.6 and 5.3 us, a launch (the gradient: two) and
+// 8192 rows of 4096 in bf16, residual read, h kept, calls of one graph, launches
+// included (a copy reaches 4.9 TB/s; what the cache still holds of the call
+// before helps):
+//   norm 49 us, 268 MB at 5.5 TB/s; to 8 bits 50, 235 MB at 4.7; gated rows to
+//   8 bits 34, 168 MB at 5.0; gradient with dh and dgamma 57, 268 MB at 4.7.
+// A kernel trace has 43 us of the first and 48 + 5 of the last.
+// One row of 4096: 3.0, 3.3, 3.1 and 4.8 us, a launch (the gradient: two) and
 // one trip to memory.
 #include <hip/hip_runtime.h>
 #include <stdint.h>

@@ -44,6 +44,10 @@
  * - Alignment: every tensor base pointer must be 16-byte aligned and every
  *   leading dimension times the element size a multiple of 16 bytes (8
  *   elements for 16-bit types, 4 for fp32, 16 for 8-bit integers).  Otherwise IGC_ERR_MISALIGNED.
+ *   A matrix's rows may be read to the end of the 16-byte piece that holds their
+ *   last value, the last row's too (what lies there does not matter and is never
+ *   written).  Vectors (bias, gamma, beta, scales, rstd) have no leading dimension:
+ *   their values lie together, and nothing beside them is read.
  * - Arguments are checked before anything is launched; on any error nothing
  *   is enqueued and the output is untouched.  No exception crosses the ABI.
  * - Outputs must not alias inputs except where an operation says so (not
@@ -500,7 +504,8 @@ int64_t igc_group_norm_workspace_bytes(int N, int H, int W, int C, int G);
  * IGC_ERR_UNSUPPORTED.  The parts of a K split are int32 in the workspace, of
  * igc_gemm_int8_workspace_bytes (-1 for sizes or a tune that the call refuses).
  * igc_gemm_int8_default_tune tells the built-in choice as
- * igc_epilogue_default_tune does (bm = 0: the kernel of few rows).
+ * igc_epilogue_default_tune does (bm = 0: the kernel of few rows), k_splits the
+ * parts that run, as whole ring periods may make them fewer than a tune asks for.
  */
 igc_status_t gemm_int8(int64_t M, int64_t N, int64_t K, const int8_t *A, int64_t lda, const float *scale_a,
                        const int8_t *B, int64_t ldb, const float *scale_b, void *D, int64_t ldd, igc_out_t d_type,
@@ -559,7 +564,8 @@ igc_status_t rms_norm_int8_fp16(int64_t M, int64_t C, const void *x, int64_t ldx
  *   dgamma[c] = sum_m dy * xh     (summed in fp32, rounded once to param_type)
  * dh is the gradient that reaches h itself, past the norm (NULL: none).  dx is
  * the gradient of x and of residual alike.  dgamma NULL: not computed.  dx may be
- * dy, dh or h (same leading dimension).  M == 0 writes dgamma = 0.
+ * dy, dh or h (same leading dimension).  M == 0 writes dgamma = 0.  The mean is of
+ * dy * gamma * h, which has to fit fp32, its sum over a row too, and loses bits below 2^-126.
  * Requirements as the norm's, but that the grid is small for every M, and
  * dgamma takes C < 2^27.  Workspace when dgamma is given:
  * igc_rms_norm_backward_workspace_bytes (-1 for bad or refused sizes).
